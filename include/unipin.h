@@ -283,6 +283,99 @@ int unipin_rank_decode_attn_noalloc(const void* q_c, const void* k_c, const void
 size_t unipin_rank_decode_noalloc_scratch_bytes(void);
 
 /*
+ * Paged pools.  A slot of n_cap rows per user reserves the longest history for
+ * every user; a paged pool gives rows out by the page.  It is a unipin_kvpool
+ * whose slots are pages: S pages of n_cap rows each (any n_cap >= 1), shared,
+ * exported and handed out like slots (unipin_kvpool_share_*, unipin_slot_ring_*).
+ * Request r's cached row j is row j % n_cap of page page_table[r, j / n_cap].
+ *   page_table     device int32 [R, max_pages], page ids 0 .. S-1; entries behind a
+ *                  request's last page are not read
+ *   key_weights    fp32 [L, S, H, n_cap]: the attention weight that each cached row has
+ *                  collected, in the pool's layout (one number per row and head)
+ * A page id out of range behind a row that a call needs, or a length out of range,
+ * is UNIPIN_ERR_OUT_OF_RANGE in *dev_status.  Rows of one layer are numbered with
+ * 32 bits: S * H * n_cap must be below 2^32 (UNIPIN_ERR_UNSUPPORTED).  R, B <= 65535.
+ */
+
+/*
+ * Rows of a ragged batch into the requests' pages (a prefill's history, or the
+ * one row of a decoded token):
+ *   row first_rows[b] + j of request b = k/v[cu_seqlens[b] + j]   for j < new_lens[b]
+ * in a bfloat16 pool bit for bit, in an E4M3 pool quantized as the pool's
+ * description says.  Nothing else in the pool is touched.  Two rows of a call must
+ * not go to one place (distinct pages per request).
+ *   k, v           [T, pool->H, D] bf16, T = total_tokens
+ *   new_lens       device int32 [B], 0 <= new_lens[b] <= the segment's length and <= max_new
+ *   first_rows     device int32 [B]: the cache row of the segment's first token
+ *   max_new        host int >= every new_lens[b] (sizes the grid)
+ *   key_weights    optional (NULL): the written rows' weights are set to 0
+ * A segment with a length out of range writes nothing; a row whose page id is out
+ * of range is left out.
+ */
+int unipin_paged_pool_write(const unipin_kvpool* pool, int layer, const void* k, const void* v,
+                            const int* cu_seqlens, const int* new_lens, const int* page_table, int max_pages,
+                            const int* first_rows, int B, int max_new, int total_tokens, float* key_weights,
+                            int* dev_status, void* stream);
+
+/*
+ * One new token per request over its cached rows.  With n_r = lens[r] cached rows,
+ * the token stands at position pos = n_r when its own key and value are passed
+ * (k_self, v_self; they are not in the cache), and at pos = n_r - 1 otherwise (its
+ * row was written first).  It sees the cached rows
+ *   j < n_r  with  pos - j < window  or  j < n_sinks
+ * (window >= 1 counts the token itself; INT_MAX: no window) and its own key, if
+ * passed.  A token that sees nothing (n_r = 0 without an own key) gets zeros.
+ * With no window and an own key this is unipin_rank_decode_attn of one candidate.
+ *   q              [R, H, D] bf16; k_self, v_self [R, pool->H, D] bf16 or both NULL
+ *   out            [R, H, D], fp32 if out_fp32 else bf16
+ *   lens           device int32 [R], 0 <= n_r <= max_len; max_len (host) sizes the
+ *                  grid, max_len <= max_pages * pool->n_cap
+ *   key_weights    optional (NULL): each cached row the token sees has its weight,
+ *                  summed over the query heads of the group, added to its entry.
+ *                  Requests may share pages; then the order of the additions, and
+ *                  so the last bits of these sums, may vary.
+ *   workspace      device scratch, 16-byte aligned, of
+ *                  unipin_paged_decode_workspace_size(...) bytes: the cache's length
+ *                  is split over blocks and joined by a second kernel.  Optional
+ *                  without key_weights (with less, each request's rows go through one
+ *                  block: slower), required with them (UNIPIN_ERR_INVALID_ARG).
+ *                  Two calls that overlap in time must not share it.
+ * A bfloat16 pool, or an E4M3 pool with any scales (its codes are read in place;
+ * powers of two are faster).  Scores, softmax statistics and sums are fp32; the
+ * softmax weights are rounded to bfloat16 (float16 over an E4M3 pool with
+ * power-of-two scales) for the product with V.
+ */
+int unipin_paged_decode_attn(const void* q, const void* k_self, const void* v_self, void* out, int out_fp32,
+                             const int* page_table, int max_pages, const int* lens, int R, int H, int D, int max_len,
+                             int window, int n_sinks, float scale, const unipin_kvpool* pool, int layer,
+                             float* key_weights, void* workspace, size_t workspace_bytes, int* dev_status,
+                             void* stream);
+
+/* Bytes of workspace unipin_paged_decode_attn uses for these sizes (0: none). */
+size_t unipin_paged_decode_workspace_size(const unipin_kvpool* pool, int R, int H, int max_len, int window,
+                                          int n_sinks, int with_weights);
+
+/*
+ * Eviction: of a request's n_r > budget cached rows, per head, the first n_sinks,
+ * the last n_recent and, of the rows between, those with the largest key_weights
+ * stay (budget in all; equal weights: the lowest row; -0 counts as 0, NaN as less
+ * than every number).  The kept rows of K, V and key_weights move to rows
+ * 0 .. budget-1 in their order; the rows behind them are left as they are.
+ * Requests with n_r <= budget are left alone.  Pages must not be shared between
+ * the call's requests.
+ *   kept           device int32 [R, pool->H, budget]: the old row of each kept row,
+ *                  -1 behind the last one
+ *   new_lens       device int32 [R], not lens itself: min(n_r, budget).  lens stays as it is,
+ *                  so that every layer can be evicted before the lengths are swapped.
+ *   max_len        host int >= every lens[r]
+ * A request whose length or a page id is out of range keeps its rows and gets
+ * kept = -1 and new_lens = -1.
+ */
+int unipin_paged_evict(const unipin_kvpool* pool, int layer, float* key_weights, const int* page_table,
+                       int max_pages, const int* lens, int R, int max_len, int budget, int n_sinks, int n_recent,
+                       int* kept, int* new_lens, int* dev_status, void* stream);
+
+/*
  * Cross-process sharing of a pool ([notes] §6 "serving: cross-process KV
  * sharing": retrieval and ranking are separate OS processes with separate
  * CUDA contexts; each retrieval replica preallocates its [L, S, H, n, D] pool

@@ -42,6 +42,10 @@ EXPORTS = (
     "unipin_selftest_exp2",
     "unipin_rank_decode_attn_noalloc",
     "unipin_rank_decode_noalloc_scratch_bytes",
+    "unipin_paged_pool_write",
+    "unipin_paged_decode_attn",
+    "unipin_paged_decode_workspace_size",
+    "unipin_paged_evict",
     "unipin_kvpool_share_export",
     "unipin_kvpool_share_open",
     "unipin_kvpool_share_close",
@@ -108,6 +112,14 @@ def _load(path: str = _LIB_PATH):
     lib.unipin_rank_decode_attn_noalloc.restype = I
     lib.unipin_rank_decode_noalloc_scratch_bytes.argtypes = []
     lib.unipin_rank_decode_noalloc_scratch_bytes.restype = SZ
+    lib.unipin_paged_pool_write.argtypes = [P, I, P, P, P, P, P, I, P, I, I, I, P, P, P]
+    lib.unipin_paged_pool_write.restype = I
+    lib.unipin_paged_decode_attn.argtypes = [P, P, P, P, I, P, I, P, I, I, I, I, I, I, F, P, I, P, P, SZ, P, P]
+    lib.unipin_paged_decode_attn.restype = I
+    lib.unipin_paged_decode_workspace_size.argtypes = [P, I, I, I, I, I, I]
+    lib.unipin_paged_decode_workspace_size.restype = SZ
+    lib.unipin_paged_evict.argtypes = [P, I, P, P, I, P, I, I, I, I, I, P, P, P, P]
+    lib.unipin_paged_evict.restype = I
     lib.unipin_kvpool_share_export.argtypes = [P, P]
     lib.unipin_kvpool_share_export.restype = I
     lib.unipin_kvpool_share_open.argtypes = [P, P]
@@ -390,6 +402,159 @@ def selftest_exp2(x: torch.Tensor, stream=None) -> torch.Tensor:
 
 def status_string(code: int) -> str:
     return LIB.unipin_status_string(int(code)).decode()
+
+
+# ------------------------------------------------------------------ paged pools
+
+NO_WINDOW = 2 ** 31 - 1    # window of an unrestricted call
+
+
+def _one_device(first: torch.Tensor, **others):
+    """The device of `first`; every other given tensor must lie on it."""
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError("%s is on %s, expected %s" % (name, t.device, first.device))
+    return first.device
+
+
+def _call(device: torch.device, stream, f, where: str, *args):
+    """f(*args, stream) with `device` current, on `stream` (default: the device's current stream)."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _call(device, stream, f, where, *args)
+    raw = torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream
+    rc = f(*args, raw)
+    if rc != UNIPIN_OK:
+        raise UnipinError(rc, where)
+
+
+def _page_table(page_table: torch.Tensor, rows: int) -> int:
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != rows \
+            or not page_table.is_contiguous() or not page_table.is_cuda:
+        raise ValueError("page_table must be a contiguous CUDA int32 tensor [%d, max_pages]" % rows)
+    return int(page_table.shape[1])
+
+
+def _key_weights(key_weights: Optional[torch.Tensor], pool_k: torch.Tensor):
+    if key_weights is not None and (key_weights.dtype != torch.float32 or key_weights.shape != pool_k.shape[:4]
+                                    or not key_weights.is_contiguous() or not key_weights.is_cuda):
+        raise ValueError("key_weights must be a contiguous CUDA float32 tensor [L, S, H, n_cap]")
+
+
+def _window(window: Optional[int], n_sinks: int):
+    window = NO_WINDOW if window is None else int(window)
+    if window < 1 or window > NO_WINDOW or n_sinks < 0 or n_sinks > NO_WINDOW:
+        raise ValueError("window must be at least 1 (None: no window) and n_sinks at least 0")
+    return window, int(n_sinks)
+
+
+def _adr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def paged_pool_write(pool_k, pool_v, layer: int, k, v, cu_seqlens, new_lens, page_table, first_rows, max_new: int,
+                     key_weights=None, dev_status=None, stream=None, pool_scales=None):
+    """The first new_lens[b] tokens of each segment into rows first_rows[b], first_rows[b] + 1, ... of
+    request b's pages (a paged pool [L, S pages, H, rows of a page, D]); their key_weights become 0."""
+    pool = _pool(pool_k, pool_v, pool_scales)
+    _tokens(k, "k", pool.D)
+    _tokens(v, "v", pool.D)
+    if k.shape != v.shape or k.shape[1] != pool.H:
+        raise ValueError("k and v must be [T, %d, %d], the pool's heads" % (pool.H, pool.D))
+    B = new_lens.shape[0]
+    _index(cu_seqlens, "cu_seqlens", B + 1)
+    _index(new_lens, "new_lens", B)
+    _index(first_rows, "first_rows", B)
+    pages = _page_table(page_table, B)
+    _key_weights(key_weights, pool_k)
+    dev = _one_device(pool_k, pool_v=pool_v, k=k, v=v, cu_seqlens=cu_seqlens, new_lens=new_lens,
+                      page_table=page_table, first_rows=first_rows, key_weights=key_weights, dev_status=dev_status)
+    _call(dev, stream, LIB.unipin_paged_pool_write, "unipin_paged_pool_write", ctypes.byref(pool), int(layer),
+          k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), new_lens.data_ptr(), page_table.data_ptr(), pages,
+          first_rows.data_ptr(), B, int(max_new), k.shape[0], _adr(key_weights), _adr(dev_status))
+
+
+def paged_decode_workspace_size(pool_k, pool_v, R: int, H: int, max_len: int, weights: bool = False,
+                                window: Optional[int] = None, n_sinks: int = 0, pool_scales=None) -> int:
+    """Workspace bytes of paged_decode_attn (0: none needed)."""
+    window, n_sinks = _window(window, n_sinks)
+    pool = _pool(pool_k, pool_v, pool_scales)
+    with torch.cuda.device(pool_k.device):
+        return int(LIB.unipin_paged_decode_workspace_size(ctypes.byref(pool), int(R), int(H), int(max_len), window,
+                                                          n_sinks, int(bool(weights))))
+
+
+def paged_decode_attn(q, page_table, lens, pool_k, pool_v, layer: int, max_len: int, k_self=None, v_self=None,
+                      window: Optional[int] = None, n_sinks: int = 0, key_weights=None, out=None,
+                      out_fp32: bool = True, scale: Optional[float] = None, workspace="auto", dev_status=None,
+                      stream=None, pool_scales=None):
+    """One new token per request ([R, H, D]) over its cached rows 0 .. lens[r]-1: the last `window` rows
+    (the token's own among them; None: all) and the first n_sinks, plus its own key and value where they
+    are passed and not yet cached.  key_weights collects each row's attention weight."""
+    _tokens(q, "q")
+    R, H, D = q.shape
+    pool = _pool(pool_k, pool_v, pool_scales)
+    if pool.D != D or H % pool.H != 0:
+        raise ValueError("q must have the pool's head dim and a multiple of its %d heads" % pool.H)
+    if (k_self is None) != (v_self is None):
+        raise ValueError("k_self and v_self go together")
+    if k_self is not None:
+        for name, t in (("k_self", k_self), ("v_self", v_self)):
+            _tokens(t, name, D)
+            if tuple(t.shape) != (R, pool.H, D):
+                raise ValueError("%s must be [%d, %d, %d]" % (name, R, pool.H, D))
+    _index(lens, "lens", R)
+    pages = _page_table(page_table, R)
+    _key_weights(key_weights, pool_k)
+    window, n_sinks = _window(window, n_sinks)
+    if out is None:
+        out = torch.empty((R, H, D), dtype=torch.float32 if out_fp32 else torch.bfloat16, device=q.device)
+    elif out.dtype != (torch.float32 if out_fp32 else torch.bfloat16) or out.shape != q.shape \
+            or not out.is_contiguous():
+        raise ValueError("out has the wrong dtype or shape")
+    if isinstance(workspace, str):
+        with torch.cuda.device(q.device):
+            nbytes = int(LIB.unipin_paged_decode_workspace_size(ctypes.byref(pool), R, H, int(max_len), window,
+                                                                n_sinks, int(key_weights is not None)))
+        workspace, ws_bytes = _workspace(workspace, nbytes, q.device)
+    else:
+        workspace, ws_bytes = _workspace(workspace, 0, q.device)
+    dev = _one_device(q, k_self=k_self, v_self=v_self, page_table=page_table, lens=lens, pool_k=pool_k,
+                      pool_v=pool_v, key_weights=key_weights, out=out, workspace=workspace, dev_status=dev_status)
+    _call(dev, stream, LIB.unipin_paged_decode_attn, "unipin_paged_decode_attn", q.data_ptr(), _adr(k_self),
+          _adr(v_self), out.data_ptr(), int(bool(out_fp32)), page_table.data_ptr(), pages, lens.data_ptr(), R, H, D,
+          int(max_len), window, n_sinks, 1.0 / math.sqrt(D) if scale is None else float(scale), ctypes.byref(pool),
+          int(layer), _adr(key_weights), _adr(workspace), ws_bytes, _adr(dev_status))
+    return out
+
+
+def paged_evict(pool_k, pool_v, key_weights, layer: int, page_table, lens, max_len: int, budget: int,
+                n_sinks: int = 0, n_recent: int = 0, kept=None, new_lens=None, dev_status=None, stream=None):
+    """Requests with more than `budget` cached rows keep, per head, the first n_sinks, the last n_recent
+    and the rows between with the largest key_weights; kept rows move to the front in their order.
+    Returns (kept [R, H, budget] int32, the old row of each kept row or -1; new_lens [R] int32)."""
+    pool = _pool(pool_k, pool_v)
+    if key_weights is None:
+        raise ValueError("key_weights is required")
+    _key_weights(key_weights, pool_k)
+    R = lens.shape[0]
+    _index(lens, "lens", R)
+    pages = _page_table(page_table, R)
+    budget = int(budget)
+    if kept is None:
+        kept = torch.empty((R, pool.H, max(budget, 0)), dtype=torch.int32, device=lens.device)
+    elif kept.dtype != torch.int32 or tuple(kept.shape) != (R, pool.H, budget) or not kept.is_contiguous():
+        raise ValueError("kept must be a contiguous int32 tensor [R, H, budget]")
+    if new_lens is None:
+        new_lens = torch.empty(R, dtype=torch.int32, device=lens.device)
+    else:
+        _index(new_lens, "new_lens", R)
+    dev = _one_device(pool_k, pool_v=pool_v, key_weights=key_weights, page_table=page_table, lens=lens, kept=kept,
+                      new_lens=new_lens, dev_status=dev_status)
+    _call(dev, stream, LIB.unipin_paged_evict, "unipin_paged_evict", ctypes.byref(pool), int(layer),
+          key_weights.data_ptr(), page_table.data_ptr(), pages, lens.data_ptr(), R, int(max_len), budget,
+          int(n_sinks), int(n_recent), kept.data_ptr(), new_lens.data_ptr(), _adr(dev_status))
+    return kept, new_lens
 
 
 # ------------------------------------------------- pool sharing and slot ring
