@@ -174,6 +174,47 @@ int unipin_masked_prefill_bwd(const void* q, const void* k, const void* v, const
 size_t unipin_masked_prefill_bwd_workspace_size(int total_tokens, int H);
 
 /*
+ * Masked prefill under a sliding window with first rows that stay visible.  A
+ * past row stands at pos = i, a candidate right after the history, at pos = n_b:
+ *   past row i < n_b       attends to past keys j <= i,
+ *   candidate row i >= n_b to past keys j < n_b and to itself,
+ *   both only to past keys with pos - j < window or j < n_sinks.
+ * (window >= 1 counts the position itself, as in unipin_paged_decode_attn, whose
+ * token with an own key is a candidate here; INT_MAX: no window.)  Key tiles that
+ * no row of a query tile sees are not read.  out, lse and every other argument
+ * and error as unipin_masked_prefill_attn (no pool: write the rows with
+ * unipin_kvpool_write or unipin_paged_pool_write).  A row with a NaN or +inf score
+ * becomes NaN (lse too); non-finite values of one segment reach no other segment,
+ * but within a segment one in a value may reach rows that the mask keeps from it.
+ * Rows behind the last segment are left as they are.
+ */
+int unipin_windowed_prefill_attn(const void* q, const void* k, const void* v, void* out, int out_fp32, float* lse,
+                                 const int* cu_seqlens, const int* past_lens, int B, int H, int H_kv, int D,
+                                 int max_seqlen, int total_tokens, int window, int n_sinks, float scale,
+                                 void* workspace, size_t workspace_bytes, int* dev_status, void* stream);
+
+/*
+ * Gradients of unipin_windowed_prefill_attn, by the formulas of
+ * unipin_masked_prefill_bwd over that mask's pairs.
+ *   dq             [T, H, D], dk and dv [T, H_kv, D]: fp32 if grad_fp32 else bf16 (sums
+ *                  are fp32, rounded once).  No atomics: the same inputs give the same
+ *                  bits.
+ *   workspace      unipin_windowed_prefill_bwd_workspace_size(total_tokens, H) bytes,
+ *                  16-byte aligned; not shared by overlapping calls
+ * B <= 65535.  Other arguments and errors as unipin_masked_prefill_bwd.  A segment
+ * whose history length is out of range gets zero gradients; rows behind the last
+ * segment are left as they are.
+ */
+int unipin_windowed_prefill_bwd(const void* q, const void* k, const void* v, const void* out, const void* dout,
+                                const float* lse, void* dq, void* dk, void* dv, int grad_fp32, const int* cu_seqlens,
+                                const int* past_lens, int B, int H, int H_kv, int D, int max_seqlen, int total_tokens,
+                                int window, int n_sinks, float scale, void* workspace, size_t workspace_bytes,
+                                int* dev_status, void* stream);
+
+/* Bytes of workspace unipin_windowed_prefill_bwd needs: 8 * total_tokens * H, rounded up to 16. */
+size_t unipin_windowed_prefill_bwd_workspace_size(int total_tokens, int H);
+
+/*
  * Pool write ([review] §2.4: retrieval writes the past K/V of every layer
  * into the shared pool; [notes] §6: pool [L, S, H, n, D], slot reuse):
  *   pool.k[layer, slot_ids[b], h, j, :] = k[cu_seqlens[b] + j, h, :]   for j < past_lens[b]

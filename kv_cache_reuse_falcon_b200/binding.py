@@ -42,6 +42,9 @@ EXPORTS = (
     "unipin_selftest_exp2",
     "unipin_rank_decode_attn_noalloc",
     "unipin_rank_decode_noalloc_scratch_bytes",
+    "unipin_windowed_prefill_attn",
+    "unipin_windowed_prefill_bwd",
+    "unipin_windowed_prefill_bwd_workspace_size",
     "unipin_paged_pool_write",
     "unipin_paged_decode_attn",
     "unipin_paged_decode_workspace_size",
@@ -112,6 +115,13 @@ def _load(path: str = _LIB_PATH):
     lib.unipin_rank_decode_attn_noalloc.restype = I
     lib.unipin_rank_decode_noalloc_scratch_bytes.argtypes = []
     lib.unipin_rank_decode_noalloc_scratch_bytes.restype = SZ
+    lib.unipin_windowed_prefill_attn.argtypes = [P, P, P, P, I, P, P, P, I, I, I, I, I, I, I, I, F, P, SZ, P, P]
+    lib.unipin_windowed_prefill_attn.restype = I
+    lib.unipin_windowed_prefill_bwd.argtypes = [P, P, P, P, P, P, P, P, P, I, P, P, I, I, I, I, I, I, I, I, F, P, SZ,
+                                                P, P]
+    lib.unipin_windowed_prefill_bwd.restype = I
+    lib.unipin_windowed_prefill_bwd_workspace_size.argtypes = [I, I]
+    lib.unipin_windowed_prefill_bwd_workspace_size.restype = SZ
     lib.unipin_paged_pool_write.argtypes = [P, I, P, P, P, P, P, I, P, I, I, I, P, P, P]
     lib.unipin_paged_pool_write.restype = I
     lib.unipin_paged_decode_attn.argtypes = [P, P, P, P, I, P, I, P, I, I, I, I, I, I, F, P, I, P, P, SZ, P, P]
@@ -404,7 +414,7 @@ def status_string(code: int) -> str:
     return LIB.unipin_status_string(int(code)).decode()
 
 
-# ------------------------------------------------------------------ paged pools
+# ------------------------------------------------- sliding window and paged pools
 
 NO_WINDOW = 2 ** 31 - 1    # window of an unrestricted call
 
@@ -450,6 +460,80 @@ def _window(window: Optional[int], n_sinks: int):
 
 def _adr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
+
+
+def windowed_prefill_attn(q, k, v, cu_seqlens, past_lens, max_seqlen: int, window: Optional[int], n_sinks: int = 0,
+                          out=None, out_fp32: bool = True, scale: Optional[float] = None, workspace="auto",
+                          dev_status=None, stream=None, lse=None):
+    """The masked prefill under a sliding window: with pos = i for a past row and pos = n_b for a
+    candidate, past keys with pos - j < window (None: all) or j < n_sinks, and a candidate's own key.
+    `lse` (fp32 [T, H]) takes the per-row log-sum-exp (base 2) that windowed_prefill_bwd needs."""
+    _tokens(q, "q")
+    T, H, D = q.shape
+    _tokens(k, "k", D)
+    _tokens(v, "v", D)
+    H_kv = _kv_heads(q, k, v)
+    B = past_lens.shape[0]
+    _index(cu_seqlens, "cu_seqlens", B + 1)
+    _index(past_lens, "past_lens", B)
+    window, n_sinks = _window(window, n_sinks)
+    if out is None:
+        out = torch.empty((T, H, D), dtype=torch.float32 if out_fp32 else torch.bfloat16, device=q.device)
+    elif out.dtype != (torch.float32 if out_fp32 else torch.bfloat16) or out.shape != q.shape or not out.is_contiguous():
+        raise ValueError("out has the wrong dtype or shape")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, H) or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous float32 tensor [T, H]")
+    ws, ws_bytes = _workspace(workspace, masked_prefill_workspace_size(), q.device)
+    dev = _one_device(q, k=k, v=v, cu_seqlens=cu_seqlens, past_lens=past_lens, out=out, lse=lse, workspace=ws,
+                      dev_status=dev_status)
+    _call(dev, stream, LIB.unipin_windowed_prefill_attn, "unipin_windowed_prefill_attn", q.data_ptr(), k.data_ptr(),
+          v.data_ptr(), out.data_ptr(), int(bool(out_fp32)), _adr(lse), cu_seqlens.data_ptr(), past_lens.data_ptr(),
+          B, H, H_kv, D, int(max_seqlen), T, window, n_sinks, 1.0 / math.sqrt(D) if scale is None else float(scale),
+          _adr(ws), ws_bytes, _adr(dev_status))
+    return out
+
+
+def windowed_prefill_bwd_workspace_size(total_tokens: int, H: int) -> int:
+    return int(LIB.unipin_windowed_prefill_bwd_workspace_size(int(total_tokens), int(H)))
+
+
+def windowed_prefill_bwd(q, k, v, out, dout, lse, cu_seqlens, past_lens, max_seqlen: int, window: Optional[int],
+                         n_sinks: int = 0, scale: Optional[float] = None, grad_fp32: bool = True, dq=None, dk=None,
+                         dv=None, workspace="auto", dev_status=None, stream=None):
+    """Gradients (dq [T, H, D], dk and dv [T, H_kv, D]; float32, or bfloat16 with grad_fp32=False) of
+    windowed_prefill_attn for the upstream gradient dout.
+
+    `out` is the forward's bf16 output and `lse` the row statistic the forward wrote."""
+    _tokens(q, "q")
+    T, H, D = q.shape
+    for name, t in (("k", k), ("v", v), ("out", out), ("dout", dout)):
+        _tokens(t, name, D)
+    H_kv = _kv_heads(q, k, v)
+    if out.shape != q.shape or dout.shape != q.shape:
+        raise ValueError("out and dout must have the shape of q")
+    if lse.dtype != torch.float32 or lse.shape != (T, H) or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous float32 tensor [T, H]")
+    B = past_lens.shape[0]
+    _index(cu_seqlens, "cu_seqlens", B + 1)
+    _index(past_lens, "past_lens", B)
+    window, n_sinks = _window(window, n_sinks)
+    kind = torch.float32 if grad_fp32 else torch.bfloat16
+    grads = []
+    for g, heads in ((dq, H), (dk, H_kv), (dv, H_kv)):
+        if g is None:
+            g = torch.empty((T, heads, D), dtype=kind, device=q.device)
+        elif g.dtype != kind or tuple(g.shape) != (T, heads, D) or not g.is_contiguous():
+            raise ValueError("gradient outputs must be contiguous %s: dq [T, H, D], dk and dv [T, H_kv, D]" % kind)
+        grads.append(g)
+    ws, ws_bytes = _workspace(workspace, windowed_prefill_bwd_workspace_size(T, H), q.device)
+    dev = _one_device(q, k=k, v=v, out=out, dout=dout, lse=lse, cu_seqlens=cu_seqlens, past_lens=past_lens,
+                      dq=grads[0], dk=grads[1], dv=grads[2], workspace=ws, dev_status=dev_status)
+    _call(dev, stream, LIB.unipin_windowed_prefill_bwd, "unipin_windowed_prefill_bwd", q.data_ptr(), k.data_ptr(),
+          v.data_ptr(), out.data_ptr(), dout.data_ptr(), lse.data_ptr(), grads[0].data_ptr(), grads[1].data_ptr(),
+          grads[2].data_ptr(), int(bool(grad_fp32)), cu_seqlens.data_ptr(), past_lens.data_ptr(), B, H, H_kv, D,
+          int(max_seqlen), T, window, n_sinks, 1.0 / math.sqrt(D) if scale is None else float(scale), _adr(ws),
+          ws_bytes, _adr(dev_status))
+    return tuple(grads)
 
 
 def paged_pool_write(pool_k, pool_v, layer: int, k, v, cu_seqlens, new_lens, page_table, first_rows, max_new: int,

@@ -75,10 +75,22 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b)
     return d;
 }
 
+// kNan: a NaN among the operands is the result (otherwise it is left out).
+template <bool kNan = false>
 __device__ __forceinline__ float max3f(float a, float b, float c)
 {
     float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    if constexpr (kNan)
+        asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    else
+        asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+__device__ __forceinline__ float fmax_nan(float a, float b)
+{
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
     return d;
 }
 

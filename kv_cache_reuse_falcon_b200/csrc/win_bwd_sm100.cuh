@@ -1,0 +1,643 @@
+// Gradients of the masked attention under a sliding window with first rows
+// that stay visible, on sm_100a.
+//
+// With P_ij = 2^(s_ij * sl2 - lse_i) (sl2 = scale * log2 e, lse_i the forward's
+// row statistic in the same units), O_i = sum_j P_ij v_j and the upstream
+// gradient dO, over the allowed pairs (i, j):
+//   Dvec_i = dO_i . O_i
+//   dS_ij  = P_ij (dO_i . v_j - Dvec_i)
+//   dV_j   = sum_i P_ij dO_i,   dK_j = scale * sum_i dS_ij q_i
+//   dQ_i   = scale * sum_j dS_ij k_j
+// Row i sees the past keys j <= i, j < n_b with min(i, n_b) - j < window or
+// j < n_sinks, and a candidate its own key.
+//
+// win_bwd_prep_kernel: Dvec of every row, and for a candidate its own key (the
+// only row that sees it): dK and dV of a candidate come from here alone, and the
+// weight of that key in dQ (dself) is left for the dQ blocks.
+// win_bwd_kernel: blocks of two kinds, the first n_kv of the grid the KV blocks.
+//   KV block: 128 past keys of (segment, key/value head).  K and V of the keys
+//     stay in shared memory; the 64-row tiles of Q and dO of the rows that see
+//     them are streamed, for each of the G query heads in turn:
+//       S^T = K Q^T, dP^T = V dO^T;  dV += P^T dO, dK += dS^T Q
+//   dQ block: 128 rows of (segment, query head).  Q and dO stay, the 64-row tiles
+//     of K and V that the rows see are streamed:
+//       S = Q K^T, dP = dO V^T;      dQ += dS K
+//   So each pair's S and dP are computed twice (7 products instead of 5), and in
+//   return no gradient is summed with atomics: under a window every key meets few
+//   rows, and adding fp32 dQ tiles into memory (written once to zero, added to
+//   once per key tile, read again to be rounded) costs more than the two products,
+//   and would leave the order of the additions open.
+// Both kinds run one pipeline: resident tiles R0, R1, streamed tiles T0, T1,
+//   S = R0 T0^T, dP = R1 T1^T (TMEM, lane = resident row, column = streamed row),
+//   P and dS from them by the softmax warps, back into TMEM as bfloat16 over the
+//   scores, acc1 += dS T0 and (KV) acc0 += P T1 with P, dS as A from TMEM.
+// Warps: 4 softmax warps per stage, then the TMA producer and the MMA issuer.  At
+// D = 128 two stages of S and dP and one block per SM: while one group of softmax
+// warps works on a tile the other's products run.  At D <= 64 one stage and two
+// blocks per SM, which also hides a block's first loads and its epilogue.
+// P and dS are rounded to bfloat16 (relative 2^-8 each) as tensor-core operands;
+// scores, P, dS and all sums are float32.
+// Segments are kept apart: streamed rows behind the segment's (or behind its
+// history) are zeroed in shared memory before they meet a zero weight, so what
+// another segment holds cannot reach a gradient through 0 * NaN.
+#pragma once
+
+#include "sm100_ptx.cuh"
+#include "tmem_wide.cuh"
+#include "unipin.h"
+
+namespace unipin {
+
+constexpr int kWbRes = 128;    // resident rows of a block = TMEM lanes
+constexpr int kWbStr = 64;     // rows of a streamed tile
+
+template <int D>
+struct WbCfg {
+    static constexpr int kBoxElems = D >= 64 ? 64 : D;
+    static constexpr int kBoxes = D / kBoxElems;
+    static constexpr int kRowBytes = kBoxElems * 2;
+    static constexpr uint32_t kLayout = D >= 64 ? kLayoutSw128 : kLayoutSw64;
+    static constexpr int kResBox = kWbRes * kRowBytes;
+    static constexpr int kResTile = kBoxes * kResBox;
+    static constexpr int kStrBox = kWbStr * kRowBytes;
+    static constexpr int kStrTile = kBoxes * kStrBox;
+    static constexpr int kSlotBytes = 2 * kStrTile;
+    static constexpr int kSlots = 4;
+    static constexpr int kStages = D == 128 ? 2 : 1;
+    static constexpr int kBlocksPerSm = D == 128 ? 1 : 2;
+    static constexpr int kSoftWarps = 4 * kStages;
+    static constexpr int kThreads = 32 * (kSoftWarps + 2);
+    static constexpr int kOffRing = 2 * kResTile;
+    static constexpr int kOffStat = kOffRing + kSlots * kSlotBytes;   // per group: 2 buffers of -lse[64], -dvec[64]
+    static constexpr int kOffBar = kOffStat + kStages * 2 * 2 * kWbStr * 4;
+    static constexpr int kSmemBytes = kOffBar + 256;
+    // TMEM columns: stage x has S at 128 x (then P, 32 columns) and dP at 128 x + 64 (then dS)
+    static constexpr int kColAcc0 = 128 * kStages;
+    static constexpr int kColAcc1 = kColAcc0 + D;
+    static constexpr int kTmemCols = D == 128 ? 512 : 256;
+    static_assert(kColAcc1 + D <= kTmemCols, "TMEM budget");
+    static_assert(kSmemBytes * kBlocksPerSm <= 226 * 1024, "shared memory budget");
+};
+
+struct WbParams {
+    const __nv_bfloat16* q;     // [T, H, D]
+    const __nv_bfloat16* k;     // [T, H_kv, D]
+    const __nv_bfloat16* v;
+    const __nv_bfloat16* o;     // forward output
+    const __nv_bfloat16* dout;
+    const float* lse;           // [T, H]
+    void* dq;                   // [T, H, D] fp32 or bf16
+    void* dk;                   // [T, H_kv, D]
+    void* dv;
+    float* dvec;                // [T, H] workspace
+    float* dself;               // [T, H] workspace: dS of a candidate's own key
+    const int* cu;
+    const int* past;
+    int B, H, Hkv, G, total_rows, max_rows;
+    int window, n_sinks;
+    int grad_fp32;
+    unsigned n_kv;
+    float scale, sl2;
+    int* status;
+    unsigned long long wait_limit_ns;
+};
+
+struct WbSegment {
+    int tok0, len, n;
+    bool rows_ok, ok;
+};
+
+__device__ __forceinline__ WbSegment wb_segment(const WbParams& p, int b)
+{
+    WbSegment s;
+    s.tok0 = p.cu[b];
+    const long long len = (long long)p.cu[b + 1] - s.tok0;
+    s.len = (int)len;
+    s.n = p.past[b];
+    s.rows_ok = s.tok0 >= 0 && len >= 0 && len <= p.max_rows && s.tok0 + len <= (long long)p.total_rows;
+    s.ok = s.rows_ok && s.n >= 0 && s.n <= s.len;
+    return s;
+}
+
+// A row of eight bfloat16 (16 bytes) as floats.
+__device__ __forceinline__ void wb_unpack8(uint4 x, float (&f)[8])
+{
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+
+// Eight gradient elements at element offset `at`.
+__device__ __forceinline__ void wb_store8(void* out, int fp32, size_t at, const float (&f)[8])
+{
+    if (fp32) {
+        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
+        dst[0] = make_float4(f[0], f[1], f[2], f[3]);
+        dst[1] = make_float4(f[4], f[5], f[6], f[7]);
+    } else {
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + at) =
+            make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                       pack_bf16x2(f[6], f[7]));
+    }
+}
+
+// A row that gave every score no weight (lse = -inf) has zero weights: 2^(s - inf).
+__device__ __forceinline__ float wb_neg_lse(float lse) { return lse == -INFINITY ? -INFINITY : -lse; }
+
+constexpr int kWbPrepThreads = 256;
+
+// Grid (blocks of (row, key/value head) pairs, B); D / 8 lanes per pair, 16 bytes of the row each.
+template <int D>
+__global__ void __launch_bounds__(kWbPrepThreads) win_bwd_prep_kernel(const WbParams p)
+{
+    constexpr int L = D / 8;
+    const int b = blockIdx.y;
+    const WbSegment s = wb_segment(p, b);
+    if (!s.ok && blockIdx.x == 0 && threadIdx.x == 0) report(p.status, (int)UNIPIN_ERR_OUT_OF_RANGE);
+    if (!s.rows_ok) return;
+    const int c = threadIdx.x % L;
+    const long long x = (long long)blockIdx.x * (kWbPrepThreads / L) + threadIdx.x / L;
+    const bool live = x < (long long)s.len * p.Hkv;      // (shuffles below: the lanes of a pair agree)
+    const int row = live ? (int)(x / p.Hkv) : 0;
+    const int hk = live ? (int)(x - (long long)row * p.Hkv) : 0;
+    const long long tok = (long long)s.tok0 + row;
+    const size_t kv_at = ((size_t)tok * p.Hkv + hk) * D + c * 8;
+    if (!s.ok) {                                         // an out-of-range history length: zero gradients
+        const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (live) {
+            wb_store8(p.dk, p.grad_fp32, kv_at, z);
+            wb_store8(p.dv, p.grad_fp32, kv_at, z);
+            for (int g = 0; g < p.G; ++g)
+                wb_store8(p.dq, p.grad_fp32, ((size_t)tok * p.H + hk * p.G + g) * D + c * 8, z);
+        }
+        return;
+    }
+    const bool cand = live && row >= s.n;
+    float kf[8], vf[8], dk[8], dv[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dk[e] = dv[e] = kf[e] = vf[e] = 0.f;
+    if (cand) {
+        wb_unpack8(__ldg(reinterpret_cast<const uint4*>(p.k + kv_at)), kf);
+        wb_unpack8(__ldg(reinterpret_cast<const uint4*>(p.v + kv_at)), vf);
+    }
+    for (int g = 0; g < p.G; ++g) {
+        const size_t qr = (size_t)tok * p.H + hk * p.G + g;
+        float of[8], gf[8], qf[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) of[e] = gf[e] = qf[e] = 0.f;
+        if (live) {
+            wb_unpack8(__ldg(reinterpret_cast<const uint4*>(p.o + qr * D + c * 8)), of);
+            wb_unpack8(__ldg(reinterpret_cast<const uint4*>(p.dout + qr * D + c * 8)), gf);
+        }
+        if (cand) wb_unpack8(__ldg(reinterpret_cast<const uint4*>(p.q + qr * D + c * 8)), qf);
+        float dvec = 0.f, qk = 0.f, gv = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            dvec = fmaf(gf[e], of[e], dvec);
+            qk = fmaf(qf[e], kf[e], qk);
+            gv = fmaf(gf[e], vf[e], gv);
+        }
+#pragma unroll
+        for (int off = L / 2; off > 0; off >>= 1) {
+            dvec += __shfl_xor_sync(0xffffffffu, dvec, off);
+            qk += __shfl_xor_sync(0xffffffffu, qk, off);
+            gv += __shfl_xor_sync(0xffffffffu, gv, off);
+        }
+        if (live && c == 0) p.dvec[qr] = dvec;
+        if (cand) {
+            const float w = ex2_approx(fmaf(qk, p.sl2, wb_neg_lse(p.lse[qr])));
+            const float ds = w * (gv - dvec);
+            if (c == 0) p.dself[qr] = ds;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                dk[e] = fmaf(p.scale * ds, qf[e], dk[e]);
+                dv[e] = fmaf(w, gf[e], dv[e]);
+            }
+        }
+    }
+    if (cand) {
+        wb_store8(p.dk, p.grad_fp32, kv_at, dk);
+        wb_store8(p.dv, p.grad_fp32, kv_at, dv);
+    }
+}
+
+// What a block works on; every warp derives the same.
+struct WbItem {
+    int b, h;            // h: key/value head (KV) or query head (dQ)
+    int r0;              // first resident row within the segment
+    int first, split, jump;   // streamed tile i (of one head) starts at row first + 64 * (i < split ? i : i + jump)
+    int cnt;             // streamed tiles of one head
+    int total;           // times G for a KV block
+    __device__ int row(int i) const { return first + kWbStr * (i < split ? i : i + jump); }
+};
+
+template <bool kKV>
+__device__ __forceinline__ bool wb_item(const WbParams& p, unsigned block, WbItem& it, WbSegment& s)
+{
+    // tile-major: the longest sweeps (a KV block's first tile sees the most rows, the sink tile all) start first
+    const int heads = kKV ? p.Hkv : p.H;
+    const unsigned bh_count = (unsigned)p.B * heads;
+    const int t = (int)(block / bh_count);
+    const unsigned bh = block - (unsigned)t * bh_count;
+    it.b = (int)(bh / heads);
+    it.h = (int)(bh - (unsigned)it.b * heads);
+    it.r0 = t * kWbRes;
+    s = wb_segment(p, it.b);
+    if (!s.ok) return false;                  // the prep kernel zeroed and reported it
+    if (kKV) {
+        if (it.r0 >= s.n) return false;
+        const bool sink = it.r0 < p.n_sinks;
+        const int last = min(it.r0 + kWbRes, s.n) - 1;               // last key
+        // past rows from the first key on, as far as the last key's window reaches (all for a sink tile)
+        const int end = sink || s.n - last <= p.window ? s.n : last + p.window;
+        const bool cand = sink || s.n - last < p.window;             // pos of a candidate is n
+        it.first = it.r0;
+        it.split = (end - it.r0 + kWbStr - 1) / kWbStr;
+        const int c0 = max((s.n - it.r0) / kWbStr, it.split);
+        const int c1 = (s.len - it.r0 + kWbStr - 1) / kWbStr;
+        it.jump = c0 - it.split;
+        it.cnt = it.split + (cand ? max(c1 - c0, 0) : 0);
+        it.total = it.cnt * p.G;
+    } else {
+        if (it.r0 >= s.len) return false;
+        const int kmax = min(min(it.r0 + kWbRes, s.len), s.n);       // keys 0 .. kmax - 1
+        const int low = max(min(it.r0, s.n) - p.window + 1, 0);      // first key of the first row's window
+        const int t0 = low / kWbStr, t1 = (kmax + kWbStr - 1) / kWbStr;
+        it.split = min((int)(((long long)min(p.n_sinks, kmax) + kWbStr - 1) / kWbStr), t0);
+        it.first = 0;
+        it.jump = t0 - it.split;
+        it.cnt = it.split + max(t1 - t0, 0);
+        it.total = it.cnt;
+    }
+    return true;
+}
+
+// One softmax pass over a streamed tile: P and dS of this thread's resident row over the 64 streamed
+// rows, from S and dP in TMEM (tS, tP + 64 columns) and back as bfloat16 pairs.  Column c is allowed
+// where c < hi and (c >= lo or c < sk).  kKV: -lse and -Dvec per column from shared memory, otherwise
+// this row's own.
+template <bool kKV>
+__device__ __forceinline__ void wb_softmax(uint32_t tS, float sl2, const float* nlse, const float* ndvec, float nl,
+                                           float nd, int lo, int hi, int sk)
+{
+    const uint64_t sc = f2_pack(sl2, sl2);
+    const uint64_t nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd);
+    const bool full = __all_sync(0xffffffffu, hi >= kWbStr && (lo <= 0 || sk >= kWbStr));
+#pragma unroll
+    for (int c0 = 0; c0 < kWbStr; c0 += 32) {
+        uint32_t sr[32], dr[32], pk[16], dk[16];
+        tmem_ld32(tS + c0, sr);
+        tmem_ld32(tS + kWbStr + c0, dr);
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+            uint64_t a[2], b[2];
+            if (kKV) {
+                const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(nlse + c0 + e);
+                const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(ndvec + c0 + e);
+                a[0] = x.x, a[1] = x.y, b[0] = y.x, b[1] = y.y;
+            } else {
+                a[0] = a[1] = nl2, b[0] = b[1] = nd2;
+            }
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+                const int i = e + 2 * f;
+                float x0, x1, d0, d1;
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), sc, a[f]), x0, x1);
+                f2_unpack(f2_add(f2_pack(__uint_as_float(dr[i]), __uint_as_float(dr[i + 1])), b[f]), d0, d1);
+                float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+                d0 *= p0;
+                d1 *= p1;
+                if (!full) {
+                    const int c = c0 + i;
+                    if (!(c < hi && (c >= lo || c < sk))) p0 = d0 = 0.f;
+                    if (!(c + 1 < hi && (c + 1 >= lo || c + 1 < sk))) p1 = d1 = 0.f;
+                }
+                pk[i / 2] = pack_bf16x2(p0, p1);
+                dk[i / 2] = pack_bf16x2(d0, d1);
+            }
+        }
+        // over columns that this thread has read already
+        if (kKV) tmem_st16(tS + c0 / 2, pk);
+        tmem_st16(tS + kWbStr + c0 / 2, dk);
+    }
+}
+
+template <int D, bool kKV>
+__device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensorMap& tm_r1, const CUtensorMap& tm_s0,
+                                        const CUtensorMap& tm_s1, const WbParams& p, unsigned block, uint8_t* smem)
+{
+    using C = WbCfg<D>;
+    const int warp = threadIdx.x / 32;
+    const int lane = threadIdx.x % 32;
+    WbItem it;
+    WbSegment s;
+    if (!wb_item<kKV>(p, block, it, s)) return;
+
+    uint8_t* sRes = smem;
+    uint8_t* ring = smem + C::kOffRing;
+    float* stat = reinterpret_cast<float*>(smem + C::kOffStat);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+    uint64_t* bar_res = bars + 0;
+    uint64_t* bar_drain = bars + 1;
+    uint64_t* acc_done = bars + 2;
+    uint64_t* s_ready = bars + 3;      // [2]
+    uint64_t* p_ready = bars + 5;      // [2]
+    uint64_t* grp = bars + 7;          // [2]
+    uint64_t* full = bars + 9;         // [kSlots]
+    uint64_t* empty = full + C::kSlots;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(empty + C::kSlots);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    if (threadIdx.x == 0) {
+        mbar_init(bar_res, 1);
+        mbar_init(bar_drain, 1);
+        mbar_init(acc_done, 1);
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(s_ready + x, 1);
+            mbar_init(p_ready + x, 4);
+            mbar_init(grp + x, 4);
+        }
+        for (int x = 0; x < C::kSlots; ++x) {
+            mbar_init(full + x, 1);
+            mbar_init(empty + x, 1);
+        }
+        *abort_flag = 0;
+        fence_mbarrier_init();
+    }
+    if (warp == C::kSoftWarps + 1) {
+        tmem_alloc(tmem_slot, C::kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    WaitCtl ctl{abort_flag, p.status, p.wait_limit_ns, (int)UNIPIN_ERR_DEVICE_TIMEOUT};
+    const bool leader = lane == 0;
+    const int total = it.total;
+
+    if (warp == C::kSoftWarps) {
+        // ------------------------------------------------------------ producer
+        if (leader && total > 0) {
+            mbar_arrive_expect_tx(bar_res, 2 * C::kResTile);
+            for (int c = 0; c < C::kBoxes; ++c) {
+                tma_load_3d(sRes + c * C::kResBox, &tm_r0, bar_res, c * C::kBoxElems, it.h, s.tok0 + it.r0);
+                tma_load_3d(sRes + C::kResTile + c * C::kResBox, &tm_r1, bar_res, c * C::kBoxElems, it.h,
+                            s.tok0 + it.r0);
+            }
+        }
+        bool ok = true;
+        int issued = 0;
+        for (int i = 0; i < total; ++i) {
+            const int st = i % C::kSlots;
+            if (i >= C::kSlots) {
+                ok = __all_sync(0xffffffffu, mbar_wait(empty + st, (i / C::kSlots - 1) & 1, ctl));
+                if (!ok) break;
+            }
+            if (leader) {
+                const int g = kKV ? i / it.cnt : 0;
+                const int head = kKV ? it.h * p.G + g : it.h / p.G;
+                const int row = s.tok0 + it.row(i - g * it.cnt);
+                uint8_t* dst = ring + st * C::kSlotBytes;
+                mbar_arrive_expect_tx(full + st, C::kSlotBytes);
+                for (int c = 0; c < C::kBoxes; ++c) {
+                    tma_load_3d(dst + c * C::kStrBox, &tm_s0, full + st, c * C::kBoxElems, head, row);
+                    tma_load_3d(dst + C::kStrTile + c * C::kStrBox, &tm_s1, full + st, c * C::kBoxElems, head, row);
+                }
+            }
+            ++issued;
+        }
+        if (leader && total > 0) {
+            // every copy lands before the block exits
+            mbar_wait_drain(bar_res, 0, p.wait_limit_ns);
+            for (int v = (issued > C::kSlots ? issued - C::kSlots : 0); v < issued; ++v)
+                mbar_wait_drain(full + v % C::kSlots, (v / C::kSlots) & 1, p.wait_limit_ns);
+        }
+    } else if (warp == C::kSoftWarps + 1) {
+        // --------------------------------------------------------- MMA issuer
+        constexpr uint32_t idesc_s = idesc_bf16_f32(kWbRes, kWbStr, false);
+        constexpr uint32_t idesc_g = idesc_bf16_f32(kWbRes, D, true);       // A from TMEM, B MN-major
+        constexpr int kStepsPerBox = C::kBoxElems / 16;
+        const uint64_t d_r0 = smem_desc(smem_u32(sRes), 16, 8 * C::kRowBytes, C::kLayout);
+        const uint64_t d_r1 = smem_desc(smem_u32(sRes) + C::kResTile, 16, 8 * C::kRowBytes, C::kLayout);
+        const uint64_t d_s0 = smem_desc(smem_u32(ring), 16, 8 * C::kRowBytes, C::kLayout);
+        const uint64_t d_s1 = smem_desc(smem_u32(ring) + C::kStrTile, 16, 8 * C::kRowBytes, C::kLayout);
+        const uint64_t d_g0 = smem_desc(smem_u32(ring), C::kStrBox, 8 * C::kRowBytes, C::kLayout);
+        const uint64_t d_g1 = smem_desc(smem_u32(ring) + C::kStrTile, C::kStrBox, 8 * C::kRowBytes, C::kLayout);
+        // S and dP of tile i into its stage; the products that read the stage's P and dS were issued
+        // before and run first
+        auto scores = [&](int i) -> bool {
+            const int st = i % C::kSlots;
+            if (!__all_sync(0xffffffffu, mbar_wait(full + st, (i / C::kSlots) & 1, ctl))) return false;
+            tc_fence_after_sync();
+            if (leader) {
+                const uint32_t tS = tmem + (i % C::kStages) * 128;
+                const uint64_t slot = (uint64_t)((st * C::kSlotBytes) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const int box = kk / kStepsPerBox, in = (kk % kStepsPerBox) * 32;
+                    umma_bf16_ss(tS, d_r0 + (uint64_t)((box * C::kResBox + in) >> 4),
+                                 d_s0 + slot + (uint64_t)((box * C::kStrBox + in) >> 4), idesc_s, kk > 0 ? 1u : 0u);
+                }
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const int box = kk / kStepsPerBox, in = (kk % kStepsPerBox) * 32;
+                    umma_bf16_ss(tS + kWbStr, d_r1 + (uint64_t)((box * C::kResBox + in) >> 4),
+                                 d_s1 + slot + (uint64_t)((box * C::kStrBox + in) >> 4), idesc_s, kk > 0 ? 1u : 0u);
+                }
+                umma_commit(s_ready + i % C::kStages);
+            }
+            return true;
+        };
+        bool ok = total == 0 || __all_sync(0xffffffffu, mbar_wait(bar_res, 0, ctl));
+        for (int i = 0; ok && i < min(C::kStages, total); ++i) ok = scores(i);
+        for (int i = 0; ok && i < total; ++i) {
+            const int x = i % C::kStages, st = i % C::kSlots;
+            ok = __all_sync(0xffffffffu, mbar_wait(p_ready + x, (i / C::kStages) & 1, ctl));
+            if (!ok) break;
+            tc_fence_after_sync();
+            if (leader) {
+                const uint64_t slot = (uint64_t)((st * C::kSlotBytes) >> 4);
+                const uint32_t tS = tmem + x * 128;
+#pragma unroll
+                for (int kk = 0; kk < kWbStr / 16; ++kk) {
+                    const uint64_t off = slot + (uint64_t)((kk * 16 * C::kRowBytes) >> 4);
+                    const uint32_t acc = (i > 0 || kk > 0) ? 1u : 0u;
+                    if (kKV) umma_bf16_ts(tmem + C::kColAcc0, tS + kk * 8, d_g1 + off, idesc_g, acc);
+                    umma_bf16_ts(tmem + C::kColAcc1, tS + kWbStr + kk * 8, d_g0 + off, idesc_g, acc);
+                }
+                umma_commit(empty + st);
+                if (i + 1 == total) umma_commit(acc_done);
+            }
+            if (i + C::kStages < total) ok = scores(i + C::kStages);
+        }
+        if (leader) {
+            umma_commit(bar_drain);
+            mbar_wait_drain(bar_drain, 0, p.wait_limit_ns);
+        }
+    } else {
+        // ------------------------------------------------- softmax + epilogue
+        const int x = warp / 4;                      // stage
+        const int t = threadIdx.x - x * 128;         // resident row
+        const uint32_t lanes = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16);
+        const int row = it.r0 + t;                   // within the segment
+        const bool live = row < (kKV ? s.n : s.len);
+        float nl = 0.f, nd = 0.f;
+        // where the row's allowed streamed rows begin and end (see wb_softmax), as segment rows
+        int lo = 0, hi = 0, sk = 0;
+        if (kKV) {
+            // rows i >= key, min(i, n) - key < window (or any, for a sink)
+            lo = row;
+            hi = !live ? 0 : (row < p.n_sinks || s.n - row < p.window ? s.len : row + p.window);
+        } else if (live) {
+            const size_t at = ((size_t)s.tok0 + row) * p.H + it.h;
+            nl = wb_neg_lse(p.lse[at]);
+            nd = -p.dvec[at];
+            lo = max(min(row, s.n) - p.window + 1, 0);
+            hi = min(row + 1, s.n);
+            sk = p.n_sinks;
+        }
+        // KV: -lse and -Dvec of a streamed tile's rows, threads 0..63 the one, 64..127 the other;
+        // fetched one tile ahead
+        auto fetch = [&](int i) -> float {
+            if (!kKV || i >= total) return 0.f;
+            const int g = i / it.cnt;
+            const int r = it.row(i - g * it.cnt) + t % 64;
+            if (r >= s.len) return 0.f;
+            const size_t at = ((size_t)s.tok0 + r) * p.H + it.h * p.G + g;
+            return t < 64 ? wb_neg_lse(p.lse[at]) : -p.dvec[at];
+        };
+        float ahead = fetch(x);
+        uint32_t ngrp = 0;
+        bool ok = true;
+        for (int i = x; i < total; i += C::kStages) {
+            const int k = i / C::kStages;
+            float* st = stat + ((x * 2 + (k & 1)) * 2) * kWbStr;
+            if (kKV) {
+                st[t] = ahead;
+                ahead = fetch(i + C::kStages);
+                if (!(ok = warp_group_sync(grp + x, ngrp, ctl, lane))) break;
+            }
+            const int row0 = it.row(kKV ? i % it.cnt : i);
+            ok = __all_sync(0xffffffffu, mbar_wait(s_ready + x, k & 1, ctl));
+            if (!ok) break;
+            tc_fence_after_sync();
+            wb_softmax<kKV>(lanes + x * 128, p.sl2, st, st + kWbStr, nl, nd, max(lo - row0, 0), max(hi - row0, 0),
+                            max(sk - row0, 0));
+            // streamed rows that are no row (KV: behind the segment) or no past key (dQ) become zeros
+            const int end = (kKV ? s.len : s.n) - row0;
+            if (end < kWbStr) {
+                if (t < kWbStr && t >= end) {
+                    uint8_t* dst = ring + (i % C::kSlots) * C::kSlotBytes + t * C::kRowBytes;
+#pragma unroll
+                    for (int c = 0; c < C::kBoxes; ++c)
+#pragma unroll
+                        for (int a = 0; a < C::kRowBytes; a += 16) {
+                            *reinterpret_cast<uint4*>(dst + c * C::kStrBox + a) = make_uint4(0u, 0u, 0u, 0u);
+                            if (kKV)
+                                *reinterpret_cast<uint4*>(dst + C::kStrTile + c * C::kStrBox + a) =
+                                    make_uint4(0u, 0u, 0u, 0u);
+                        }
+                }
+                fence_proxy_async_smem();
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_ready + x);
+        }
+        if (ok && total > 0) {
+            ok = __all_sync(0xffffffffu, mbar_wait(acc_done, 0, ctl));
+            tc_fence_after_sync();
+        }
+        if (ok) {
+            const size_t tok = (size_t)s.tok0 + row;
+            if (kKV) {
+                // group 0 stores dV, the last group dK (the TMEM loads are warp-collective)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    if (C::kStages == 2 && y != x) continue;
+                    const uint32_t col = y == 0 ? C::kColAcc0 : C::kColAcc1;
+                    const float f = y == 0 ? 1.f : p.scale;
+                    void* out = y == 0 ? p.dv : p.dk;
+#pragma unroll
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        uint32_t a[32];
+                        tmem_ld32(lanes + col + c0, a);
+                        if (!live) continue;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            float o[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) o[i] = f * __uint_as_float(a[e + i]);
+                            wb_store8(out, p.grad_fp32, (tok * p.Hkv + it.h) * D + c0 + e, o);
+                        }
+                    }
+                }
+            } else {
+                const size_t at = tok * p.H + it.h;
+                const bool cand = live && row >= s.n;
+                const float ds = cand ? p.dself[at] : 0.f;
+#pragma unroll
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    if (C::kStages == 2 && (c0 / 64) % 2 != x) continue;
+                    uint32_t a[32];
+                    if (total > 0) {
+                        tmem_ld32(lanes + C::kColAcc1 + c0, a);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) a[e] = 0u;
+                    }
+                    if (!live) continue;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        float o[8], kf[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) o[i] = __uint_as_float(a[e + i]);
+                        if (cand) {
+                            wb_unpack8(__ldg(reinterpret_cast<const uint4*>(
+                                           p.k + (tok * p.Hkv + it.h / p.G) * D + c0 + e)), kf);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) o[i] = fmaf(ds, kf[i], o[i]);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) o[i] *= p.scale;
+                        wb_store8(p.dq, p.grad_fp32, at * D + c0 + e, o);
+                    }
+                }
+            }
+        }
+    }
+
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == C::kSoftWarps + 1) {
+        __syncwarp();
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, C::kTmemCols);
+    }
+}
+
+// Maps: r = boxes of 128 rows, s = boxes of 64 rows.
+template <int D>
+__global__ void __launch_bounds__(WbCfg<D>::kThreads, WbCfg<D>::kBlocksPerSm)
+    win_bwd_kernel(const __grid_constant__ CUtensorMap tm_qr, const __grid_constant__ CUtensorMap tm_gr,
+                   const __grid_constant__ CUtensorMap tm_kr, const __grid_constant__ CUtensorMap tm_vr,
+                   const __grid_constant__ CUtensorMap tm_qs, const __grid_constant__ CUtensorMap tm_gs,
+                   const __grid_constant__ CUtensorMap tm_ks, const __grid_constant__ CUtensorMap tm_vs,
+                   const __grid_constant__ WbParams p)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (p.status && *reinterpret_cast<volatile int*>(p.status) == (int)UNIPIN_ERR_DEVICE_TIMEOUT) return;
+    if ((smem_u32(smem) & 1023u) != 0) {
+        if (threadIdx.x == 0) report(p.status, (int)UNIPIN_ERR_CUDA);
+        return;
+    }
+    if (blockIdx.x < p.n_kv)
+        wb_body<D, true>(tm_kr, tm_vr, tm_qs, tm_gs, p, blockIdx.x, smem);
+    else
+        wb_body<D, false>(tm_qr, tm_gr, tm_ks, tm_vs, p, blockIdx.x - p.n_kv, smem);
+}
+
+}  // namespace unipin
