@@ -183,15 +183,14 @@ size_t unipin_masked_prefill_bwd_workspace_size(int total_tokens, int H);
  * token with an own key is a candidate here; INT_MAX: no window.)  Key tiles that
  * no row of a query tile sees are not read.  out, lse and every other argument
  * and error as unipin_masked_prefill_attn (no pool: write the rows with
- * unipin_kvpool_write or unipin_paged_pool_write).  A row with a NaN or +inf score
- * becomes NaN (lse too); non-finite values of one segment reach no other segment,
- * but within a segment one in a value may reach rows that the mask keeps from it.
- * Rows behind the last segment are left as they are.
+ * unipin_kvpool_write or unipin_paged_pool_write; no workspace).  A row that sees a
+ * NaN or +inf score becomes NaN (lse too); NaN and infinities that a row does not
+ * see do not reach it.  Rows behind the last segment are left as they are.
  */
 int unipin_windowed_prefill_attn(const void* q, const void* k, const void* v, void* out, int out_fp32, float* lse,
                                  const int* cu_seqlens, const int* past_lens, int B, int H, int H_kv, int D,
-                                 int max_seqlen, int total_tokens, int window, int n_sinks, float scale,
-                                 void* workspace, size_t workspace_bytes, int* dev_status, void* stream);
+                                 int max_seqlen, int total_tokens, int window, int n_sinks, float scale, int* dev_status,
+                                 void* stream);
 
 /*
  * Gradients of unipin_windowed_prefill_attn, by the formulas of

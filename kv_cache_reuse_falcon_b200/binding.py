@@ -115,7 +115,7 @@ def _load(path: str = _LIB_PATH):
     lib.unipin_rank_decode_attn_noalloc.restype = I
     lib.unipin_rank_decode_noalloc_scratch_bytes.argtypes = []
     lib.unipin_rank_decode_noalloc_scratch_bytes.restype = SZ
-    lib.unipin_windowed_prefill_attn.argtypes = [P, P, P, P, I, P, P, P, I, I, I, I, I, I, I, I, F, P, SZ, P, P]
+    lib.unipin_windowed_prefill_attn.argtypes = [P, P, P, P, I, P, P, P, I, I, I, I, I, I, I, I, F, P, P]
     lib.unipin_windowed_prefill_attn.restype = I
     lib.unipin_windowed_prefill_bwd.argtypes = [P, P, P, P, P, P, P, P, P, I, P, P, I, I, I, I, I, I, I, I, F, P, SZ,
                                                 P, P]
@@ -463,8 +463,8 @@ def _adr(t: Optional[torch.Tensor]):
 
 
 def windowed_prefill_attn(q, k, v, cu_seqlens, past_lens, max_seqlen: int, window: Optional[int], n_sinks: int = 0,
-                          out=None, out_fp32: bool = True, scale: Optional[float] = None, workspace="auto",
-                          dev_status=None, stream=None, lse=None):
+                          out=None, out_fp32: bool = True, scale: Optional[float] = None, dev_status=None, stream=None,
+                          lse=None):
     """The masked prefill under a sliding window: with pos = i for a past row and pos = n_b for a
     candidate, past keys with pos - j < window (None: all) or j < n_sinks, and a candidate's own key.
     `lse` (fp32 [T, H]) takes the per-row log-sum-exp (base 2) that windowed_prefill_bwd needs."""
@@ -483,13 +483,11 @@ def windowed_prefill_attn(q, k, v, cu_seqlens, past_lens, max_seqlen: int, windo
         raise ValueError("out has the wrong dtype or shape")
     if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, H) or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 tensor [T, H]")
-    ws, ws_bytes = _workspace(workspace, masked_prefill_workspace_size(), q.device)
-    dev = _one_device(q, k=k, v=v, cu_seqlens=cu_seqlens, past_lens=past_lens, out=out, lse=lse, workspace=ws,
-                      dev_status=dev_status)
+    dev = _one_device(q, k=k, v=v, cu_seqlens=cu_seqlens, past_lens=past_lens, out=out, lse=lse, dev_status=dev_status)
     _call(dev, stream, LIB.unipin_windowed_prefill_attn, "unipin_windowed_prefill_attn", q.data_ptr(), k.data_ptr(),
           v.data_ptr(), out.data_ptr(), int(bool(out_fp32)), _adr(lse), cu_seqlens.data_ptr(), past_lens.data_ptr(),
           B, H, H_kv, D, int(max_seqlen), T, window, n_sinks, 1.0 / math.sqrt(D) if scale is None else float(scale),
-          _adr(ws), ws_bytes, _adr(dev_status))
+          _adr(dev_status))
     return out
 
 

@@ -20,17 +20,6 @@
 // Key tiles past kmax are never visited; key tiles entirely below the
 // diagonal and below kmax skip the per-element predicate.
 //
-// kWin: the prefill under a sliding window with first rows that stay visible.
-// With pos = min(i, n_b) (a candidate stands right after the history) row i sees
-// the past keys of its prefill mask that have pos - j < window or j < n_sinks, and
-// a candidate its own.  A pair's key tiles are then the sink tiles and the tiles
-// from tile A's window on; tile B leaves out those that only A's window reaches
-// (WinTiles).  Tiles that lie in every row's window, or among the sinks, skip the
-// predicate as before.  A segment's keys and values reach no other segment:
-// where a history is shorter than a key tile and the tile begins in the
-// segment before, those rows of V are zeroed in shared memory.  A visible score
-// that is NaN or +inf makes its row NaN.
-//
 // Warp roles (384 threads):
 //   warps 0-3  softmax of tile A, warps 4-7 softmax of tile B: thread r owns
 //              query row r = TMEM lane r, so the row max and row sum stay in
@@ -153,7 +142,6 @@ struct AttnParams {
     int store_pool;               // prefill: also write the past K/V into slots[seg] of the pool
     void* pool_k;                 // [L, S, H, n_cap, D] (prefill pool write)
     void* pool_v;
-    int window, n_sinks;          // kWin
 };
 
 // Key tile t of nt covering keys [0, kmax): tiles are kN wide from key 0;
@@ -247,33 +235,9 @@ struct Work {
     int kmax_a, kmax_b, kmax;   // key ranges; tile geometry follows kmax
     int nt_all, t_begin;
     int nt_a, nt_b, nt;         // key tiles swept for A, B, and loaded
-    // kWin: the loaded tiles are tiles 0 .. sink_tiles-1, then t_begin, t_begin+1, ...; entry i of that
-    // list with skip0 <= i < skip1 is not tile B's
-    int sink_tiles, skip0, skip1;
 };
 
-// Index of the i-th loaded key tile.
-template <bool kWin>
-__device__ __forceinline__ int tile_index(const Work& w, int i)
-{
-    return kWin ? (i < w.sink_tiles ? i : i - w.sink_tiles + w.t_begin) : w.t_begin + i;
-}
-
-// The entries of the loaded list that query tile x (0: A, 1: B) takes, in order.
-struct WinTiles {
-    int skip0, skip, n;
-    __device__ WinTiles(const Work& w, int x)
-    {
-        const int ntx = x == 0 ? w.nt_a : w.nt_b;
-        skip0 = w.skip0;
-        skip = x == 0 ? 0 : max(min(w.skip1, ntx) - w.skip0, 0);
-        n = ntx - skip;
-    }
-    __device__ int at(int i) const { return i < skip0 ? i : i + skip; }
-    __device__ bool has(int entry) const { return entry < n + skip && (entry < skip0 || entry >= skip0 + skip); }
-};
-
-template <bool kDecode, int kN, bool kWin = false>
+template <bool kDecode, int kN>
 __device__ __forceinline__ Work make_work(const AttnParams& p, int seg, int local)
 {
     Work w;
@@ -317,19 +281,8 @@ __device__ __forceinline__ Work make_work(const AttnParams& p, int seg, int loca
         t_end_a = min(w.t_begin + per, t_end_a);
         t_end_b = min(w.t_begin + per, t_end_b);
     }
-    w.sink_tiles = w.skip0 = w.skip1 = 0;
-    if constexpr (kWin) {
-        // first key of the window of tile A's (B's) first row, the lowest of the tile
-        const int low_a = max(min(w.qrow0, w.npast) - p.window + 1, 0);
-        const int low_b = max(min(w.qrow0 + kBlockM, w.npast) - p.window + 1, 0);
-        const int sinks = (int)(((long long)min(p.n_sinks, max(w.kmax, 0)) + kN - 1) / kN);
-        w.t_begin = low_a / kN;
-        w.sink_tiles = min(sinks, w.t_begin);
-        w.skip0 = max(sinks, w.t_begin) - w.t_begin + w.sink_tiles;
-        w.skip1 = max(low_b / kN - w.t_begin + w.sink_tiles, w.skip0);
-    }
-    w.nt_a = w.sink_tiles + max(t_end_a - w.t_begin, 0);
-    w.nt_b = w.has_b ? w.sink_tiles + max(t_end_b - w.t_begin, 0) : 0;
+    w.nt_a = max(t_end_a - w.t_begin, 0);
+    w.nt_b = w.has_b ? max(t_end_b - w.t_begin, 0) : 0;
     w.nt = w.valid ? max(w.nt_a, w.nt_b) : 0;
     if (!w.valid) w.nt_a = w.nt_b = 0;
     // The segment's last pair sees every past key (kmax = npast) and is its first item.
@@ -338,7 +291,7 @@ __device__ __forceinline__ Work make_work(const AttnParams& p, int seg, int loca
     return w;
 }
 
-template <int D, bool kDecode, bool kWin = false>
+template <int D, bool kDecode>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_pk,
@@ -464,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ++n_items;
             if (!found) break;
-            const Work w = make_work<kDecode, C::kN, kWin>(p, seg, local);
+            const Work w = make_work<kDecode, C::kN>(p, seg, local);
             if (!w.valid) {
                 if (leader) report(p.status, (int)UNIPIN_ERR_OUT_OF_RANGE);
                 continue;
@@ -487,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int pool_plane = (p.layer * p.S + w.slot) * (p.H / p.G) + hkv;
             for (int i = 0; ok && i < w.nt; ++i) {      // K_i and V_i into one slot
                 int start, lo;
-                key_tile<C::kN>(tile_index<kWin>(w, i), w.nt_all, w.kmax, start, lo);
+                key_tile<C::kN>(w.t_begin + i, w.nt_all, w.kmax, start, lo);
                 const int st = u % NS;
                 if (u >= NS) {
                     ok = __all_sync(0xffffffffu, mbar_wait(kv_empty + st, ((u / NS) - 1) & 1, ctl));
@@ -539,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int u = 0;
         bool ok = true;
         while (pop_item(ok)) {
-            const Work w = make_work<kDecode, C::kN, kWin>(p, seg, local);
+            const Work w = make_work<kDecode, C::kN>(p, seg, local);
             if (!kDecode && p.store_pool && w.valid && (local / p.H) == 0 && (w.h % p.G) == 0 && !w.store &&
                 leader)
                 report(p.status, (int)UNIPIN_ERR_OUT_OF_RANGE);   // slot id or history length beyond the pool
@@ -550,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 if (w.store) {
                     int start, lo;
-                    key_tile<C::kN>(tile_index<kWin>(w, i), w.nt_all, w.kmax, start, lo);
+                    key_tile<C::kN>(w.t_begin + i, w.nt_all, w.kmax, start, lo);
                     const uint8_t* src[2] = {ring + st * C::kSlotBytes, ring + st * C::kSlotBytes + C::kTileKV};
                     if (start >= 0) {
                         // the whole tile is rows start .. start+kN-1 of the slot (all below npast)
@@ -650,53 +603,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             return r;
         };
         while (pop_item(ok)) {
-            const Work w = make_work<kDecode, C::kN, kWin>(p, seg, local);
+            const Work w = make_work<kDecode, C::kN>(p, seg, local);
             if (w.nt == 0) continue;
             const int ntx = x == 0 ? w.nt_a : w.nt_b;
-            if constexpr (kWin) {
-                // as below over the entries that are this tile's; the others are released once they landed
-                const WinTiles tiles(w, x);
-                ok = __all_sync(0xffffffffu, mbar_wait(bar_q, nq & 1, ctl));
-                if (!ok) break;
-                if (tiles.n == 0 && leader) mbar_arrive(q_empty);
-                int k = 0;
-                for (int i = 0; ok && i < w.nt; ++i, ++u) {
-                    if (!tiles.has(i)) {
-                        if (!(ok = wait_fill(u))) break;
-                        if (leader) mbar_arrive(kv_empty + u % NS);
-                        continue;
-                    }
-                    if (k == 0) {
-                        if (!(ok = wait_fill(u)) || !(ok = wait_s_free())) break;
-                        tc_fence_after_sync();
-                        if (leader) {
-                            issue_qk(u % NS);
-                            if (tiles.n == 1) umma_commit(q_empty);
-                        }
-                        ++nsq;
-                    }
-                    if (k + 1 < tiles.n) {
-                        // at most three entries on: within the ring (NS >= 4)
-                        if (!(ok = wait_s_free())) break;
-                        if (leader) {
-                            issue_qk((u + tiles.at(k + 1) - i) % NS);
-                            if (k + 2 == tiles.n) umma_commit(q_empty);
-                        }
-                        ++nsq;
-                    }
-                    ok = __all_sync(0xffffffffu, mbar_wait(p_full + x, np & 1, ctl));
-                    if (!ok) break;
-                    ++np;
-                    tc_fence_after_sync();
-                    if (leader) {
-                        issue_pv(u % NS, k > 0);
-                        umma_commit(kv_empty + u % NS);
-                    }
-                    ++k;
-                }
-                ++nq;
-                continue;
-            }
             // Q landed: this also means both warps released the previous Q.
             ok = __all_sync(0xffffffffu, mbar_wait(bar_q, nq & 1, ctl)) && wait_fill(u);
             if (!ok) break;
@@ -771,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         bool ok = true;
         while (pop_item(ok)) {
-            const Work w = make_work<kDecode, C::kN, kWin>(p, seg, local);
+            const Work w = make_work<kDecode, C::kN>(p, seg, local);
             const int u_item = u_sm;
             u_sm += w.nt;
             if (!w.valid) {
@@ -797,8 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 continue;
             }
-            const WinTiles tiles(w, x);
-            const int ntx = kWin ? tiles.n : (x == 0 ? w.nt_a : w.nt_b);
+            const int ntx = x == 0 ? w.nt_a : w.nt_b;
             const int nrows_x = x == 0 ? w.nrows_a : w.nrows_b;
             if (nrows_x <= 0) continue;
             const int kmax_x = x == 0 ? w.kmax_a : w.kmax_b;
@@ -833,15 +741,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             float m = -INFINITY;     // reference max (log2 units) the P values and O are relative to
             float l = 0.f;           // row sum relative to m
-            // kWin: the row's window begins behind key `below` (the tile's rows: at most `below_all`)
-            const int below = kWin ? min(irow, w.npast) - p.window : -1;
-            const int below_all = kWin ? min(posx0 + kBlockM - 1, w.npast) - p.window : -1;
-            bool odd = false;        // kWin: a visible score is NaN or +inf
             for (int i = 0; i < ntx; ++i) {
                 int start, lo;
-                key_tile<C::kN>(tile_index<kWin>(w, kWin ? tiles.at(i) : i), w.nt_all, w.kmax, start, lo);
-                bool full_tile = (start == lo) && (start + kN <= kmax_x) && (start + kN - 1 <= posx0);
-                if (kWin) full_tile = full_tile && (start > below_all || start + kN <= p.n_sinks);
+                key_tile<C::kN>(w.t_begin + i, w.nt_all, w.kmax, start, lo);
+                const bool full_tile = (start == lo) && (start + kN <= kmax_x) && (start + kN - 1 <= posx0);
                 // warp-uniform: the TMEM accesses below are warp-collective
                 ok = __all_sync(0xffffffffu, mbar_wait(s_full + x, ns & 1, ctl));
                 if (!ok) break;
@@ -856,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // also needs K_{i+1}; the first warp of the group signals only once
                 // its ring slot has landed, so the MMA warp waits on s_free alone.
                 if (i + 1 < ntx && (warp % 4) == 0) {
-                    const int un = u_item + (kWin ? tiles.at(i + 1) : i + 1);
+                    const int un = u_item + i + 1;
                     ok = __all_sync(0xffffffffu, mbar_wait(kv_full + un % NS, (un / NS) & 1, ctl));
                     if (!ok) break;
                 }
@@ -870,34 +773,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < kN; ++e) {
                         const int j = start + e;
-                        bool see = j >= lo && j < kmax_x && j <= irow;
-                        if (kWin) see = see && (j > below || j < p.n_sinks);
-                        if (!see) s[e] = 0xff800000u;   // -inf
+                        if (!(j >= lo && j < kmax_x && j <= irow)) s[e] = 0xff800000u;   // -inf
                     }
-                }
-                if constexpr (kWin) {
-                    // rows of V that belong to the segment before (a history shorter than the tile)
-                    if (start < 0 && r < -start) {
-                        uint8_t* row = ring + ((u_item + tiles.at(i)) % NS) * C::kSlotBytes + C::kTileKV + r * C::kRowBytes;
-#pragma unroll
-                        for (int c = 0; c < C::kChunks; ++c)
-#pragma unroll
-                            for (int b = 0; b < C::kRowBytes; b += 16)
-                                *reinterpret_cast<uint4*>(row + c * C::kAtomKV + b) = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    if (start < 0) fence_proxy_async_smem();
                 }
                 float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
 #pragma unroll
                 for (int e = 0; e < kN; e += 8) {
-                    mx0 = max3f<kWin>(mx0, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-                    mx1 = max3f<kWin>(mx1, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
-                    mx2 = max3f<kWin>(mx2, __uint_as_float(s[e + 4]), __uint_as_float(s[e + 5]));
-                    mx3 = max3f<kWin>(mx3, __uint_as_float(s[e + 6]), __uint_as_float(s[e + 7]));
+                    mx0 = max3f(mx0, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+                    mx1 = max3f(mx1, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
+                    mx2 = max3f(mx2, __uint_as_float(s[e + 4]), __uint_as_float(s[e + 5]));
+                    mx3 = max3f(mx3, __uint_as_float(s[e + 6]), __uint_as_float(s[e + 7]));
                 }
-                const float m_tile = (kWin ? fmax_nan(fmax_nan(mx0, mx1), fmax_nan(mx2, mx3))
-                                           : fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3))) * sl2;
-                if (kWin) odd = odd || !(m_tile < INFINITY);
+                const float m_tile = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * sl2;
                 // Lazy rescale: move the reference max only when some row of the
                 // warp would otherwise see P > 2^8; then every row moves to its own max.
                 const bool need = m_tile > m + kRescaleLog2;
@@ -981,13 +868,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float m_fin = fmaxf(m, ss);
                 a = (m == -INFINITY) ? 0.f : ex2_approx(m - m_fin);
                 b = self ? ex2_approx(ss - m_fin) : 0.f;
-                if (kWin) {
-                    if (ss == -INFINITY) b = 0.f;
-                    if (odd || (self && !(ss < INFINITY))) l = __int_as_float(0x7fffffff);
-                }
                 const float denom = l * a + b;
                 inv = denom > 0.f ? 1.f / denom : 0.f;
-                if (kWin && denom != denom) inv = denom;
                 if (!kDecode && p.lse) p.lse[(size_t)tok * p.H + w.h] = m_fin + log2f(denom);
             }
 #pragma unroll

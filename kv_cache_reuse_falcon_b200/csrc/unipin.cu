@@ -17,6 +17,7 @@
 #include "attn_sm100.cuh"
 #include "bwd_sm100.cuh"
 #include "win_bwd_sm100.cuh"
+#include "win_fwd_sm100.cuh"
 #include "decode_smallk_sm100.cuh"
 #include "kvpool_sm100.cuh"
 
@@ -64,9 +65,8 @@ template <int D>
 int set_attn_attrs()
 {
     int rc = set_attn_attr(attn_fwd_kernel<D, false>, AttnCfg<D, false>::kSmemBytes);
-    if (rc == UNIPIN_OK) rc = set_attn_attr(attn_fwd_kernel<D, true>, AttnCfg<D, true>::kSmemBytes);
-    if (rc == UNIPIN_OK) rc = set_attn_attr(attn_fwd_kernel<D, false, true>, AttnCfg<D, false>::kSmemBytes);
-    return rc;
+    if (rc != UNIPIN_OK) return rc;
+    return set_attn_attr(attn_fwd_kernel<D, true>, AttnCfg<D, true>::kSmemBytes);
 }
 
 template <int D, int N, bool kE4M3>
@@ -92,17 +92,24 @@ int set_sk_attrs()
     return rc;
 }
 
-template <int D>
-int set_win_bwd_attr()
+// Shared-memory limit of a windowed kernel, and all of the SM's on-chip memory as shared memory, so that
+// as many blocks fit as are meant to.
+template <typename K>
+int set_win_attr(K kernel, int smem_bytes)
 {
-    if (cudaFuncSetAttribute(win_bwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, WbCfg<D>::kSmemBytes) !=
-        cudaSuccess)
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes) != cudaSuccess)
         return UNIPIN_ERR_CUDA;
-    // all of the SM's on-chip memory as shared memory, so that two blocks fit where they are meant to
-    if (cudaFuncSetAttribute(win_bwd_kernel<D>, cudaFuncAttributePreferredSharedMemoryCarveout,
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
                              (int)cudaSharedmemCarveoutMaxShared) != cudaSuccess)
         return UNIPIN_ERR_CUDA;
     return UNIPIN_OK;
+}
+
+template <int D>
+int set_win_attrs()
+{
+    const int rc = set_win_attr(win_fwd_kernel<D>, WfCfg<D>::kSmemBytes);
+    return rc != UNIPIN_OK ? rc : set_win_attr(win_bwd_kernel<D>, WbCfg<D>::kSmemBytes);
 }
 
 // Once per device: check it is an sm_100 part, resolve the tensor-map
@@ -144,9 +151,9 @@ int ensure_device()
          cudaFuncSetAttribute(bwd_kv_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               BwCfg<128>::kSmemBytes) != cudaSuccess))
         rc = UNIPIN_ERR_CUDA;
-    if (rc == UNIPIN_OK) rc = set_win_bwd_attr<32>();
-    if (rc == UNIPIN_OK) rc = set_win_bwd_attr<64>();
-    if (rc == UNIPIN_OK) rc = set_win_bwd_attr<128>();
+    if (rc == UNIPIN_OK) rc = set_win_attrs<32>();
+    if (rc == UNIPIN_OK) rc = set_win_attrs<64>();
+    if (rc == UNIPIN_OK) rc = set_win_attrs<128>();
     if (rc != UNIPIN_OK) return rc;
     g_device_ready[dev] = true;
     return UNIPIN_OK;
@@ -203,22 +210,20 @@ int make_pool_map(CUtensorMap* m, const void* base, const unipin_kvpool* pool, i
 }
 
 // tpk, tpv: the pool as the prefill's fused pool write stores into it (unused otherwise).
-template <bool kDecode, bool kWin = false>
+template <bool kDecode>
 int launch_attn(int D, dim3 grid, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                 const CUtensorMap& tpk, const CUtensorMap& tpv, const AttnParams& p, cudaStream_t s)
 {
     switch (D) {
     case 32:
-        attn_fwd_kernel<32, kDecode, kWin>
-            <<<grid, kThreads, AttnCfg<32, kDecode>::kSmemBytes, s>>>(tq, tk, tv, tpk, tpv, p);
+        attn_fwd_kernel<32, kDecode><<<grid, kThreads, AttnCfg<32, kDecode>::kSmemBytes, s>>>(tq, tk, tv, tpk, tpv, p);
         break;
     case 64:
-        attn_fwd_kernel<64, kDecode, kWin>
-            <<<grid, kThreads, AttnCfg<64, kDecode>::kSmemBytes, s>>>(tq, tk, tv, tpk, tpv, p);
+        attn_fwd_kernel<64, kDecode><<<grid, kThreads, AttnCfg<64, kDecode>::kSmemBytes, s>>>(tq, tk, tv, tpk, tpv, p);
         break;
     case 128:
-        attn_fwd_kernel<128, kDecode, kWin>
-            <<<grid, kThreads, AttnCfg<128, kDecode>::kSmemBytes, s>>>(tq, tk, tv, tpk, tpv, p);
+        attn_fwd_kernel<128, kDecode><<<grid, kThreads, AttnCfg<128, kDecode>::kSmemBytes, s>>>(tq, tk, tv, tpk, tpv,
+                                                                                               p);
         break;
     default:
         return UNIPIN_ERR_UNSUPPORTED;
@@ -271,6 +276,14 @@ int launch_pool_write(const unipin_kvpool* pool, int layer, const void* k, const
     p.total_tokens = total_tokens;
     p.status = status;
     kvpool_write_kernel<<<grid, 256, 0, s>>>(p);
+    return cudaGetLastError() == cudaSuccess ? UNIPIN_OK : UNIPIN_ERR_CUDA;
+}
+
+template <int D>
+int launch_win_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const WfParams& p,
+                   cudaStream_t s)
+{
+    win_fwd_kernel<D><<<p.blocks, WfCfg<D>::kThreads, WfCfg<D>::kSmemBytes, s>>>(tq, tk, tv, p);
     return cudaGetLastError() == cudaSuccess ? UNIPIN_OK : UNIPIN_ERR_CUDA;
 }
 
@@ -893,8 +906,8 @@ size_t unipin_rank_decode_noalloc_scratch_bytes(void) { return kNoAllocScratchBy
 
 int unipin_windowed_prefill_attn(const void* q, const void* k, const void* v, void* out, int out_fp32, float* lse,
                                  const int* cu_seqlens, const int* past_lens, int B, int H, int H_kv, int D,
-                                 int max_seqlen, int total_tokens, int window, int n_sinks, float scale,
-                                 void* workspace, size_t workspace_bytes, int* dev_status, void* stream)
+                                 int max_seqlen, int total_tokens, int window, int n_sinks, float scale, int* dev_status,
+                                 void* stream)
 {
     if (B < 0 || H < 1 || H_kv < 1 || H % H_kv != 0 || max_seqlen < 0 || total_tokens < 0 || window < 1 || n_sinks < 0)
         return UNIPIN_ERR_INVALID_ARG;
@@ -903,46 +916,40 @@ int unipin_windowed_prefill_attn(const void* q, const void* k, const void* v, vo
     if (B == 0 || total_tokens == 0 || max_seqlen == 0) return UNIPIN_OK;
     if (!q || !k || !v || !out || !cu_seqlens || !past_lens) return UNIPIN_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out)) return UNIPIN_ERR_MISALIGNED;
-    if (workspace && !aligned16(workspace)) return UNIPIN_ERR_MISALIGNED;
     if (lse && (reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return UNIPIN_ERR_MISALIGNED;
+    const long long blocks = ((long long)max_seqlen + kWinRes - 1) / kWinRes * B * H;
+    if (blocks >= (1ll << 31)) return UNIPIN_ERR_INVALID_ARG;
     int rc = ensure_device();
     if (rc != UNIPIN_OK) return rc;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const long long bound = (long long)B * H * ((max_seqlen + kPairRows - 1) / kPairRows);
-    const dim3 grid(persistent_blocks(bound), 1, 1);
-    // with one item per block or fewer there is nothing to hand out, and zeroing the counter costs a
-    // launch of its own
-    unsigned long long* sched = nullptr;
-    if (workspace && workspace_bytes >= kSchedBytes && bound > (long long)grid.x) {
-        sched = static_cast<unsigned long long*>(workspace);
-        if (cudaMemsetAsync(sched, 0, sizeof(unsigned long long), s) != cudaSuccess) return UNIPIN_ERR_CUDA;
-    }
     CUtensorMap tq, tk, tv;
-    if ((rc = make_token_map(&tq, q, total_tokens, H, D, kBlockM)) != UNIPIN_OK) return rc;
-    if ((rc = make_token_map(&tk, k, total_tokens, H_kv, D, key_tile_width(D, false))) != UNIPIN_OK) return rc;
-    if ((rc = make_token_map(&tv, v, total_tokens, H_kv, D, key_tile_width(D, false))) != UNIPIN_OK) return rc;
-    AttnParams p = {};
+    if ((rc = make_token_map(&tq, q, total_tokens, H, D, kWinRes)) != UNIPIN_OK) return rc;
+    if ((rc = make_token_map(&tk, k, total_tokens, H_kv, D, kWinStr)) != UNIPIN_OK) return rc;
+    if ((rc = make_token_map(&tv, v, total_tokens, H_kv, D, kWinStr)) != UNIPIN_OK) return rc;
+    WfParams p = {};
     p.q = static_cast<const __nv_bfloat16*>(q);
-    p.k_self = static_cast<const __nv_bfloat16*>(k);
-    p.v_self = static_cast<const __nv_bfloat16*>(v);
+    p.k = static_cast<const __nv_bfloat16*>(k);
+    p.v = static_cast<const __nv_bfloat16*>(v);
     p.out = out;
+    p.lse = lse;
     p.cu = cu_seqlens;
     p.past = past_lens;
-    p.nseg = B;
+    p.B = B;
     p.H = H;
+    p.Hkv = H_kv;
     p.G = H / H_kv;
-    p.max_rows = max_seqlen;
     p.total_rows = total_tokens;
+    p.max_rows = max_seqlen;
+    p.window = window;
+    p.n_sinks = n_sinks;
     p.out_fp32 = out_fp32 ? 1 : 0;
-    p.nsplit = 1;
+    p.blocks = (unsigned)blocks;
     p.sl2 = scale * kLog2e;
     p.status = dev_status;
     p.wait_limit_ns = wait_limit_ns();
-    p.sched = sched;
-    p.lse = lse;
-    p.window = window;
-    p.n_sinks = n_sinks;
-    return launch_attn<false, true>(D, grid, tq, tk, tv, tk, tv, p, s);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (D == 32) return launch_win_fwd<32>(tq, tk, tv, p, s);
+    if (D == 64) return launch_win_fwd<64>(tq, tk, tv, p, s);
+    return launch_win_fwd<128>(tq, tk, tv, p, s);
 }
 
 size_t unipin_windowed_prefill_bwd_workspace_size(int total_tokens, int H)
@@ -969,7 +976,7 @@ int unipin_windowed_prefill_bwd(const void* q, const void* k, const void* v, con
                             (const void*)workspace})
         if (!aligned16(ptr)) return UNIPIN_ERR_MISALIGNED;
     if ((reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return UNIPIN_ERR_MISALIGNED;
-    const long long tiles = ((long long)max_seqlen + kWbRes - 1) / kWbRes;
+    const long long tiles = ((long long)max_seqlen + kWinRes - 1) / kWinRes;
     const long long n_kv = tiles * B * H_kv, n_dq = tiles * B * H;
     const long long prep = ((long long)max_seqlen * H_kv * (D / 8) + kWbPrepThreads - 1) / kWbPrepThreads;
     if (B > 65535 || n_kv + n_dq >= (1ll << 31) || prep >= (1ll << 31)) return UNIPIN_ERR_INVALID_ARG;
@@ -1007,7 +1014,7 @@ int unipin_windowed_prefill_bwd(const void* q, const void* k, const void* v, con
 
     CUtensorMap m[8];    // q, dout, k, v as resident tiles, then as streamed ones
     for (int i = 0; i < 2; ++i) {
-        const int rows = i == 0 ? kWbRes : kWbStr;
+        const int rows = i == 0 ? kWinRes : kWinStr;
         if ((rc = make_token_map(&m[4 * i], q, total_tokens, H, D, rows)) != UNIPIN_OK) return rc;
         if ((rc = make_token_map(&m[4 * i + 1], dout, total_tokens, H, D, rows)) != UNIPIN_OK) return rc;
         if ((rc = make_token_map(&m[4 * i + 2], k, total_tokens, H_kv, D, rows)) != UNIPIN_OK) return rc;

@@ -31,7 +31,9 @@
 //   S = R0 T0^T, dP = R1 T1^T (TMEM, lane = resident row, column = streamed row),
 //   P and dS from them by the softmax warps, back into TMEM as bfloat16 over the
 //   scores, acc1 += dS T0 and (KV) acc0 += P T1 with P, dS as A from TMEM.
-// Warps: 4 softmax warps per stage, then the TMA producer and the MMA issuer.  At
+// Warps: 8 softmax warps per stage (two threads per resident row, 32 streamed rows
+// each: no row statistic is left to be computed, so they need not meet), then the
+// TMA producer and the MMA issuer.  At
 // D = 128 two stages of S and dP and one block per SM: while one group of softmax
 // warps works on a tile the other's products run.  At D <= 64 one stage and two
 // blocks per SM, which also hides a block's first loads and its epilogue.
@@ -45,11 +47,9 @@
 #include "sm100_ptx.cuh"
 #include "tmem_wide.cuh"
 #include "unipin.h"
+#include "win_common.cuh"
 
 namespace unipin {
-
-constexpr int kWbRes = 128;    // resident rows of a block = TMEM lanes
-constexpr int kWbStr = 64;     // rows of a streamed tile
 
 template <int D>
 struct WbCfg {
@@ -57,21 +57,22 @@ struct WbCfg {
     static constexpr int kBoxes = D / kBoxElems;
     static constexpr int kRowBytes = kBoxElems * 2;
     static constexpr uint32_t kLayout = D >= 64 ? kLayoutSw128 : kLayoutSw64;
-    static constexpr int kResBox = kWbRes * kRowBytes;
+    static constexpr int kResBox = kWinRes * kRowBytes;
     static constexpr int kResTile = kBoxes * kResBox;
-    static constexpr int kStrBox = kWbStr * kRowBytes;
+    static constexpr int kStrBox = kWinStr * kRowBytes;
     static constexpr int kStrTile = kBoxes * kStrBox;
     static constexpr int kSlotBytes = 2 * kStrTile;
     static constexpr int kSlots = 4;
     static constexpr int kStages = D == 128 ? 2 : 1;
     static constexpr int kBlocksPerSm = D == 128 ? 1 : 2;
-    static constexpr int kSoftWarps = 4 * kStages;
+    static constexpr int kSoftWarps = 8 * kStages;
     static constexpr int kThreads = 32 * (kSoftWarps + 2);
     static constexpr int kOffRing = 2 * kResTile;
     static constexpr int kOffStat = kOffRing + kSlots * kSlotBytes;   // per group: 2 buffers of -lse[64], -dvec[64]
-    static constexpr int kOffBar = kOffStat + kStages * 2 * 2 * kWbStr * 4;
+    static constexpr int kOffBar = kOffStat + kStages * 2 * 2 * kWinStr * 4;
     static constexpr int kSmemBytes = kOffBar + 256;
-    // TMEM columns: stage x has S at 128 x (then P, 32 columns) and dP at 128 x + 64 (then dS)
+    // TMEM columns: stage x has S at 128 x and dP at 128 x + 64; then P and dS of streamed rows 0..31 in
+    // the first 16 columns of each, of rows 32..63 in the 16 from column 32 on
     static constexpr int kColAcc0 = 128 * kStages;
     static constexpr int kColAcc1 = kColAcc0 + D;
     static constexpr int kTmemCols = D == 128 ? 512 : 256;
@@ -102,51 +103,6 @@ struct WbParams {
     unsigned long long wait_limit_ns;
 };
 
-struct WbSegment {
-    int tok0, len, n;
-    bool rows_ok, ok;
-};
-
-__device__ __forceinline__ WbSegment wb_segment(const WbParams& p, int b)
-{
-    WbSegment s;
-    s.tok0 = p.cu[b];
-    const long long len = (long long)p.cu[b + 1] - s.tok0;
-    s.len = (int)len;
-    s.n = p.past[b];
-    s.rows_ok = s.tok0 >= 0 && len >= 0 && len <= p.max_rows && s.tok0 + len <= (long long)p.total_rows;
-    s.ok = s.rows_ok && s.n >= 0 && s.n <= s.len;
-    return s;
-}
-
-// A row of eight bfloat16 (16 bytes) as floats.
-__device__ __forceinline__ void wb_unpack8(uint4 x, float (&f)[8])
-{
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-}
-
-// Eight gradient elements at element offset `at`.
-__device__ __forceinline__ void wb_store8(void* out, int fp32, size_t at, const float (&f)[8])
-{
-    if (fp32) {
-        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
-        dst[0] = make_float4(f[0], f[1], f[2], f[3]);
-        dst[1] = make_float4(f[4], f[5], f[6], f[7]);
-    } else {
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + at) =
-            make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                       pack_bf16x2(f[6], f[7]));
-    }
-}
-
-// A row that gave every score no weight (lse = -inf) has zero weights: 2^(s - inf).
-__device__ __forceinline__ float wb_neg_lse(float lse) { return lse == -INFINITY ? -INFINITY : -lse; }
-
 constexpr int kWbPrepThreads = 256;
 
 // Grid (blocks of (row, key/value head) pairs, B); D / 8 lanes per pair, 16 bytes of the row each.
@@ -155,7 +111,7 @@ __global__ void __launch_bounds__(kWbPrepThreads) win_bwd_prep_kernel(const WbPa
 {
     constexpr int L = D / 8;
     const int b = blockIdx.y;
-    const WbSegment s = wb_segment(p, b);
+    const WinSegment s = win_segment(p.cu, p.past, b, p.max_rows, p.total_rows);
     if (!s.ok && blockIdx.x == 0 && threadIdx.x == 0) report(p.status, (int)UNIPIN_ERR_OUT_OF_RANGE);
     if (!s.rows_ok) return;
     const int c = threadIdx.x % L;
@@ -168,10 +124,10 @@ __global__ void __launch_bounds__(kWbPrepThreads) win_bwd_prep_kernel(const WbPa
     if (!s.ok) {                                         // an out-of-range history length: zero gradients
         const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         if (live) {
-            wb_store8(p.dk, p.grad_fp32, kv_at, z);
-            wb_store8(p.dv, p.grad_fp32, kv_at, z);
+            win_store8(p.dk, p.grad_fp32, kv_at, z);
+            win_store8(p.dv, p.grad_fp32, kv_at, z);
             for (int g = 0; g < p.G; ++g)
-                wb_store8(p.dq, p.grad_fp32, ((size_t)tok * p.H + hk * p.G + g) * D + c * 8, z);
+                win_store8(p.dq, p.grad_fp32, ((size_t)tok * p.H + hk * p.G + g) * D + c * 8, z);
         }
         return;
     }
@@ -180,8 +136,8 @@ __global__ void __launch_bounds__(kWbPrepThreads) win_bwd_prep_kernel(const WbPa
 #pragma unroll
     for (int e = 0; e < 8; ++e) dk[e] = dv[e] = kf[e] = vf[e] = 0.f;
     if (cand) {
-        wb_unpack8(__ldg(reinterpret_cast<const uint4*>(p.k + kv_at)), kf);
-        wb_unpack8(__ldg(reinterpret_cast<const uint4*>(p.v + kv_at)), vf);
+        win_unpack8(__ldg(reinterpret_cast<const uint4*>(p.k + kv_at)), kf);
+        win_unpack8(__ldg(reinterpret_cast<const uint4*>(p.v + kv_at)), vf);
     }
     for (int g = 0; g < p.G; ++g) {
         const size_t qr = (size_t)tok * p.H + hk * p.G + g;
@@ -189,10 +145,10 @@ __global__ void __launch_bounds__(kWbPrepThreads) win_bwd_prep_kernel(const WbPa
 #pragma unroll
         for (int e = 0; e < 8; ++e) of[e] = gf[e] = qf[e] = 0.f;
         if (live) {
-            wb_unpack8(__ldg(reinterpret_cast<const uint4*>(p.o + qr * D + c * 8)), of);
-            wb_unpack8(__ldg(reinterpret_cast<const uint4*>(p.dout + qr * D + c * 8)), gf);
+            win_unpack8(__ldg(reinterpret_cast<const uint4*>(p.o + qr * D + c * 8)), of);
+            win_unpack8(__ldg(reinterpret_cast<const uint4*>(p.dout + qr * D + c * 8)), gf);
         }
-        if (cand) wb_unpack8(__ldg(reinterpret_cast<const uint4*>(p.q + qr * D + c * 8)), qf);
+        if (cand) win_unpack8(__ldg(reinterpret_cast<const uint4*>(p.q + qr * D + c * 8)), qf);
         float dvec = 0.f, qk = 0.f, gv = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -208,7 +164,7 @@ __global__ void __launch_bounds__(kWbPrepThreads) win_bwd_prep_kernel(const WbPa
         }
         if (live && c == 0) p.dvec[qr] = dvec;
         if (cand) {
-            const float w = ex2_approx(fmaf(qk, p.sl2, wb_neg_lse(p.lse[qr])));
+            const float w = ex2_approx(fmaf(qk, p.sl2, win_neg_lse(p.lse[qr])));
             const float ds = w * (gv - dvec);
             if (c == 0) p.dself[qr] = ds;
 #pragma unroll
@@ -219,8 +175,8 @@ __global__ void __launch_bounds__(kWbPrepThreads) win_bwd_prep_kernel(const WbPa
         }
     }
     if (cand) {
-        wb_store8(p.dk, p.grad_fp32, kv_at, dk);
-        wb_store8(p.dv, p.grad_fp32, kv_at, dv);
+        win_store8(p.dk, p.grad_fp32, kv_at, dk);
+        win_store8(p.dv, p.grad_fp32, kv_at, dv);
     }
 }
 
@@ -228,14 +184,11 @@ __global__ void __launch_bounds__(kWbPrepThreads) win_bwd_prep_kernel(const WbPa
 struct WbItem {
     int b, h;            // h: key/value head (KV) or query head (dQ)
     int r0;              // first resident row within the segment
-    int first, split, jump;   // streamed tile i (of one head) starts at row first + 64 * (i < split ? i : i + jump)
-    int cnt;             // streamed tiles of one head
-    int total;           // times G for a KV block
-    __device__ int row(int i) const { return first + kWbStr * (i < split ? i : i + jump); }
+    WinSweep sweep;      // the streamed tiles (KV: of each of the G query heads in turn)
 };
 
 template <bool kKV>
-__device__ __forceinline__ bool wb_item(const WbParams& p, unsigned block, WbItem& it, WbSegment& s)
+__device__ __forceinline__ bool wb_item(const WbParams& p, unsigned block, WbItem& it, WinSegment& s)
 {
     // tile-major: the longest sweeps (a KV block's first tile sees the most rows, the sink tile all) start first
     const int heads = kKV ? p.Hkv : p.H;
@@ -244,85 +197,55 @@ __device__ __forceinline__ bool wb_item(const WbParams& p, unsigned block, WbIte
     const unsigned bh = block - (unsigned)t * bh_count;
     it.b = (int)(bh / heads);
     it.h = (int)(bh - (unsigned)it.b * heads);
-    it.r0 = t * kWbRes;
-    s = wb_segment(p, it.b);
-    if (!s.ok) return false;                  // the prep kernel zeroed and reported it
-    if (kKV) {
-        if (it.r0 >= s.n) return false;
-        const bool sink = it.r0 < p.n_sinks;
-        const int last = min(it.r0 + kWbRes, s.n) - 1;               // last key
-        // past rows from the first key on, as far as the last key's window reaches (all for a sink tile)
-        const int end = sink || s.n - last <= p.window ? s.n : last + p.window;
-        const bool cand = sink || s.n - last < p.window;             // pos of a candidate is n
-        it.first = it.r0;
-        it.split = (end - it.r0 + kWbStr - 1) / kWbStr;
-        const int c0 = max((s.n - it.r0) / kWbStr, it.split);
-        const int c1 = (s.len - it.r0 + kWbStr - 1) / kWbStr;
-        it.jump = c0 - it.split;
-        it.cnt = it.split + (cand ? max(c1 - c0, 0) : 0);
-        it.total = it.cnt * p.G;
-    } else {
-        if (it.r0 >= s.len) return false;
-        const int kmax = min(min(it.r0 + kWbRes, s.len), s.n);       // keys 0 .. kmax - 1
-        const int low = max(min(it.r0, s.n) - p.window + 1, 0);      // first key of the first row's window
-        const int t0 = low / kWbStr, t1 = (kmax + kWbStr - 1) / kWbStr;
-        it.split = min((int)(((long long)min(p.n_sinks, kmax) + kWbStr - 1) / kWbStr), t0);
-        it.first = 0;
-        it.jump = t0 - it.split;
-        it.cnt = it.split + max(t1 - t0, 0);
-        it.total = it.cnt;
-    }
+    it.r0 = t * kWinRes;
+    s = win_segment(p.cu, p.past, it.b, p.max_rows, p.total_rows);
+    if (!s.ok || it.r0 >= (kKV ? s.n : s.len)) return false;   // the prep kernel zeroed and reported bad segments
+    it.sweep = kKV ? win_row_sweep(it.r0, s, p.window, p.n_sinks) : win_key_sweep(it.r0, s, p.window, p.n_sinks);
     return true;
 }
 
-// One softmax pass over a streamed tile: P and dS of this thread's resident row over the 64 streamed
-// rows, from S and dP in TMEM (tS, tP + 64 columns) and back as bfloat16 pairs.  Column c is allowed
-// where c < hi and (c >= lo or c < sk).  kKV: -lse and -Dvec per column from shared memory, otherwise
-// this row's own.
+// One softmax pass over half a streamed tile: P and dS of this thread's resident row over 32 of the 64
+// streamed rows, from S and dP in TMEM (32 columns at tS and at tS + 64) and back as bfloat16 pairs over
+// the first 16 of those columns.  `see`: the columns that are allowed pairs.  kKV: -lse and -Dvec per
+// column from shared memory, otherwise this row's own.
 template <bool kKV>
 __device__ __forceinline__ void wb_softmax(uint32_t tS, float sl2, const float* nlse, const float* ndvec, float nl,
-                                           float nd, int lo, int hi, int sk)
+                                           float nd, uint32_t see)
 {
     const uint64_t sc = f2_pack(sl2, sl2);
     const uint64_t nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd);
-    const bool full = __all_sync(0xffffffffu, hi >= kWbStr && (lo <= 0 || sk >= kWbStr));
+    const bool full = __all_sync(0xffffffffu, see == ~0u);
+    uint32_t sr[32], dr[32], pk[16], dk[16];
+    tmem_ld32x2(tS, sr, tS + kWinStr, dr);
 #pragma unroll
-    for (int c0 = 0; c0 < kWbStr; c0 += 32) {
-        uint32_t sr[32], dr[32], pk[16], dk[16];
-        tmem_ld32(tS + c0, sr);
-        tmem_ld32(tS + kWbStr + c0, dr);
-#pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-            uint64_t a[2], b[2];
-            if (kKV) {
-                const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(nlse + c0 + e);
-                const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(ndvec + c0 + e);
-                a[0] = x.x, a[1] = x.y, b[0] = y.x, b[1] = y.y;
-            } else {
-                a[0] = a[1] = nl2, b[0] = b[1] = nd2;
-            }
-#pragma unroll
-            for (int f = 0; f < 2; ++f) {
-                const int i = e + 2 * f;
-                float x0, x1, d0, d1;
-                f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), sc, a[f]), x0, x1);
-                f2_unpack(f2_add(f2_pack(__uint_as_float(dr[i]), __uint_as_float(dr[i + 1])), b[f]), d0, d1);
-                float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-                d0 *= p0;
-                d1 *= p1;
-                if (!full) {
-                    const int c = c0 + i;
-                    if (!(c < hi && (c >= lo || c < sk))) p0 = d0 = 0.f;
-                    if (!(c + 1 < hi && (c + 1 >= lo || c + 1 < sk))) p1 = d1 = 0.f;
-                }
-                pk[i / 2] = pack_bf16x2(p0, p1);
-                dk[i / 2] = pack_bf16x2(d0, d1);
-            }
+    for (int e = 0; e < 32; e += 4) {
+        uint64_t a[2], b[2];
+        if (kKV) {
+            const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(nlse + e);
+            const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(ndvec + e);
+            a[0] = x.x, a[1] = x.y, b[0] = y.x, b[1] = y.y;
+        } else {
+            a[0] = a[1] = nl2, b[0] = b[1] = nd2;
         }
-        // over columns that this thread has read already
-        if (kKV) tmem_st16(tS + c0 / 2, pk);
-        tmem_st16(tS + kWbStr + c0 / 2, dk);
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+            const int i = e + 2 * f;
+            float x0, x1, d0, d1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), sc, a[f]), x0, x1);
+            f2_unpack(f2_add(f2_pack(__uint_as_float(dr[i]), __uint_as_float(dr[i + 1])), b[f]), d0, d1);
+            float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+            d0 *= p0;
+            d1 *= p1;
+            if (!full) {
+                if (!(see >> i & 1u)) p0 = d0 = 0.f;
+                if (!(see >> (i + 1) & 1u)) p1 = d1 = 0.f;
+            }
+            pk[i / 2] = pack_bf16x2(p0, p1);
+            dk[i / 2] = pack_bf16x2(d0, d1);
+        }
     }
+    if (kKV) tmem_st16_nowait(tS, pk);
+    tmem_st16(tS + kWinStr, dk);
 }
 
 template <int D, bool kKV>
@@ -333,8 +256,10 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
     const int warp = threadIdx.x / 32;
     const int lane = threadIdx.x % 32;
     WbItem it;
-    WbSegment s;
+    WinSegment s;
     if (!wb_item<kKV>(p, block, it, s)) return;
+    const int cnt = it.sweep.cnt;
+    const int total = kKV ? cnt * p.G : cnt;
 
     uint8_t* sRes = smem;
     uint8_t* ring = smem + C::kOffRing;
@@ -350,21 +275,51 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
     uint64_t* empty = full + C::kSlots;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(empty + C::kSlots);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    if (threadIdx.x == 0) {
-        mbar_init(bar_res, 1);
-        mbar_init(bar_drain, 1);
-        mbar_init(acc_done, 1);
-        for (int x = 0; x < 2; ++x) {
-            mbar_init(s_ready + x, 1);
-            mbar_init(p_ready + x, 4);
-            mbar_init(grp + x, 4);
+    WaitCtl ctl{abort_flag, p.status, p.wait_limit_ns, (int)UNIPIN_ERR_DEVICE_TIMEOUT};
+    const bool leader = lane == 0;
+    // streamed tile i = tile `idx` of query head `g` of the group, into its ring slot
+    auto load_tile = [&](int i, int g, int idx) {
+        const int st = i % C::kSlots;
+        const int head = kKV ? it.h * p.G + g : it.h / p.G;
+        const int row = s.tok0 + it.sweep.row(idx);
+        uint8_t* dst = ring + st * C::kSlotBytes;
+        mbar_arrive_expect_tx(full + st, C::kSlotBytes);
+        for (int c = 0; c < C::kBoxes; ++c) {
+            tma_load_3d(dst + c * C::kStrBox, &tm_s0, full + st, c * C::kBoxElems, head, row);
+            tma_load_3d(dst + C::kStrTile + c * C::kStrBox, &tm_s1, full + st, c * C::kBoxElems, head, row);
         }
-        for (int x = 0; x < C::kSlots; ++x) {
-            mbar_init(full + x, 1);
-            mbar_init(empty + x, 1);
+    };
+    int pi = 0, pg = 0;                // producer: next tile's place
+    if (warp == C::kSoftWarps) {
+        if (leader) {
+            mbar_init(bar_res, 1);
+            mbar_init(bar_drain, 1);
+            mbar_init(acc_done, 1);
+            for (int x = 0; x < 2; ++x) {
+                mbar_init(s_ready + x, 1);
+                mbar_init(p_ready + x, 8);
+                mbar_init(grp + x, 8);
+            }
+            for (int x = 0; x < C::kSlots; ++x) {
+                mbar_init(full + x, 1);
+                mbar_init(empty + x, 1);
+            }
+            *abort_flag = 0;
+            fence_mbarrier_init();
+            // the first loads need no other warp
+            if (total > 0) {
+                mbar_arrive_expect_tx(bar_res, 2 * C::kResTile);
+                for (int c = 0; c < C::kBoxes; ++c) {
+                    tma_load_3d(sRes + c * C::kResBox, &tm_r0, bar_res, c * C::kBoxElems, it.h, s.tok0 + it.r0);
+                    tma_load_3d(sRes + C::kResTile + c * C::kResBox, &tm_r1, bar_res, c * C::kBoxElems, it.h,
+                                s.tok0 + it.r0);
+                }
+            }
         }
-        *abort_flag = 0;
-        fence_mbarrier_init();
+        for (int i = 0; i < min(total, C::kSlots); ++i) {
+            if (leader) load_tile(i, pg, pi);
+            if (++pi == cnt) pi = 0, ++pg;
+        }
     }
     if (warp == C::kSoftWarps + 1) {
         tmem_alloc(tmem_slot, C::kTmemCols);
@@ -374,40 +329,14 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    WaitCtl ctl{abort_flag, p.status, p.wait_limit_ns, (int)UNIPIN_ERR_DEVICE_TIMEOUT};
-    const bool leader = lane == 0;
-    const int total = it.total;
 
     if (warp == C::kSoftWarps) {
         // ------------------------------------------------------------ producer
-        if (leader && total > 0) {
-            mbar_arrive_expect_tx(bar_res, 2 * C::kResTile);
-            for (int c = 0; c < C::kBoxes; ++c) {
-                tma_load_3d(sRes + c * C::kResBox, &tm_r0, bar_res, c * C::kBoxElems, it.h, s.tok0 + it.r0);
-                tma_load_3d(sRes + C::kResTile + c * C::kResBox, &tm_r1, bar_res, c * C::kBoxElems, it.h,
-                            s.tok0 + it.r0);
-            }
-        }
-        bool ok = true;
-        int issued = 0;
-        for (int i = 0; i < total; ++i) {
-            const int st = i % C::kSlots;
-            if (i >= C::kSlots) {
-                ok = __all_sync(0xffffffffu, mbar_wait(empty + st, (i / C::kSlots - 1) & 1, ctl));
-                if (!ok) break;
-            }
-            if (leader) {
-                const int g = kKV ? i / it.cnt : 0;
-                const int head = kKV ? it.h * p.G + g : it.h / p.G;
-                const int row = s.tok0 + it.row(i - g * it.cnt);
-                uint8_t* dst = ring + st * C::kSlotBytes;
-                mbar_arrive_expect_tx(full + st, C::kSlotBytes);
-                for (int c = 0; c < C::kBoxes; ++c) {
-                    tma_load_3d(dst + c * C::kStrBox, &tm_s0, full + st, c * C::kBoxElems, head, row);
-                    tma_load_3d(dst + C::kStrTile + c * C::kStrBox, &tm_s1, full + st, c * C::kBoxElems, head, row);
-                }
-            }
-            ++issued;
+        int issued = min(total, C::kSlots);
+        for (; issued < total; ++issued) {
+            if (!__all_sync(0xffffffffu, mbar_wait(empty + issued % C::kSlots, (issued / C::kSlots - 1) & 1, ctl))) break;
+            if (leader) load_tile(issued, pg, pi);
+            if (++pi == cnt) pi = 0, ++pg;
         }
         if (leader && total > 0) {
             // every copy lands before the block exits
@@ -417,8 +346,8 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
         }
     } else if (warp == C::kSoftWarps + 1) {
         // --------------------------------------------------------- MMA issuer
-        constexpr uint32_t idesc_s = idesc_bf16_f32(kWbRes, kWbStr, false);
-        constexpr uint32_t idesc_g = idesc_bf16_f32(kWbRes, D, true);       // A from TMEM, B MN-major
+        constexpr uint32_t idesc_s = idesc_bf16_f32(kWinRes, kWinStr, false);
+        constexpr uint32_t idesc_g = idesc_bf16_f32(kWinRes, D, true);       // A from TMEM, B MN-major
         constexpr int kStepsPerBox = C::kBoxElems / 16;
         const uint64_t d_r0 = smem_desc(smem_u32(sRes), 16, 8 * C::kRowBytes, C::kLayout);
         const uint64_t d_r1 = smem_desc(smem_u32(sRes) + C::kResTile, 16, 8 * C::kRowBytes, C::kLayout);
@@ -444,7 +373,7 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const int box = kk / kStepsPerBox, in = (kk % kStepsPerBox) * 32;
-                    umma_bf16_ss(tS + kWbStr, d_r1 + (uint64_t)((box * C::kResBox + in) >> 4),
+                    umma_bf16_ss(tS + kWinStr, d_r1 + (uint64_t)((box * C::kResBox + in) >> 4),
                                  d_s1 + slot + (uint64_t)((box * C::kStrBox + in) >> 4), idesc_s, kk > 0 ? 1u : 0u);
                 }
                 umma_commit(s_ready + i % C::kStages);
@@ -460,13 +389,14 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
             tc_fence_after_sync();
             if (leader) {
                 const uint64_t slot = (uint64_t)((st * C::kSlotBytes) >> 4);
-                const uint32_t tS = tmem + x * 128;
 #pragma unroll
-                for (int kk = 0; kk < kWbStr / 16; ++kk) {
+                for (int kk = 0; kk < kWinStr / 16; ++kk) {
+                    // 16 streamed rows: 8 columns of pairs, those of rows 32.. at column 32
+                    const uint32_t tS = tmem + x * 128 + (kk / 2) * 32 + (kk % 2) * 8;
                     const uint64_t off = slot + (uint64_t)((kk * 16 * C::kRowBytes) >> 4);
                     const uint32_t acc = (i > 0 || kk > 0) ? 1u : 0u;
-                    if (kKV) umma_bf16_ts(tmem + C::kColAcc0, tS + kk * 8, d_g1 + off, idesc_g, acc);
-                    umma_bf16_ts(tmem + C::kColAcc1, tS + kWbStr + kk * 8, d_g0 + off, idesc_g, acc);
+                    if (kKV) umma_bf16_ts(tmem + C::kColAcc0, tS, d_g1 + off, idesc_g, acc);
+                    umma_bf16_ts(tmem + C::kColAcc1, tS + kWinStr, d_g0 + off, idesc_g, acc);
                 }
                 umma_commit(empty + st);
                 if (i + 1 == total) umma_commit(acc_done);
@@ -479,13 +409,14 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
         }
     } else {
         // ------------------------------------------------- softmax + epilogue
-        const int x = warp / 4;                      // stage
-        const int t = threadIdx.x - x * 128;         // resident row
+        const int x = warp / 8;                      // stage
+        const int half = (warp / 4) % 2;             // which 32 streamed rows of a tile
+        const int t = (warp % 4) * 32 + lane;        // resident row
         const uint32_t lanes = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16);
         const int row = it.r0 + t;                   // within the segment
         const bool live = row < (kKV ? s.n : s.len);
         float nl = 0.f, nd = 0.f;
-        // where the row's allowed streamed rows begin and end (see wb_softmax), as segment rows
+        // the resident row's allowed streamed rows: r < hi with r >= lo or r < sk
         int lo = 0, hi = 0, sk = 0;
         if (kKV) {
             // rows i >= key, min(i, n) - key < window (or any, for a sink)
@@ -493,53 +424,57 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
             hi = !live ? 0 : (row < p.n_sinks || s.n - row < p.window ? s.len : row + p.window);
         } else if (live) {
             const size_t at = ((size_t)s.tok0 + row) * p.H + it.h;
-            nl = wb_neg_lse(p.lse[at]);
+            nl = win_neg_lse(p.lse[at]);
             nd = -p.dvec[at];
             lo = max(min(row, s.n) - p.window + 1, 0);
             hi = min(row + 1, s.n);
             sk = p.n_sinks;
         }
-        // KV: -lse and -Dvec of a streamed tile's rows, threads 0..63 the one, 64..127 the other;
-        // fetched one tile ahead
-        auto fetch = [&](int i) -> float {
-            if (!kKV || i >= total) return 0.f;
-            const int g = i / it.cnt;
-            const int r = it.row(i - g * it.cnt) + t % 64;
+        // KV: -lse and -Dvec of a streamed tile's rows: threads 0..63 of the group's first half the one,
+        // 64..127 the other; fetched one tile ahead
+        int idx = x, g = 0;                          // place of the group's tile
+        auto wrap = [&]() {
+            while (idx >= cnt && g < p.G) idx -= cnt, ++g;
+        };
+        wrap();
+        auto fetch = [&]() -> float {
+            if (!kKV || half != 0 || g >= p.G) return 0.f;
+            const int r = it.sweep.row(idx) + t % 64;
             if (r >= s.len) return 0.f;
             const size_t at = ((size_t)s.tok0 + r) * p.H + it.h * p.G + g;
-            return t < 64 ? wb_neg_lse(p.lse[at]) : -p.dvec[at];
+            return t < 64 ? win_neg_lse(p.lse[at]) : -p.dvec[at];
         };
-        float ahead = fetch(x);
+        float ahead = total > 0 ? fetch() : 0.f;
         uint32_t ngrp = 0;
         bool ok = true;
         for (int i = x; i < total; i += C::kStages) {
             const int k = i / C::kStages;
-            float* st = stat + ((x * 2 + (k & 1)) * 2) * kWbStr;
+            float* st = stat + ((x * 2 + (k & 1)) * 2) * kWinStr;
+            const int row0 = it.sweep.row(idx);
+            idx += C::kStages;
             if (kKV) {
-                st[t] = ahead;
-                ahead = fetch(i + C::kStages);
+                wrap();
+                if (half == 0) st[t] = ahead;
+                ahead = fetch();
                 if (!(ok = warp_group_sync(grp + x, ngrp, ctl, lane))) break;
             }
-            const int row0 = it.row(kKV ? i % it.cnt : i);
+            const int c0 = row0 + half * 32;         // streamed row of this half's first column
+            const uint32_t see = (uint32_t)win_see(lo - c0, hi - c0, sk - c0);
             ok = __all_sync(0xffffffffu, mbar_wait(s_ready + x, k & 1, ctl));
             if (!ok) break;
             tc_fence_after_sync();
-            wb_softmax<kKV>(lanes + x * 128, p.sl2, st, st + kWbStr, nl, nd, max(lo - row0, 0), max(hi - row0, 0),
-                            max(sk - row0, 0));
+            wb_softmax<kKV>(lanes + x * 128 + half * 32, p.sl2, st + half * 32, st + kWinStr + half * 32, nl, nd, see);
             // streamed rows that are no row (KV: behind the segment) or no past key (dQ) become zeros
             const int end = (kKV ? s.len : s.n) - row0;
-            if (end < kWbStr) {
-                if (t < kWbStr && t >= end) {
-                    uint8_t* dst = ring + (i % C::kSlots) * C::kSlotBytes + t * C::kRowBytes;
+            if (end < kWinStr) {
+                // the first half of the group clears T0's rows, the second T1's
+                if (t < kWinStr && t >= end && (kKV || half == 0)) {
+                    uint8_t* dst = ring + (i % C::kSlots) * C::kSlotBytes + half * C::kStrTile + t * C::kRowBytes;
 #pragma unroll
                     for (int c = 0; c < C::kBoxes; ++c)
 #pragma unroll
-                        for (int a = 0; a < C::kRowBytes; a += 16) {
+                        for (int a = 0; a < C::kRowBytes; a += 16)
                             *reinterpret_cast<uint4*>(dst + c * C::kStrBox + a) = make_uint4(0u, 0u, 0u, 0u);
-                            if (kKV)
-                                *reinterpret_cast<uint4*>(dst + C::kStrTile + c * C::kStrBox + a) =
-                                    make_uint4(0u, 0u, 0u, 0u);
-                        }
                 }
                 fence_proxy_async_smem();
             }
@@ -552,36 +487,36 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
             tc_fence_after_sync();
         }
         if (ok) {
+            // (the TMEM loads are warp-collective: every lane loads)
             const size_t tok = (size_t)s.tok0 + row;
             if (kKV) {
-                // group 0 stores dV, the last group dK (the TMEM loads are warp-collective)
+                // 2 D accumulator columns over the block's groups of warps, dV first
+                constexpr int kPart = 2 * D / (2 * C::kStages);
+                const int c_first = (x * 2 + half) * kPart;
+                const bool is_dk = c_first >= D;
+                const float f = is_dk ? p.scale : 1.f;
+                void* out = is_dk ? p.dk : p.dv;
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    if (C::kStages == 2 && y != x) continue;
-                    const uint32_t col = y == 0 ? C::kColAcc0 : C::kColAcc1;
-                    const float f = y == 0 ? 1.f : p.scale;
-                    void* out = y == 0 ? p.dv : p.dk;
+                for (int c = 0; c < kPart; c += 32) {
+                    uint32_t a[32];
+                    tmem_ld32(lanes + C::kColAcc0 + c_first + c, a);
+                    if (!live) continue;
 #pragma unroll
-                    for (int c0 = 0; c0 < D; c0 += 32) {
-                        uint32_t a[32];
-                        tmem_ld32(lanes + col + c0, a);
-                        if (!live) continue;
+                    for (int e = 0; e < 32; e += 8) {
+                        float o[8];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            float o[8];
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) o[i] = f * __uint_as_float(a[e + i]);
-                            wb_store8(out, p.grad_fp32, (tok * p.Hkv + it.h) * D + c0 + e, o);
-                        }
+                        for (int i = 0; i < 8; ++i) o[i] = f * __uint_as_float(a[e + i]);
+                        win_store8(out, p.grad_fp32, (tok * p.Hkv + it.h) * D + (c_first - (is_dk ? D : 0)) + c + e, o);
                     }
                 }
             } else {
                 const size_t at = tok * p.H + it.h;
                 const bool cand = live && row >= s.n;
                 const float ds = cand ? p.dself[at] : 0.f;
+                // D columns in pieces of 32 over the groups of warps
 #pragma unroll
                 for (int c0 = 0; c0 < D; c0 += 32) {
-                    if (C::kStages == 2 && (c0 / 64) % 2 != x) continue;
+                    if ((c0 / 32) % (2 * C::kStages) != x * 2 + half) continue;
                     uint32_t a[32];
                     if (total > 0) {
                         tmem_ld32(lanes + C::kColAcc1 + c0, a);
@@ -596,14 +531,14 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
 #pragma unroll
                         for (int i = 0; i < 8; ++i) o[i] = __uint_as_float(a[e + i]);
                         if (cand) {
-                            wb_unpack8(__ldg(reinterpret_cast<const uint4*>(
-                                           p.k + (tok * p.Hkv + it.h / p.G) * D + c0 + e)), kf);
+                            win_unpack8(__ldg(reinterpret_cast<const uint4*>(
+                                            p.k + (tok * p.Hkv + it.h / p.G) * D + c0 + e)), kf);
 #pragma unroll
                             for (int i = 0; i < 8; ++i) o[i] = fmaf(ds, kf[i], o[i]);
                         }
 #pragma unroll
                         for (int i = 0; i < 8; ++i) o[i] *= p.scale;
-                        wb_store8(p.dq, p.grad_fp32, at * D + c0 + e, o);
+                        win_store8(p.dq, p.grad_fp32, at * D + c0 + e, o);
                     }
                 }
             }

@@ -1,0 +1,445 @@
+// The masked prefill under a sliding window with first rows that stay visible,
+// on sm_100a.
+//
+// Row i of a segment of n past rows and its candidates stands at pos = min(i, n)
+// and sees the past keys j <= i, j < n with pos - j < window or j < n_sinks, and
+// a candidate its own key:
+//   O_i = sum_j softmax_j(scale q_i . k_j) v_j
+// One block per (segment, query head, 128 query rows): it visits the 64-key
+// tiles of the sinks and of the rows' windows and no others.  Under a window a
+// block's sweep is short (window / 64 + 3 tiles), so what the masked prefill's
+// engine does for long sweeps (two query tiles per block, one persistent block
+// per SM) leaves the SM waiting for one item's first loads, its chain of
+// products and softmaxes and its epilogue; here several small blocks share an
+// SM and fill each other's gaps (three at D <= 64, two at D = 128).
+// Per key tile: S = Q K^T (tcgen05, TMEM: lane = row), the softmax warps (thread
+// = row) read S, update the row maximum and sum (float32; O in TMEM is rescaled
+// only when a maximum grows by more than 2^8), write P as bfloat16 over S
+// (relative 2^-8), O += P V with P as A from TMEM.  At D = 128 S has two stages,
+// so the next tile's S is computed while the softmax works; at D <= 64 one, and
+// the other blocks' products run meanwhile.
+// Warps: 0-3 softmax and epilogue, 4 TMA producer, 5 MMA issuer (owns TMEM).
+// What a row does not see reaches nothing of it: masked scores are replaced, and
+// rows of V that are no past key of the segment are zeroed in shared memory.  A
+// value that is NaN or infinite can still reach a row of its tile that the mask
+// keeps from it, as 0 * NaN in the product P V; so a row whose result is not
+// finite is computed again from its visible keys alone (win_row_again).
+#pragma once
+
+#include "sm100_ptx.cuh"
+#include "tmem_wide.cuh"
+#include "unipin.h"
+#include "win_common.cuh"
+
+namespace unipin {
+
+constexpr float kWfRescaleLog2 = 8.0f;   // rescale O only when a row max grows by > 2^8
+
+template <int D>
+struct WfCfg {
+    static constexpr int kBoxElems = D >= 64 ? 64 : D;
+    static constexpr int kBoxes = D / kBoxElems;
+    static constexpr int kRowBytes = kBoxElems * 2;
+    static constexpr uint32_t kLayout = D >= 64 ? kLayoutSw128 : kLayoutSw64;
+    static constexpr int kQBox = kWinRes * kRowBytes;
+    static constexpr int kQTile = kBoxes * kQBox;
+    static constexpr int kKvBox = kWinStr * kRowBytes;
+    static constexpr int kKvTile = kBoxes * kKvBox;
+    static constexpr int kSlotBytes = 2 * kKvTile;                 // K and V of a key tile
+    static constexpr int kSlots = D == 128 ? 2 : 3;
+    static constexpr int kStages = D == 128 ? 2 : 1;               // of S
+    static constexpr int kBlocksPerSm = D == 128 ? 2 : 3;
+    static constexpr int kThreads = 192;
+    static constexpr int kOffRing = kQTile;
+    static constexpr int kOffBar = kOffRing + kSlots * kSlotBytes;
+    static constexpr int kSmemBytes = kOffBar + 256;
+    // TMEM columns: the S stages (P over the first half of each), then O
+    static constexpr int kColO = kStages * kWinStr;
+    static constexpr int kTmemCols = D == 128 ? 256 : 128;
+    static_assert(kColO + D <= kTmemCols, "TMEM budget");
+    static_assert((kSmemBytes + 1024) * kBlocksPerSm <= 228 * 1024, "shared memory budget");
+    static_assert(kTmemCols * kBlocksPerSm <= 512, "TMEM budget");
+};
+
+struct WfParams {
+    const __nv_bfloat16* q;     // [T, H, D]
+    const __nv_bfloat16* k;     // [T, H_kv, D]
+    const __nv_bfloat16* v;
+    void* out;                  // [T, H, D] fp32 or bf16
+    float* lse;                 // [T, H] or null
+    const int* cu;
+    const int* past;
+    int B, H, Hkv, G, total_rows, max_rows;
+    int window, n_sinks;
+    int out_fp32;
+    unsigned blocks;
+    float sl2;
+    int* status;
+    unsigned long long wait_limit_ns;
+};
+
+// q . k in log2 units, both rows of D bfloat16.
+template <int D>
+__device__ __forceinline__ float wf_score(const __nv_bfloat16* q, const __nv_bfloat16* k, float sl2)
+{
+    float a = 0.f, b = 0.f;
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) {
+        float x[8], y[8];
+        win_unpack8(__ldg(reinterpret_cast<const uint4*>(q) + c), x);
+        win_unpack8(__ldg(reinterpret_cast<const uint4*>(k) + c), y);
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+            a = fmaf(x[e], y[e], a);
+            b = fmaf(x[e + 1], y[e + 1], b);
+        }
+    }
+    return (a + b) * sl2;
+}
+
+// A row whose result is not finite, from its visible keys alone: O = sum_j 2^(s_j - lse) v_j, in pieces
+// of eight elements (one thread; rare, so not fast).
+template <int D>
+__device__ __noinline__ void win_row_again(const WfParams& p, int tok0, int n, int row, int h, float lse)
+{
+    const size_t tok = (size_t)tok0 + row;
+    const __nv_bfloat16* q = p.q + (tok * p.H + h) * D;
+    const int hk = h / p.G;
+    const int lo = max(min(row, n) - p.window + 1, 0), hi = min(row + 1, n), sk = min(p.n_sinks, lo);
+    const float nl = win_neg_lse(lse);
+    for (int c = 0; c < D / 8; ++c) {
+        float o[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = 0.f;
+        auto add = [&](int j) {
+            const size_t at = (((size_t)tok0 + j) * p.Hkv + hk) * D;
+            const float w = ex2_approx(wf_score<D>(q, p.k + at, p.sl2) + nl);
+            float v[8];
+            win_unpack8(__ldg(reinterpret_cast<const uint4*>(p.v + at) + c), v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = fmaf(w, v[e], o[e]);
+        };
+        for (int j = 0; j < min(sk, hi); ++j) add(j);
+        for (int j = lo; j < hi; ++j) add(j);
+        if (row >= n) add(row);
+        win_store8(p.out, p.out_fp32, (tok * p.H + h) * D + c * 8, o);
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
+    win_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ WfParams p)
+{
+    using C = WfCfg<D>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int warp = threadIdx.x / 32;
+    const int lane = threadIdx.x % 32;
+    if (p.status && *reinterpret_cast<volatile int*>(p.status) == (int)UNIPIN_ERR_DEVICE_TIMEOUT) return;
+    if ((smem_u32(smem) & 1023u) != 0) {   // the layout needs 1024-byte aligned tiles
+        if (threadIdx.x == 0) report(p.status, (int)UNIPIN_ERR_CUDA);
+        return;
+    }
+    // the last rows of the segments, whose sweeps are the longest, come first
+    const unsigned block = p.blocks - 1 - blockIdx.x;
+    const unsigned bh_count = (unsigned)p.B * p.H;
+    const int t0 = (int)(block / bh_count);
+    const unsigned bh = block - (unsigned)t0 * bh_count;
+    const int b = (int)(bh / p.H), h = (int)(bh - (unsigned)b * p.H);
+    const int r0 = t0 * kWinRes;
+    const WinSegment s = win_segment(p.cu, p.past, b, p.max_rows, p.total_rows);
+    if (!s.ok && t0 == 0 && h == 0 && threadIdx.x == 0) report(p.status, (int)UNIPIN_ERR_OUT_OF_RANGE);
+    if (!s.rows_ok || r0 >= s.len) return;
+    if (!s.ok) {
+        // a history length out of range: zeros
+        const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        const int row = r0 + threadIdx.x;
+        if (threadIdx.x < kWinRes && row < s.len)
+            for (int c = 0; c < D / 8; ++c)
+                win_store8(p.out, p.out_fp32, (((size_t)s.tok0 + row) * p.H + h) * D + c * 8, z);
+        return;
+    }
+    const WinSweep sweep = win_key_sweep(r0, s, p.window, p.n_sinks);
+    const int total = sweep.cnt;
+
+    uint8_t* sQ = smem;
+    uint8_t* ring = smem + C::kOffRing;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+    uint64_t* bar_q = bars + 0;
+    uint64_t* bar_drain = bars + 1;
+    uint64_t* pv_done = bars + 2;
+    uint64_t* s_ready = bars + 3;      // [2]
+    uint64_t* p_ready = bars + 5;      // [2]
+    uint64_t* full = bars + 7;         // [kSlots]
+    uint64_t* empty = full + C::kSlots;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(empty + C::kSlots);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const bool leader = lane == 0;
+    WaitCtl ctl{abort_flag, p.status, p.wait_limit_ns, (int)UNIPIN_ERR_DEVICE_TIMEOUT};
+    auto load_tile = [&](int i) {
+        const int st = i % C::kSlots;
+        uint8_t* dst = ring + st * C::kSlotBytes;
+        const int tok = s.tok0 + sweep.row(i), hk = h / p.G;
+        mbar_arrive_expect_tx(full + st, C::kSlotBytes);
+        for (int c = 0; c < C::kBoxes; ++c) {
+            tma_load_3d(dst + c * C::kKvBox, &tm_k, full + st, c * C::kBoxElems, hk, tok);
+            tma_load_3d(dst + C::kKvTile + c * C::kKvBox, &tm_v, full + st, c * C::kBoxElems, hk, tok);
+        }
+    };
+    if (warp == 4 && leader) {
+        mbar_init(bar_q, 1);
+        mbar_init(bar_drain, 1);
+        mbar_init(pv_done, 1);
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(s_ready + x, 1);
+            mbar_init(p_ready + x, 4);
+        }
+        for (int x = 0; x < C::kSlots; ++x) {
+            mbar_init(full + x, 1);
+            mbar_init(empty + x, 1);
+        }
+        *abort_flag = 0;
+        fence_mbarrier_init();
+        // the first loads need no other warp
+        if (total > 0) {
+            mbar_arrive_expect_tx(bar_q, C::kQTile);
+            for (int c = 0; c < C::kBoxes; ++c)
+                tma_load_3d(sQ + c * C::kQBox, &tm_q, bar_q, c * C::kBoxElems, h, s.tok0 + r0);
+            for (int i = 0; i < min(total, C::kSlots); ++i) load_tile(i);
+        }
+    }
+    if (warp == 5) {
+        tmem_alloc(tmem_slot, C::kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 4) {
+        // ------------------------------------------------------------ producer
+        int issued = min(total, C::kSlots);
+        for (; issued < total; ++issued) {
+            if (!__all_sync(0xffffffffu, mbar_wait(empty + issued % C::kSlots, (issued / C::kSlots - 1) & 1, ctl))) break;
+            if (leader) load_tile(issued);
+        }
+        if (leader && total > 0) {
+            // every copy lands before the block exits
+            mbar_wait_drain(bar_q, 0, p.wait_limit_ns);
+            for (int v = (issued > C::kSlots ? issued - C::kSlots : 0); v < issued; ++v)
+                mbar_wait_drain(full + v % C::kSlots, (v / C::kSlots) & 1, p.wait_limit_ns);
+        }
+    } else if (warp == 5) {
+        // --------------------------------------------------------- MMA issuer
+        constexpr uint32_t idesc_s = idesc_bf16_f32(kWinRes, kWinStr, false);
+        constexpr uint32_t idesc_o = idesc_bf16_f32(kWinRes, D, true);      // A from TMEM, B MN-major
+        constexpr int kStepsPerBox = C::kBoxElems / 16;
+        const uint64_t d_q = smem_desc(smem_u32(sQ), 16, 8 * C::kRowBytes, C::kLayout);
+        const uint64_t d_k = smem_desc(smem_u32(ring), 16, 8 * C::kRowBytes, C::kLayout);
+        const uint64_t d_v = smem_desc(smem_u32(ring) + C::kKvTile, C::kKvBox, 8 * C::kRowBytes, C::kLayout);
+        // S of tile i; the product that reads the stage's P was issued before and runs first
+        auto scores = [&](int i) -> bool {
+            const int st = i % C::kSlots;
+            if (!__all_sync(0xffffffffu, mbar_wait(full + st, (i / C::kSlots) & 1, ctl))) return false;
+            tc_fence_after_sync();
+            if (leader) {
+                const uint64_t slot = (uint64_t)((st * C::kSlotBytes) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const int box = kk / kStepsPerBox, in = (kk % kStepsPerBox) * 32;
+                    umma_bf16_ss(tmem + (i % C::kStages) * kWinStr, d_q + (uint64_t)((box * C::kQBox + in) >> 4),
+                                 d_k + slot + (uint64_t)((box * C::kKvBox + in) >> 4), idesc_s, kk > 0 ? 1u : 0u);
+                }
+                umma_commit(s_ready + i % C::kStages);
+            }
+            return true;
+        };
+        bool ok = total == 0 || __all_sync(0xffffffffu, mbar_wait(bar_q, 0, ctl));
+        for (int i = 0; ok && i < min(C::kStages, total); ++i) ok = scores(i);
+        for (int i = 0; ok && i < total; ++i) {
+            const int x = i % C::kStages, st = i % C::kSlots;
+            ok = __all_sync(0xffffffffu, mbar_wait(p_ready + x, (i / C::kStages) & 1, ctl));
+            if (!ok) break;
+            tc_fence_after_sync();
+            if (leader) {
+                const uint64_t slot = (uint64_t)((st * C::kSlotBytes) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < kWinStr / 16; ++kk)
+                    umma_bf16_ts(tmem + C::kColO, tmem + x * kWinStr + kk * 8,
+                                 d_v + slot + (uint64_t)((kk * 16 * C::kRowBytes) >> 4), idesc_o,
+                                 (i > 0 || kk > 0) ? 1u : 0u);
+                umma_commit(empty + st);
+                umma_commit(pv_done);
+            }
+            if (i + C::kStages < total) ok = scores(i + C::kStages);
+        }
+        if (leader) {
+            umma_commit(bar_drain);
+            mbar_wait_drain(bar_drain, 0, p.wait_limit_ns);
+        }
+    } else {
+        // ------------------------------------------------- softmax + epilogue
+        const int t = threadIdx.x;
+        const int row = r0 + t;                      // within the segment
+        const bool live = row < s.len;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+        const uint32_t tO = lanes + C::kColO;
+        const size_t at = ((size_t)s.tok0 + row) * p.H + h;
+        const size_t at_kv = ((size_t)s.tok0 + row) * p.Hkv + h / p.G;
+        const bool self = live && row >= s.n;        // a candidate: its own key
+        const float ss = self ? wf_score<D>(p.q + at * D, p.k + at_kv * D, p.sl2) : -INFINITY;
+        // the row sees keys j < hi with j >= lo or j < sk
+        const int lo = max(min(row, s.n) - p.window + 1, 0);
+        const int hi = live ? min(row + 1, s.n) : 0;
+        const float sl2 = p.sl2;
+        float m = -INFINITY;     // reference max (log2 units) that P and O are relative to
+        float l = 0.f;           // row sum relative to m
+        bool odd = false;        // a visible score is NaN or +inf: so is the row
+        bool ok = true;
+        for (int i = 0; i < total; ++i) {
+            const int x = i % C::kStages;
+            const uint32_t tS = lanes + x * kWinStr;
+            const int row0 = sweep.row(i);
+            ok = __all_sync(0xffffffffu, mbar_wait(s_ready + x, (i / C::kStages) & 1, ctl));
+            if (!ok) break;
+            tc_fence_after_sync();
+            uint32_t sc[kWinStr];
+            tmem_ld64(tS, sc);
+            const uint64_t see = win_see(lo - row0, hi - row0, p.n_sinks - row0);
+            if (!__all_sync(0xffffffffu, see == ~0ull)) {
+#pragma unroll
+                for (int e = 0; e < kWinStr; ++e)
+                    if (!((e < 32 ? (uint32_t)see : (uint32_t)(see >> 32)) >> (e & 31) & 1u)) sc[e] = 0xff800000u;   // -inf
+            }
+            float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < kWinStr; e += 8) {
+                mx0 = max3f<true>(mx0, __uint_as_float(sc[e]), __uint_as_float(sc[e + 1]));
+                mx1 = max3f<true>(mx1, __uint_as_float(sc[e + 2]), __uint_as_float(sc[e + 3]));
+                mx2 = max3f<true>(mx2, __uint_as_float(sc[e + 4]), __uint_as_float(sc[e + 5]));
+                mx3 = max3f<true>(mx3, __uint_as_float(sc[e + 6]), __uint_as_float(sc[e + 7]));
+            }
+            const float m_tile = fmax_nan(fmax_nan(mx0, mx1), fmax_nan(mx2, mx3)) * sl2;
+            odd = odd || !(m_tile < INFINITY);
+            // move the reference max only when some row of the warp would see P > 2^8
+            if (__any_sync(0xffffffffu, m_tile > m + kWfRescaleLog2)) {
+                const float m_new = fmaxf(m, m_tile);
+                const float corr = m == -INFINITY ? 0.f : ex2_approx(m - m_new);
+                if (i > 0) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(pv_done, (i - 1) & 1, ctl));
+                    if (!ok) break;
+                    tc_fence_after_sync();
+#pragma unroll
+                    for (int c = 0; c < D; c += 8) {
+                        uint32_t o[8];
+                        tmem_ld8(tO + c, o);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+                        tmem_st8(tO + c, o);
+                    }
+                }
+                l *= corr;
+                m = m_new;
+            }
+            const float m_use = m == -INFINITY ? 0.f : m;
+            const uint64_t sc2 = f2_pack(sl2, sl2), nm2 = f2_pack(-m_use, -m_use);
+            uint64_t acc[2] = {0ull, 0ull};
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    const int e = half * 32 + 2 * c;
+                    const uint64_t x2 = f2_fma(f2_pack(__uint_as_float(sc[e]), __uint_as_float(sc[e + 1])), sc2, nm2);
+                    float p0, p1;
+                    if ((c & 3) == 3) {              // one pair in four on the FMA pipe
+                        exp2_poly2(x2, p0, p1);
+                    } else {
+                        f2_unpack(x2, p0, p1);
+                        p0 = ex2_approx(p0);
+                        p1 = ex2_approx(p1);
+                    }
+                    acc[c & 1] = f2_add(acc[c & 1], f2_pack(p0, p1));
+                    pk[c] = pack_bf16x2(p0, p1);
+                }
+                tmem_st16(tS + half * 16, pk);
+            }
+            {
+                float a, c;
+                f2_unpack(f2_add(acc[0], acc[1]), a, c);
+                l += a + c;
+            }
+            // rows of V that are no past key of the segment become zeros
+            const int end = s.n - row0;
+            if (end < kWinStr) {
+                if (t < kWinStr && t >= end) {
+                    uint8_t* dst = ring + (i % C::kSlots) * C::kSlotBytes + C::kKvTile + t * C::kRowBytes;
+#pragma unroll
+                    for (int c = 0; c < C::kBoxes; ++c)
+#pragma unroll
+                        for (int a = 0; a < C::kRowBytes; a += 16)
+                            *reinterpret_cast<uint4*>(dst + c * C::kKvBox + a) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_ready + x);
+        }
+        if (ok && total > 0) {
+            ok = __all_sync(0xffffffffu, mbar_wait(pv_done, (total - 1) & 1, ctl));
+            tc_fence_after_sync();
+        }
+        if (ok) {
+            const float m_fin = fmaxf(m, ss);
+            const float a = m == -INFINITY ? 0.f : ex2_approx(m - m_fin);
+            const float w = ss == -INFINITY ? 0.f : ex2_approx(ss - m_fin);
+            if (odd || !(ss < INFINITY)) l = __int_as_float(0x7fffffff);
+            const float denom = l * a + w;
+            const float inv = denom == 0.f ? 0.f : 1.f / denom;
+            const float lse = m_fin + log2f(denom);
+            if (live && p.lse) p.lse[at] = lse;
+            float chk = 0.f;     // NaN once an element is not finite
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                if (total > 0) {
+                    tmem_ld32(tO + c * 32, o);       // warp-collective: every lane loads
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0u;
+                }
+                if (!live) continue;
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    float f[8], vf[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(o[g * 8 + e]) * a;
+                    if (self) {
+                        win_unpack8(__ldg(reinterpret_cast<const uint4*>(p.v + at_kv * D) + c * 4 + g), vf);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) f[e] = fmaf(w, vf[e], f[e]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        f[e] *= inv;
+                        chk = fmaf(f[e], 0.f, chk);
+                    }
+                    win_store8(p.out, p.out_fp32, at * D + c * 32 + g * 8, f);
+                }
+            }
+            if (chk != chk) win_row_again<D>(p, s.tok0, s.n, row, h, lse);
+        }
+    }
+
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 5) {
+        __syncwarp();
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, C::kTmemCols);
+    }
+}
+
+}  // namespace unipin
