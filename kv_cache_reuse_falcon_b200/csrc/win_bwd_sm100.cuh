@@ -255,9 +255,18 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
     using C = WbCfg<D>;
     const int warp = threadIdx.x / 32;
     const int lane = threadIdx.x % 32;
+    if (warp == C::kSoftWarps && lane == 0) {
+        tma_prefetch_map(&tm_r0);
+        tma_prefetch_map(&tm_r1);
+        tma_prefetch_map(&tm_s0);
+        tma_prefetch_map(&tm_s1);
+    }
+    // a timeout recorded earlier: later blocks skip their work instead of waiting again
+    const int failed = p.status ? *reinterpret_cast<volatile int*>(p.status) : 0;
     WbItem it;
     WinSegment s;
-    if (!wb_item<kKV>(p, block, it, s)) return;
+    const bool work = wb_item<kKV>(p, block, it, s);
+    if (!work || failed == (int)UNIPIN_ERR_DEVICE_TIMEOUT) return;
     const int cnt = it.sweep.cnt;
     const int total = kKV ? cnt * p.G : cnt;
 
@@ -355,12 +364,13 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
         const uint64_t d_s1 = smem_desc(smem_u32(ring) + C::kStrTile, 16, 8 * C::kRowBytes, C::kLayout);
         const uint64_t d_g0 = smem_desc(smem_u32(ring), C::kStrBox, 8 * C::kRowBytes, C::kLayout);
         const uint64_t d_g1 = smem_desc(smem_u32(ring) + C::kStrTile, C::kStrBox, 8 * C::kRowBytes, C::kLayout);
-        // S and dP of tile i into its stage; the products that read the stage's P and dS were issued
-        // before and run first
-        auto scores = [&](int i) -> bool {
+        auto landed = [&](int i) -> bool {
+            return i >= total ||
+                   __all_sync(0xffffffffu, mbar_wait(full + i % C::kSlots, (i / C::kSlots) & 1, ctl));
+        };
+        // S and dP of tile i (landed) into its stage, whose P and dS no product reads any more
+        auto scores = [&](int i) {
             const int st = i % C::kSlots;
-            if (!__all_sync(0xffffffffu, mbar_wait(full + st, (i / C::kSlots) & 1, ctl))) return false;
-            tc_fence_after_sync();
             if (leader) {
                 const uint32_t tS = tmem + (i % C::kStages) * 128;
                 const uint64_t slot = (uint64_t)((st * C::kSlotBytes) >> 4);
@@ -378,13 +388,18 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
                 }
                 umma_commit(s_ready + i % C::kStages);
             }
-            return true;
         };
         bool ok = total == 0 || __all_sync(0xffffffffu, mbar_wait(bar_res, 0, ctl));
-        for (int i = 0; ok && i < min(C::kStages, total); ++i) ok = scores(i);
+        for (int i = 0; ok && i < min(C::kStages, total); ++i) {
+            if (!(ok = landed(i))) break;
+            tc_fence_after_sync();
+            scores(i);
+        }
         for (int i = 0; ok && i < total; ++i) {
             const int x = i % C::kStages, st = i % C::kSlots;
-            ok = __all_sync(0xffffffffu, mbar_wait(p_ready + x, (i / C::kStages) & 1, ctl));
+            // kSlots > kStages: the later tile's load does not need this tile's slot
+            ok = landed(i + C::kStages) &&
+                 __all_sync(0xffffffffu, mbar_wait(p_ready + x, (i / C::kStages) & 1, ctl));
             if (!ok) break;
             tc_fence_after_sync();
             if (leader) {
@@ -401,7 +416,14 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
                 umma_commit(empty + st);
                 if (i + 1 == total) umma_commit(acc_done);
             }
-            if (i + C::kStages < total) ok = scores(i + C::kStages);
+            if (i + C::kStages < total) {
+                // only products into one accumulator are sure to run in order: S and dP over P and dS wait
+                // for the products that read those
+                ok = __all_sync(0xffffffffu, mbar_wait(empty + st, (i / C::kSlots) & 1, ctl));
+                if (!ok) break;
+                tc_fence_after_sync();
+                scores(i + C::kStages);
+            }
         }
         if (leader) {
             umma_commit(bar_drain);
@@ -564,7 +586,6 @@ __global__ void __launch_bounds__(WbCfg<D>::kThreads, WbCfg<D>::kBlocksPerSm)
                    const __grid_constant__ WbParams p)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
-    if (p.status && *reinterpret_cast<volatile int*>(p.status) == (int)UNIPIN_ERR_DEVICE_TIMEOUT) return;
     if ((smem_u32(smem) & 1023u) != 0) {
         if (threadIdx.x == 0) report(p.status, (int)UNIPIN_ERR_CUDA);
         return;

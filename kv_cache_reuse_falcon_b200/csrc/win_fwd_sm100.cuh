@@ -45,13 +45,15 @@ struct WfCfg {
     static constexpr int kQTile = kBoxes * kQBox;
     static constexpr int kKvBox = kWinStr * kRowBytes;
     static constexpr int kKvTile = kBoxes * kKvBox;
-    static constexpr int kSlotBytes = 2 * kKvTile;                 // K and V of a key tile
-    static constexpr int kSlots = D == 128 ? 2 : 3;
+    // rings of K and of V tiles; K runs ahead by the stages of S, so at D = 128 it has one slot more
+    static constexpr int kKSlots = 3;
+    static constexpr int kVSlots = D == 128 ? 2 : 3;
     static constexpr int kStages = D == 128 ? 2 : 1;               // of S
     static constexpr int kBlocksPerSm = D == 128 ? 2 : 3;
     static constexpr int kThreads = 192;
-    static constexpr int kOffRing = kQTile;
-    static constexpr int kOffBar = kOffRing + kSlots * kSlotBytes;
+    static constexpr int kOffK = kQTile;
+    static constexpr int kOffV = kOffK + kKSlots * kKvTile;
+    static constexpr int kOffBar = kOffV + kVSlots * kKvTile;
     static constexpr int kSmemBytes = kOffBar + 256;
     // TMEM columns: the S stages (P over the first half of each), then O
     static constexpr int kColO = kStages * kWinStr;
@@ -135,7 +137,13 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x / 32;
     const int lane = threadIdx.x % 32;
-    if (p.status && *reinterpret_cast<volatile int*>(p.status) == (int)UNIPIN_ERR_DEVICE_TIMEOUT) return;
+    if (warp == 4 && lane == 0) {
+        tma_prefetch_map(&tm_q);
+        tma_prefetch_map(&tm_k);
+        tma_prefetch_map(&tm_v);
+    }
+    // a timeout recorded earlier: later blocks skip their work instead of waiting again
+    const int failed = p.status ? *reinterpret_cast<volatile int*>(p.status) : 0;
     if ((smem_u32(smem) & 1023u) != 0) {   // the layout needs 1024-byte aligned tiles
         if (threadIdx.x == 0) report(p.status, (int)UNIPIN_ERR_CUDA);
         return;
@@ -149,7 +157,7 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
     const int r0 = t0 * kWinRes;
     const WinSegment s = win_segment(p.cu, p.past, b, p.max_rows, p.total_rows);
     if (!s.ok && t0 == 0 && h == 0 && threadIdx.x == 0) report(p.status, (int)UNIPIN_ERR_OUT_OF_RANGE);
-    if (!s.rows_ok || r0 >= s.len) return;
+    if (!s.rows_ok || r0 >= s.len || failed == (int)UNIPIN_ERR_DEVICE_TIMEOUT) return;
     if (!s.ok) {
         // a history length out of range: zeros
         const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -163,29 +171,29 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
     const int total = sweep.cnt;
 
     uint8_t* sQ = smem;
-    uint8_t* ring = smem + C::kOffRing;
+    uint8_t* sK = smem + C::kOffK;
+    uint8_t* sV = smem + C::kOffV;
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
     uint64_t* bar_q = bars + 0;
     uint64_t* bar_drain = bars + 1;
     uint64_t* pv_done = bars + 2;
     uint64_t* s_ready = bars + 3;      // [2]
     uint64_t* p_ready = bars + 5;      // [2]
-    uint64_t* full = bars + 7;         // [kSlots]
-    uint64_t* empty = full + C::kSlots;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(empty + C::kSlots);
+    uint64_t* k_full = bars + 7;       // [3]
+    uint64_t* k_empty = bars + 10;
+    uint64_t* v_full = bars + 13;
+    uint64_t* v_empty = bars + 16;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 19);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const bool leader = lane == 0;
     WaitCtl ctl{abort_flag, p.status, p.wait_limit_ns, (int)UNIPIN_ERR_DEVICE_TIMEOUT};
-    auto load_tile = [&](int i) {
-        const int st = i % C::kSlots;
-        uint8_t* dst = ring + st * C::kSlotBytes;
-        const int tok = s.tok0 + sweep.row(i), hk = h / p.G;
-        mbar_arrive_expect_tx(full + st, C::kSlotBytes);
-        for (int c = 0; c < C::kBoxes; ++c) {
-            tma_load_3d(dst + c * C::kKvBox, &tm_k, full + st, c * C::kBoxElems, hk, tok);
-            tma_load_3d(dst + C::kKvTile + c * C::kKvBox, &tm_v, full + st, c * C::kBoxElems, hk, tok);
-        }
+    auto load_tile = [&](const CUtensorMap& map, uint8_t* dst, uint64_t* bar, int i) {
+        mbar_arrive_expect_tx(bar, C::kKvTile);
+        for (int c = 0; c < C::kBoxes; ++c)
+            tma_load_3d(dst + c * C::kKvBox, &map, bar, c * C::kBoxElems, h / p.G, s.tok0 + sweep.row(i));
     };
+    auto load_k = [&](int i) { load_tile(tm_k, sK + i % C::kKSlots * C::kKvTile, k_full + i % C::kKSlots, i); };
+    auto load_v = [&](int i) { load_tile(tm_v, sV + i % C::kVSlots * C::kKvTile, v_full + i % C::kVSlots, i); };
     if (warp == 4 && leader) {
         mbar_init(bar_q, 1);
         mbar_init(bar_drain, 1);
@@ -194,9 +202,11 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
             mbar_init(s_ready + x, 1);
             mbar_init(p_ready + x, 4);
         }
-        for (int x = 0; x < C::kSlots; ++x) {
-            mbar_init(full + x, 1);
-            mbar_init(empty + x, 1);
+        for (int x = 0; x < 3; ++x) {
+            mbar_init(k_full + x, 1);
+            mbar_init(k_empty + x, 1);
+            mbar_init(v_full + x, 1);
+            mbar_init(v_empty + x, 1);
         }
         *abort_flag = 0;
         fence_mbarrier_init();
@@ -205,7 +215,10 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
             mbar_arrive_expect_tx(bar_q, C::kQTile);
             for (int c = 0; c < C::kBoxes; ++c)
                 tma_load_3d(sQ + c * C::kQBox, &tm_q, bar_q, c * C::kBoxElems, h, s.tok0 + r0);
-            for (int i = 0; i < min(total, C::kSlots); ++i) load_tile(i);
+            for (int i = 0; i < min(total, C::kKSlots); ++i) {
+                load_k(i);
+                if (i < C::kVSlots) load_v(i);
+            }
         }
     }
     if (warp == 5) {
@@ -219,16 +232,32 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
 
     if (warp == 4) {
         // ------------------------------------------------------------ producer
-        int issued = min(total, C::kSlots);
-        for (; issued < total; ++issued) {
-            if (!__all_sync(0xffffffffu, mbar_wait(empty + issued % C::kSlots, (issued / C::kSlots - 1) & 1, ctl))) break;
-            if (leader) load_tile(issued);
+        // in the order in which the slots come free: V of a tile behind the P V of the tile kVSlots before,
+        // K behind the (earlier) S of the tile kKSlots before
+        int nk = min(total, C::kKSlots), nv = min(total, C::kVSlots);
+        bool ok = true;
+        while (ok && (nk < total || nv < total)) {
+            if (nv < total && nv - C::kVSlots < nk - C::kKSlots) {
+                ok = __all_sync(0xffffffffu, mbar_wait(v_empty + nv % C::kVSlots, (nv / C::kVSlots - 1) & 1, ctl));
+                if (ok && leader) load_v(nv);
+                nv += ok;
+            } else if (nk < total) {
+                ok = __all_sync(0xffffffffu, mbar_wait(k_empty + nk % C::kKSlots, (nk / C::kKSlots - 1) & 1, ctl));
+                if (ok && leader) load_k(nk);
+                nk += ok;
+            } else {
+                ok = __all_sync(0xffffffffu, mbar_wait(v_empty + nv % C::kVSlots, (nv / C::kVSlots - 1) & 1, ctl));
+                if (ok && leader) load_v(nv);
+                nv += ok;
+            }
         }
         if (leader && total > 0) {
             // every copy lands before the block exits
             mbar_wait_drain(bar_q, 0, p.wait_limit_ns);
-            for (int v = (issued > C::kSlots ? issued - C::kSlots : 0); v < issued; ++v)
-                mbar_wait_drain(full + v % C::kSlots, (v / C::kSlots) & 1, p.wait_limit_ns);
+            for (int i = max(nk - C::kKSlots, 0); i < nk; ++i)
+                mbar_wait_drain(k_full + i % C::kKSlots, (i / C::kKSlots) & 1, p.wait_limit_ns);
+            for (int i = max(nv - C::kVSlots, 0); i < nv; ++i)
+                mbar_wait_drain(v_full + i % C::kVSlots, (i / C::kVSlots) & 1, p.wait_limit_ns);
         }
     } else if (warp == 5) {
         // --------------------------------------------------------- MMA issuer
@@ -236,15 +265,16 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
         constexpr uint32_t idesc_o = idesc_bf16_f32(kWinRes, D, true);      // A from TMEM, B MN-major
         constexpr int kStepsPerBox = C::kBoxElems / 16;
         const uint64_t d_q = smem_desc(smem_u32(sQ), 16, 8 * C::kRowBytes, C::kLayout);
-        const uint64_t d_k = smem_desc(smem_u32(ring), 16, 8 * C::kRowBytes, C::kLayout);
-        const uint64_t d_v = smem_desc(smem_u32(ring) + C::kKvTile, C::kKvBox, 8 * C::kRowBytes, C::kLayout);
-        // S of tile i; the product that reads the stage's P was issued before and runs first
-        auto scores = [&](int i) -> bool {
-            const int st = i % C::kSlots;
-            if (!__all_sync(0xffffffffu, mbar_wait(full + st, (i / C::kSlots) & 1, ctl))) return false;
-            tc_fence_after_sync();
+        const uint64_t d_k = smem_desc(smem_u32(sK), 16, 8 * C::kRowBytes, C::kLayout);
+        const uint64_t d_v = smem_desc(smem_u32(sV), C::kKvBox, 8 * C::kRowBytes, C::kLayout);
+        auto k_landed = [&](int i) -> bool {
+            return i >= total ||
+                   __all_sync(0xffffffffu, mbar_wait(k_full + i % C::kKSlots, (i / C::kKSlots) & 1, ctl));
+        };
+        // S of tile i (landed) into its stage, whose P no product reads any more
+        auto scores = [&](int i) {
             if (leader) {
-                const uint64_t slot = (uint64_t)((st * C::kSlotBytes) >> 4);
+                const uint64_t slot = (uint64_t)((i % C::kKSlots * C::kKvTile) >> 4);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const int box = kk / kStepsPerBox, in = (kk % kStepsPerBox) * 32;
@@ -252,27 +282,40 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
                                  d_k + slot + (uint64_t)((box * C::kKvBox + in) >> 4), idesc_s, kk > 0 ? 1u : 0u);
                 }
                 umma_commit(s_ready + i % C::kStages);
+                umma_commit(k_empty + i % C::kKSlots);
             }
-            return true;
         };
         bool ok = total == 0 || __all_sync(0xffffffffu, mbar_wait(bar_q, 0, ctl));
-        for (int i = 0; ok && i < min(C::kStages, total); ++i) ok = scores(i);
+        for (int i = 0; ok && i < min(C::kStages, total); ++i) {
+            if (!(ok = k_landed(i))) break;
+            tc_fence_after_sync();
+            scores(i);
+        }
         for (int i = 0; ok && i < total; ++i) {
-            const int x = i % C::kStages, st = i % C::kSlots;
-            ok = __all_sync(0xffffffffu, mbar_wait(p_ready + x, (i / C::kStages) & 1, ctl));
+            const int x = i % C::kStages;
+            // kKSlots > kStages: K of the later tile does not need this tile's slot.  The softmax has seen
+            // this tile's V land before it says that P is there.
+            ok = k_landed(i + C::kStages) &&
+                 __all_sync(0xffffffffu, mbar_wait(p_ready + x, (i / C::kStages) & 1, ctl));
             if (!ok) break;
             tc_fence_after_sync();
             if (leader) {
-                const uint64_t slot = (uint64_t)((st * C::kSlotBytes) >> 4);
+                const uint64_t slot = (uint64_t)((i % C::kVSlots * C::kKvTile) >> 4);
 #pragma unroll
                 for (int kk = 0; kk < kWinStr / 16; ++kk)
                     umma_bf16_ts(tmem + C::kColO, tmem + x * kWinStr + kk * 8,
                                  d_v + slot + (uint64_t)((kk * 16 * C::kRowBytes) >> 4), idesc_o,
                                  (i > 0 || kk > 0) ? 1u : 0u);
-                umma_commit(empty + st);
+                umma_commit(v_empty + i % C::kVSlots);
                 umma_commit(pv_done);
             }
-            if (i + C::kStages < total) ok = scores(i + C::kStages);
+            if (i + C::kStages < total) {
+                // only products into one accumulator are sure to run in order: S over P waits for P V
+                ok = __all_sync(0xffffffffu, mbar_wait(pv_done, i & 1, ctl));
+                if (!ok) break;
+                tc_fence_after_sync();
+                scores(i + C::kStages);
+            }
         }
         if (leader) {
             umma_commit(bar_drain);
@@ -370,11 +413,13 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
                 f2_unpack(f2_add(acc[0], acc[1]), a, c);
                 l += a + c;
             }
+            ok = __all_sync(0xffffffffu, mbar_wait(v_full + i % C::kVSlots, (i / C::kVSlots) & 1, ctl));
+            if (!ok) break;
             // rows of V that are no past key of the segment become zeros
             const int end = s.n - row0;
             if (end < kWinStr) {
                 if (t < kWinStr && t >= end) {
-                    uint8_t* dst = ring + (i % C::kSlots) * C::kSlotBytes + C::kKvTile + t * C::kRowBytes;
+                    uint8_t* dst = sV + (i % C::kVSlots) * C::kKvTile + t * C::kRowBytes;
 #pragma unroll
                     for (int c = 0; c < C::kBoxes; ++c)
 #pragma unroll
