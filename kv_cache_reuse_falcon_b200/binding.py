@@ -195,17 +195,19 @@ def _pool(pool_k: torch.Tensor, pool_v: torch.Tensor, pool_scales=None) -> KVPoo
     """A pool descriptor: bfloat16 tensors, or E4M3 codes (float8_e4m3fn or uint8) with
     pool_scales = (k_scale, v_scale) (default (1, 1))."""
     for name, t in (("pool_k", pool_k), ("pool_v", pool_v)):
-        if (t.dtype != torch.bfloat16 and t.dtype not in _E4M3_TYPES) or t.dim() != 5 or not t.is_contiguous() \
+        kind = t.dtype
+        if (kind is not torch.bfloat16 and kind not in _E4M3_TYPES) or t.dim() != 5 or not t.is_contiguous() \
                 or not t.is_cuda:
             raise ValueError("%s must be a contiguous CUDA tensor [L, S, H, n_cap, D] of bfloat16 or E4M3 codes "
                              "(float8_e4m3fn or uint8)" % name)
-    if pool_k.shape != pool_v.shape or (pool_k.dtype == torch.bfloat16) != (pool_v.dtype == torch.bfloat16):
+    shape = pool_k.shape
+    bf16 = pool_k.dtype is torch.bfloat16
+    if shape != pool_v.shape or bf16 != (kind is torch.bfloat16):
         raise ValueError("pool_k and pool_v differ in shape or element type")
-    L, S, H, n_cap, D = pool_k.shape
-    if pool_k.dtype == torch.bfloat16:
-        return KVPool(pool_k.data_ptr(), pool_v.data_ptr(), L, S, H, n_cap, D, POOL_BF16, 1.0, 1.0)
+    if bf16:
+        return KVPool(pool_k.data_ptr(), pool_v.data_ptr(), *shape, POOL_BF16, 1.0, 1.0)
     ks, vs = (1.0, 1.0) if pool_scales is None else (float(pool_scales[0]), float(pool_scales[1]))
-    return KVPool(pool_k.data_ptr(), pool_v.data_ptr(), L, S, H, n_cap, D, POOL_E4M3, ks, vs)
+    return KVPool(pool_k.data_ptr(), pool_v.data_ptr(), *shape, POOL_E4M3, ks, vs)
 
 
 def _workspace(workspace, nbytes: int, device):
@@ -415,40 +417,65 @@ def status_string(code: int) -> str:
 
 
 # ------------------------------------------------- sliding window and paged pools
+#
+# Serving calls these once per layer and step on small inputs, where the checks below are most of a
+# call: they look at each property of a tensor once.
 
 NO_WINDOW = 2 ** 31 - 1    # window of an unrestricted call
 
 
-def _one_device(first: torch.Tensor, **others):
-    """The device of `first`; every other given tensor must lie on it."""
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError("%s is on %s, expected %s" % (name, t.device, first.device))
-    return first.device
+def _fits(t: torch.Tensor, name: str, dtype: torch.dtype, shape):
+    """A contiguous tensor of this type and shape (that it is on the device, _one_device sees)."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous CUDA %s tensor %s" % (name, dtype, list(shape)))
 
 
-def _call(device: torch.device, stream, f, where: str, *args):
+def _token_rows(t: torch.Tensor, name: str):
+    """The shape of a contiguous bfloat16 tensor [T, H, D]."""
+    if t.dtype is not torch.bfloat16 or t.dim() != 3 or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous CUDA bfloat16 tensor [T, H, D]" % name)
+    return t.shape
+
+
+def _one_device(*tensors) -> int:
+    """The index of the CUDA device that every given tensor (None: not given) lies on."""
+    d = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != d or d < 0:
+            raise ValueError("the tensors must lie on one CUDA device: %s"
+                             % [str(x.device) for x in tensors if x is not None])
+    return d
+
+
+def _call(device: int, stream, f, where: str, *args):
     """f(*args, stream) with `device` current, on `stream` (default: the device's current stream)."""
-    if device.index != torch.cuda.current_device():
+    raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    if device == torch._C._cuda_getDevice():
+        rc = f(*args, raw)
+    else:
         with torch.cuda.device(device):
-            return _call(device, stream, f, where, *args)
-    raw = torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream
-    rc = f(*args, raw)
+            rc = f(*args, raw)
     if rc != UNIPIN_OK:
         raise UnipinError(rc, where)
 
 
 def _page_table(page_table: torch.Tensor, rows: int) -> int:
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != rows \
-            or not page_table.is_contiguous() or not page_table.is_cuda:
+    if page_table.dtype is not torch.int32 or page_table.dim() != 2 or page_table.size(0) != rows \
+            or not page_table.is_contiguous():
         raise ValueError("page_table must be a contiguous CUDA int32 tensor [%d, max_pages]" % rows)
-    return int(page_table.shape[1])
+    return page_table.size(1)
 
 
-def _key_weights(key_weights: Optional[torch.Tensor], pool_k: torch.Tensor):
-    if key_weights is not None and (key_weights.dtype != torch.float32 or key_weights.shape != pool_k.shape[:4]
-                                    or not key_weights.is_contiguous() or not key_weights.is_cuda):
-        raise ValueError("key_weights must be a contiguous CUDA float32 tensor [L, S, H, n_cap]")
+def _batch(t: torch.Tensor, name: str) -> int:
+    """The length of an int32 vector with an entry per request."""
+    if t.dtype is not torch.int32 or t.dim() != 1 or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous CUDA int32 vector" % name)
+    return t.size(0)
+
+
+def _key_weights(key_weights: Optional[torch.Tensor], pool: KVPool):
+    if key_weights is not None:
+        _fits(key_weights, "key_weights", torch.float32, (pool.L, pool.S, pool.H, pool.n_cap))
 
 
 def _window(window: Optional[int], n_sinks: int):
@@ -462,32 +489,34 @@ def _adr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+def _scale(scale: Optional[float], D: int) -> float:
+    return 1.0 / math.sqrt(D) if scale is None else float(scale)
+
+
 def windowed_prefill_attn(q, k, v, cu_seqlens, past_lens, max_seqlen: int, window: Optional[int], n_sinks: int = 0,
                           out=None, out_fp32: bool = True, scale: Optional[float] = None, dev_status=None, stream=None,
                           lse=None):
     """The masked prefill under a sliding window: with pos = i for a past row and pos = n_b for a
     candidate, past keys with pos - j < window (None: all) or j < n_sinks, and a candidate's own key.
     `lse` (fp32 [T, H]) takes the per-row log-sum-exp (base 2) that windowed_prefill_bwd needs."""
-    _tokens(q, "q")
-    T, H, D = q.shape
-    _tokens(k, "k", D)
-    _tokens(v, "v", D)
-    H_kv = _kv_heads(q, k, v)
-    B = past_lens.shape[0]
-    _index(cu_seqlens, "cu_seqlens", B + 1)
-    _index(past_lens, "past_lens", B)
+    T, H, D = _token_rows(q, "q")
+    H_kv = _token_rows(k, "k")[1]
+    _fits(k, "k", torch.bfloat16, (T, H_kv, D))
+    _fits(v, "v", torch.bfloat16, (T, H_kv, D))
+    B = _batch(past_lens, "past_lens")
+    _fits(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,))
     window, n_sinks = _window(window, n_sinks)
+    kind = torch.float32 if out_fp32 else torch.bfloat16
     if out is None:
-        out = torch.empty((T, H, D), dtype=torch.float32 if out_fp32 else torch.bfloat16, device=q.device)
-    elif out.dtype != (torch.float32 if out_fp32 else torch.bfloat16) or out.shape != q.shape or not out.is_contiguous():
-        raise ValueError("out has the wrong dtype or shape")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, H) or not lse.is_contiguous()):
-        raise ValueError("lse must be a contiguous float32 tensor [T, H]")
-    dev = _one_device(q, k=k, v=v, cu_seqlens=cu_seqlens, past_lens=past_lens, out=out, lse=lse, dev_status=dev_status)
+        out = torch.empty((T, H, D), dtype=kind, device=q.device)
+    else:
+        _fits(out, "out", kind, (T, H, D))
+    if lse is not None:
+        _fits(lse, "lse", torch.float32, (T, H))
+    dev = _one_device(q, k, v, cu_seqlens, past_lens, out, lse, dev_status)
     _call(dev, stream, LIB.unipin_windowed_prefill_attn, "unipin_windowed_prefill_attn", q.data_ptr(), k.data_ptr(),
-          v.data_ptr(), out.data_ptr(), int(bool(out_fp32)), _adr(lse), cu_seqlens.data_ptr(), past_lens.data_ptr(),
-          B, H, H_kv, D, int(max_seqlen), T, window, n_sinks, 1.0 / math.sqrt(D) if scale is None else float(scale),
-          _adr(dev_status))
+          v.data_ptr(), out.data_ptr(), 1 if out_fp32 else 0, _adr(lse), cu_seqlens.data_ptr(), past_lens.data_ptr(),
+          B, H, H_kv, D, int(max_seqlen), T, window, n_sinks, _scale(scale, D), _adr(dev_status))
     return out
 
 
@@ -502,36 +531,37 @@ def windowed_prefill_bwd(q, k, v, out, dout, lse, cu_seqlens, past_lens, max_seq
     windowed_prefill_attn for the upstream gradient dout.
 
     `out` is the forward's bf16 output and `lse` the row statistic the forward wrote."""
-    _tokens(q, "q")
-    T, H, D = q.shape
-    for name, t in (("k", k), ("v", v), ("out", out), ("dout", dout)):
-        _tokens(t, name, D)
-    H_kv = _kv_heads(q, k, v)
-    if out.shape != q.shape or dout.shape != q.shape:
-        raise ValueError("out and dout must have the shape of q")
-    if lse.dtype != torch.float32 or lse.shape != (T, H) or not lse.is_contiguous():
-        raise ValueError("lse must be a contiguous float32 tensor [T, H]")
-    B = past_lens.shape[0]
-    _index(cu_seqlens, "cu_seqlens", B + 1)
-    _index(past_lens, "past_lens", B)
+    T, H, D = _token_rows(q, "q")
+    H_kv = _token_rows(k, "k")[1]
+    _fits(k, "k", torch.bfloat16, (T, H_kv, D))
+    _fits(v, "v", torch.bfloat16, (T, H_kv, D))
+    _fits(out, "out", torch.bfloat16, (T, H, D))
+    _fits(dout, "dout", torch.bfloat16, (T, H, D))
+    _fits(lse, "lse", torch.float32, (T, H))
+    B = _batch(past_lens, "past_lens")
+    _fits(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,))
     window, n_sinks = _window(window, n_sinks)
     kind = torch.float32 if grad_fp32 else torch.bfloat16
-    grads = []
-    for g, heads in ((dq, H), (dk, H_kv), (dv, H_kv)):
-        if g is None:
-            g = torch.empty((T, heads, D), dtype=kind, device=q.device)
-        elif g.dtype != kind or tuple(g.shape) != (T, heads, D) or not g.is_contiguous():
-            raise ValueError("gradient outputs must be contiguous %s: dq [T, H, D], dk and dv [T, H_kv, D]" % kind)
-        grads.append(g)
-    ws, ws_bytes = _workspace(workspace, windowed_prefill_bwd_workspace_size(T, H), q.device)
-    dev = _one_device(q, k=k, v=v, out=out, dout=dout, lse=lse, cu_seqlens=cu_seqlens, past_lens=past_lens,
-                      dq=grads[0], dk=grads[1], dv=grads[2], workspace=ws, dev_status=dev_status)
+    device = q.device
+    if dq is None:
+        dq = torch.empty((T, H, D), dtype=kind, device=device)
+    else:
+        _fits(dq, "dq", kind, (T, H, D))
+    if dk is None:
+        dk = torch.empty((T, H_kv, D), dtype=kind, device=device)
+    else:
+        _fits(dk, "dk", kind, (T, H_kv, D))
+    if dv is None:
+        dv = torch.empty((T, H_kv, D), dtype=kind, device=device)
+    else:
+        _fits(dv, "dv", kind, (T, H_kv, D))
+    ws, ws_bytes = _workspace(workspace, windowed_prefill_bwd_workspace_size(T, H), device)
+    dev = _one_device(q, k, v, out, dout, lse, cu_seqlens, past_lens, dq, dk, dv, ws, dev_status)
     _call(dev, stream, LIB.unipin_windowed_prefill_bwd, "unipin_windowed_prefill_bwd", q.data_ptr(), k.data_ptr(),
-          v.data_ptr(), out.data_ptr(), dout.data_ptr(), lse.data_ptr(), grads[0].data_ptr(), grads[1].data_ptr(),
-          grads[2].data_ptr(), int(bool(grad_fp32)), cu_seqlens.data_ptr(), past_lens.data_ptr(), B, H, H_kv, D,
-          int(max_seqlen), T, window, n_sinks, 1.0 / math.sqrt(D) if scale is None else float(scale), _adr(ws),
-          ws_bytes, _adr(dev_status))
-    return tuple(grads)
+          v.data_ptr(), out.data_ptr(), dout.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+          1 if grad_fp32 else 0, cu_seqlens.data_ptr(), past_lens.data_ptr(), B, H, H_kv, D, int(max_seqlen), T,
+          window, n_sinks, _scale(scale, D), _adr(ws), ws_bytes, _adr(dev_status))
+    return dq, dk, dv
 
 
 def paged_pool_write(pool_k, pool_v, layer: int, k, v, cu_seqlens, new_lens, page_table, first_rows, max_new: int,
@@ -539,21 +569,19 @@ def paged_pool_write(pool_k, pool_v, layer: int, k, v, cu_seqlens, new_lens, pag
     """The first new_lens[b] tokens of each segment into rows first_rows[b], first_rows[b] + 1, ... of
     request b's pages (a paged pool [L, S pages, H, rows of a page, D]); their key_weights become 0."""
     pool = _pool(pool_k, pool_v, pool_scales)
-    _tokens(k, "k", pool.D)
-    _tokens(v, "v", pool.D)
-    if k.shape != v.shape or k.shape[1] != pool.H:
-        raise ValueError("k and v must be [T, %d, %d], the pool's heads" % (pool.H, pool.D))
-    B = new_lens.shape[0]
-    _index(cu_seqlens, "cu_seqlens", B + 1)
-    _index(new_lens, "new_lens", B)
-    _index(first_rows, "first_rows", B)
+    T = _token_rows(k, "k")[0]
+    shape = (T, pool.H, pool.D)
+    _fits(k, "k", torch.bfloat16, shape)
+    _fits(v, "v", torch.bfloat16, shape)
+    B = _batch(new_lens, "new_lens")
+    _fits(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,))
+    _fits(first_rows, "first_rows", torch.int32, (B,))
     pages = _page_table(page_table, B)
-    _key_weights(key_weights, pool_k)
-    dev = _one_device(pool_k, pool_v=pool_v, k=k, v=v, cu_seqlens=cu_seqlens, new_lens=new_lens,
-                      page_table=page_table, first_rows=first_rows, key_weights=key_weights, dev_status=dev_status)
+    _key_weights(key_weights, pool)
+    dev = _one_device(pool_k, pool_v, k, v, cu_seqlens, new_lens, page_table, first_rows, key_weights, dev_status)
     _call(dev, stream, LIB.unipin_paged_pool_write, "unipin_paged_pool_write", ctypes.byref(pool), int(layer),
           k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), new_lens.data_ptr(), page_table.data_ptr(), pages,
-          first_rows.data_ptr(), B, int(max_new), k.shape[0], _adr(key_weights), _adr(dev_status))
+          first_rows.data_ptr(), B, int(max_new), T, _adr(key_weights), _adr(dev_status))
 
 
 def paged_decode_workspace_size(pool_k, pool_v, R: int, H: int, max_len: int, weights: bool = False,
@@ -573,40 +601,37 @@ def paged_decode_attn(q, page_table, lens, pool_k, pool_v, layer: int, max_len: 
     """One new token per request ([R, H, D]) over its cached rows 0 .. lens[r]-1: the last `window` rows
     (the token's own among them; None: all) and the first n_sinks, plus its own key and value where they
     are passed and not yet cached.  key_weights collects each row's attention weight."""
-    _tokens(q, "q")
-    R, H, D = q.shape
+    R, H, D = _token_rows(q, "q")
     pool = _pool(pool_k, pool_v, pool_scales)
     if pool.D != D or H % pool.H != 0:
         raise ValueError("q must have the pool's head dim and a multiple of its %d heads" % pool.H)
     if (k_self is None) != (v_self is None):
         raise ValueError("k_self and v_self go together")
     if k_self is not None:
-        for name, t in (("k_self", k_self), ("v_self", v_self)):
-            _tokens(t, name, D)
-            if tuple(t.shape) != (R, pool.H, D):
-                raise ValueError("%s must be [%d, %d, %d]" % (name, R, pool.H, D))
-    _index(lens, "lens", R)
+        shape = (R, pool.H, D)
+        _fits(k_self, "k_self", torch.bfloat16, shape)
+        _fits(v_self, "v_self", torch.bfloat16, shape)
+    _fits(lens, "lens", torch.int32, (R,))
     pages = _page_table(page_table, R)
-    _key_weights(key_weights, pool_k)
+    _key_weights(key_weights, pool)
     window, n_sinks = _window(window, n_sinks)
+    max_len = int(max_len)
+    kind = torch.float32 if out_fp32 else torch.bfloat16
     if out is None:
-        out = torch.empty((R, H, D), dtype=torch.float32 if out_fp32 else torch.bfloat16, device=q.device)
-    elif out.dtype != (torch.float32 if out_fp32 else torch.bfloat16) or out.shape != q.shape \
-            or not out.is_contiguous():
-        raise ValueError("out has the wrong dtype or shape")
+        out = torch.empty((R, H, D), dtype=kind, device=q.device)
+    else:
+        _fits(out, "out", kind, (R, H, D))
+    nbytes = 0
     if isinstance(workspace, str):
         with torch.cuda.device(q.device):
-            nbytes = int(LIB.unipin_paged_decode_workspace_size(ctypes.byref(pool), R, H, int(max_len), window,
-                                                                n_sinks, int(key_weights is not None)))
-        workspace, ws_bytes = _workspace(workspace, nbytes, q.device)
-    else:
-        workspace, ws_bytes = _workspace(workspace, 0, q.device)
-    dev = _one_device(q, k_self=k_self, v_self=v_self, page_table=page_table, lens=lens, pool_k=pool_k,
-                      pool_v=pool_v, key_weights=key_weights, out=out, workspace=workspace, dev_status=dev_status)
+            nbytes = int(LIB.unipin_paged_decode_workspace_size(ctypes.byref(pool), R, H, max_len, window, n_sinks,
+                                                                int(key_weights is not None)))
+    workspace, ws_bytes = _workspace(workspace, nbytes, q.device)
+    dev = _one_device(q, k_self, v_self, page_table, lens, pool_k, pool_v, key_weights, out, workspace, dev_status)
     _call(dev, stream, LIB.unipin_paged_decode_attn, "unipin_paged_decode_attn", q.data_ptr(), _adr(k_self),
-          _adr(v_self), out.data_ptr(), int(bool(out_fp32)), page_table.data_ptr(), pages, lens.data_ptr(), R, H, D,
-          int(max_len), window, n_sinks, 1.0 / math.sqrt(D) if scale is None else float(scale), ctypes.byref(pool),
-          int(layer), _adr(key_weights), _adr(workspace), ws_bytes, _adr(dev_status))
+          _adr(v_self), out.data_ptr(), 1 if out_fp32 else 0, page_table.data_ptr(), pages, lens.data_ptr(), R, H, D,
+          max_len, window, n_sinks, _scale(scale, D), ctypes.byref(pool), int(layer), _adr(key_weights),
+          _adr(workspace), ws_bytes, _adr(dev_status))
     return out
 
 
@@ -618,21 +643,19 @@ def paged_evict(pool_k, pool_v, key_weights, layer: int, page_table, lens, max_l
     pool = _pool(pool_k, pool_v)
     if key_weights is None:
         raise ValueError("key_weights is required")
-    _key_weights(key_weights, pool_k)
-    R = lens.shape[0]
-    _index(lens, "lens", R)
+    _key_weights(key_weights, pool)
+    R = _batch(lens, "lens")
     pages = _page_table(page_table, R)
     budget = int(budget)
     if kept is None:
         kept = torch.empty((R, pool.H, max(budget, 0)), dtype=torch.int32, device=lens.device)
-    elif kept.dtype != torch.int32 or tuple(kept.shape) != (R, pool.H, budget) or not kept.is_contiguous():
-        raise ValueError("kept must be a contiguous int32 tensor [R, H, budget]")
+    else:
+        _fits(kept, "kept", torch.int32, (R, pool.H, budget))
     if new_lens is None:
         new_lens = torch.empty(R, dtype=torch.int32, device=lens.device)
     else:
-        _index(new_lens, "new_lens", R)
-    dev = _one_device(pool_k, pool_v=pool_v, key_weights=key_weights, page_table=page_table, lens=lens, kept=kept,
-                      new_lens=new_lens, dev_status=dev_status)
+        _fits(new_lens, "new_lens", torch.int32, (R,))
+    dev = _one_device(pool_k, pool_v, key_weights, page_table, lens, kept, new_lens, dev_status)
     _call(dev, stream, LIB.unipin_paged_evict, "unipin_paged_evict", ctypes.byref(pool), int(layer),
           key_weights.data_ptr(), page_table.data_ptr(), pages, lens.data_ptr(), R, int(max_len), budget,
           int(n_sinks), int(n_recent), kept.data_ptr(), new_lens.data_ptr(), _adr(dev_status))
