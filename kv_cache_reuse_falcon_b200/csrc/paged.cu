@@ -22,12 +22,12 @@ bool g_paged_ready[kMaxDevices] = {};
 
 constexpr int kSelKeysCap = 48 * 1024;   // keys of the selection's shared-memory copy (192 KB)
 
-template <int D, int kMode, bool kWide>
+template <int D, int kMode, int kNG>
 int set_decode_attr()
 {
-    return cudaFuncSetAttribute(paged_decode_kernel<D, kMode, kWide>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(paged_decode_kernel<D, kMode, kNG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 PgCfg<D, kMode>::kSmemBytes) == cudaSuccess &&
-                   cudaFuncSetAttribute(paged_decode_kernel<D, kMode, kWide>,
+                   cudaFuncSetAttribute(paged_decode_kernel<D, kMode, kNG>,
                                         cudaFuncAttributePreferredSharedMemoryCarveout,
                                         (int)cudaSharedmemCarveoutMaxShared) == cudaSuccess
                ? UNIPIN_OK
@@ -37,12 +37,12 @@ int set_decode_attr()
 template <int D>
 int set_decode_attrs()
 {
-    int rc = set_decode_attr<D, kPgBf16, false>();
-    if (rc == UNIPIN_OK) rc = set_decode_attr<D, kPgBf16, true>();
-    if (rc == UNIPIN_OK) rc = set_decode_attr<D, kPgE4M3Pow2, false>();
-    if (rc == UNIPIN_OK) rc = set_decode_attr<D, kPgE4M3Pow2, true>();
-    if (rc == UNIPIN_OK) rc = set_decode_attr<D, kPgE4M3Any, false>();
-    if (rc == UNIPIN_OK) rc = set_decode_attr<D, kPgE4M3Any, true>();
+    int rc = set_decode_attr<D, kPgBf16, 1>();
+    if (rc == UNIPIN_OK) rc = set_decode_attr<D, kPgBf16, 2>();
+    if (rc == UNIPIN_OK) rc = set_decode_attr<D, kPgE4M3Pow2, 1>();
+    if (rc == UNIPIN_OK) rc = set_decode_attr<D, kPgE4M3Pow2, 2>();
+    if (rc == UNIPIN_OK) rc = set_decode_attr<D, kPgE4M3Any, 1>();
+    if (rc == UNIPIN_OK) rc = set_decode_attr<D, kPgE4M3Any, 2>();
     return rc;
 }
 
@@ -126,13 +126,19 @@ int decode_mode(const unipin_kvpool* pool)
 
 struct DecodePlan {
     int vmax;      // most visible rows of a request
-    int chunk;     // visible rows per block (a multiple of kPgSpan)
-    int nsplit;
-    bool split;    // partials and the join kernel
+    int shares;    // blocks
+    bool whole;    // every row within one block: no join kernel
 };
 
-// Chunks of the visible rows.  Enough blocks to fill the device a few times over, so that ragged
-// lengths balance, and no chunk below four steps of a block, where its start-up outweighs its work.
+int decode_blocks_per_sm(const unipin_kvpool* pool)
+{
+    const int row_bytes = (int)(pool->D * elt_bytes(pool));
+    return row_bytes >= 256 ? PgCfg<128, kPgBf16>::kBlocksPerSm : PgCfg<64, kPgBf16>::kBlocksPerSm;
+}
+
+// One wave of blocks.  Rows stay whole (no partials, no second launch) where they are short: at four
+// units (512 visible rows) a block's sweep takes less time than the join's launch, and without
+// parallelism to gain the join would only add to it.
 DecodePlan decode_plan(const unipin_kvpool* pool, int R, int H, int max_len, int window, int n_sinks, bool weights,
                        int sms)
 {
@@ -141,52 +147,69 @@ DecodePlan decode_plan(const unipin_kvpool* pool, int R, int H, int max_len, int
     if (vmax > max_len) vmax = max_len;
     pl.vmax = (int)vmax;
     const int G = H / pool->H;
-    const long long units = (long long)R * pool->H * ((G + 15) / 16);
-    const long long target = 12ll * sms;
-    long long ns = (target + units - 1) / units;
-    const long long most = (vmax + 4 * kPgSpan - 1) / (4 * kPgSpan);
-    if (ns > most) ns = most;
-    if (ns < 1) ns = 1;
-    long long chunk = (vmax + ns - 1) / ns;
-    chunk = (chunk + kPgSpan - 1) / kPgSpan * kPgSpan;
-    if (chunk < kPgSpan) chunk = kPgSpan;
-    pl.chunk = (int)chunk;
-    pl.nsplit = (int)((vmax + chunk - 1) / chunk);
-    if (pl.nsplit < 1) pl.nsplit = 1;
-    pl.split = pl.nsplit > 1 || weights;
+    const long long pairs = (long long)R * pool->H * ((G + 15) / 16);
+    const long long units = vmax > 0 ? (vmax + kPgUnit - 1) / kPgUnit : 1;
+    pl.whole = !weights && units <= 4;
+    const long long slots = (long long)sms * decode_blocks_per_sm(pool);
+    const long long most = pl.whole ? pairs : pairs * units;
+    pl.shares = (int)(most < slots ? most : slots);
     return pl;
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Workspace: partial O [R * H, nsplit, D], (m, l) [R * H, nsplit, 2], scores [R * H, vmax padded to 4].
-size_t plan_bytes(const DecodePlan& pl, int R, int H, int D, bool weights)
+// Workspace: pieces' O [2 shares, heads, D] and (m, l), the requests' first units [R + 1]; with weights the
+// rows' log sums [R * H] and the scores [R * H, vmax padded to 4].
+struct DecodeSpace {
+    size_t ml, first, lse, scores, bytes;
+};
+
+DecodeSpace decode_space(const DecodePlan& pl, int R, int H, int Hkv, int D, bool weights)
 {
-    if (!pl.split) return 0;
-    const size_t rows = (size_t)R * H;
-    size_t n = align256(rows * pl.nsplit * D * 4) + align256(rows * pl.nsplit * 2 * 4);
-    if (weights) n += align256(rows * ((pl.vmax + 3) / 4 * 4) * 4);
-    return n;
+    DecodeSpace w = {};
+    if (pl.whole) return w;
+    const int G = H / Hkv;
+    const size_t pieces = 2 * (size_t)pl.shares * (G < 16 ? G : 16), rows = (size_t)R * H;
+    w.ml = align256(pieces * D * 4);
+    w.first = w.ml + align256(pieces * 2 * 4);
+    w.lse = w.first + align256(((size_t)R + 1) * 4);
+    w.scores = w.lse + (weights ? align256(rows * 4) : 0);
+    w.bytes = w.scores + (weights ? align256(rows * ((pl.vmax + 3) / 4 * 4) * 4) : 0);
+    return w;
 }
 
 template <int D, int kMode>
-int launch_decode(bool wide, dim3 grid, const PgParams& p, cudaStream_t s)
+int launch_decode(bool wide, const PgParams& p, cudaStream_t s)
 {
     if (wide)
-        paged_decode_kernel<D, kMode, true><<<grid, kPgThreads, PgCfg<D, kMode>::kSmemBytes, s>>>(p);
+        paged_decode_kernel<D, kMode, 2><<<p.shares, kPgThreads, PgCfg<D, kMode>::kSmemBytes, s>>>(p);
     else
-        paged_decode_kernel<D, kMode, false><<<grid, kPgThreads, PgCfg<D, kMode>::kSmemBytes, s>>>(p);
+        paged_decode_kernel<D, kMode, 1><<<p.shares, kPgThreads, PgCfg<D, kMode>::kSmemBytes, s>>>(p);
     return cudaGetLastError() == cudaSuccess ? UNIPIN_OK : UNIPIN_ERR_CUDA;
 }
 
 template <int D>
-int launch_decode_mode(int mode, bool wide, dim3 grid, const PgParams& p, cudaStream_t s)
+int launch_decode_mode(int mode, bool wide, const PgParams& p, cudaStream_t s)
 {
     switch (mode) {
-    case kPgBf16: return launch_decode<D, kPgBf16>(wide, grid, p, s);
-    case kPgE4M3Pow2: return launch_decode<D, kPgE4M3Pow2>(wide, grid, p, s);
-    default: return launch_decode<D, kPgE4M3Any>(wide, grid, p, s);
+    case kPgBf16: return launch_decode<D, kPgBf16>(wide, p, s);
+    case kPgE4M3Pow2: return launch_decode<D, kPgE4M3Pow2>(wide, p, s);
+    default: return launch_decode<D, kPgE4M3Any>(wide, p, s);
     }
+}
+
+// j / d = umulhi(j, mul) >> shift for 0 <= j < 2^31 and d >= 2: with s = ceil(log2 d) and
+// mul = floor(2^(31 + s) / d) + 1 <= 2^32 - 1 the product exceeds 2^(31 + s) j / d by at most
+// j < 2^31 <= 2^(31 + s) / d, too little to reach the next quotient.
+void set_divisor(PgParams* p, int d)
+{
+    p->ps_mul = 0;
+    p->ps_shift = 0;
+    if (d < 2) return;
+    int s = 0;
+    while ((1ll << s) < d) ++s;
+    p->ps_mul = (uint32_t)((1ull << (31 + s)) / (uint64_t)d + 1);
+    p->ps_shift = s - 1;
 }
 
 }  // namespace
@@ -249,8 +272,10 @@ size_t unipin_paged_decode_workspace_size(const unipin_kvpool* pool, int R, int 
         window < 1 || n_sinks < 0)
         return 0;
     const int sms = current_sms() > kNumSmsHint ? current_sms() : kNumSmsHint;
-    return plan_bytes(decode_plan(pool, R, H, max_len, window, n_sinks, with_weights != 0, sms), R, H, pool->D,
-                      with_weights != 0);
+    const bool weights = with_weights != 0;
+    return decode_space(decode_plan(pool, R, H, max_len, window, n_sinks, weights, sms), R, H, pool->H, pool->D,
+                        weights)
+        .bytes;
 }
 
 int unipin_paged_decode_attn(const void* q, const void* k_self, const void* v_self, void* out, int out_fp32,
@@ -271,18 +296,18 @@ int unipin_paged_decode_attn(const void* q, const void* k_self, const void* v_se
     if ((long long)max_len > (long long)max_pages * pool->n_cap) return UNIPIN_ERR_OUT_OF_RANGE;
     if (!aligned16(q) || !aligned16(k_self) || !aligned16(v_self) || !aligned16(out)) return UNIPIN_ERR_MISALIGNED;
     if (workspace && !aligned16(workspace)) return UNIPIN_ERR_MISALIGNED;
-    const int G = H / pool->H;
-    const long long gy = (long long)pool->H * ((G + 15) / 16);
-    if (R > 65535 || gy > 65535) return UNIPIN_ERR_INVALID_ARG;
-    rc = ensure_paged();
-    if (rc != UNIPIN_OK) return rc;
+    const int G = H / pool->H, groups = (G + 15) / 16;
     const bool weights = key_weights != nullptr;
     DecodePlan pl = decode_plan(pool, R, H, max_len, window, n_sinks, weights, current_sms());
-    if (pl.split && (!workspace || workspace_bytes < plan_bytes(pl, R, H, D, weights))) {
+    // rows and units are numbered with 31 bits
+    const long long units = (long long)R * pool->H * groups * ((pl.vmax + kPgUnit - 1) / kPgUnit + 1);
+    if (R > 65535 || max_len > (1 << 30) || units >= (1ll << 31)) return UNIPIN_ERR_INVALID_ARG;
+    rc = ensure_paged();
+    if (rc != UNIPIN_OK) return rc;
+    DecodeSpace w = decode_space(pl, R, H, pool->H, D, weights);
+    if (!pl.whole && (!workspace || workspace_bytes < w.bytes)) {
         if (weights) return UNIPIN_ERR_INVALID_ARG;     // the scores need a place
-        pl.chunk = (pl.vmax + kPgSpan - 1) / kPgSpan * kPgSpan;   // one chunk: slower, same result
-        pl.nsplit = 1;
-        pl.split = false;
+        pl.whole = true;                                // slower where few rows are long, same result
     }
     PgParams p = {};
     p.q = static_cast<const __nv_bfloat16*>(q);
@@ -299,13 +324,16 @@ int unipin_paged_decode_attn(const void* q, const void* k_self, const void* v_se
     p.G = G;
     p.S = pool->S;
     p.ps = pool->n_cap;
+    set_divisor(&p, pool->n_cap);
     p.max_pages = max_pages;
     p.max_len = max_len;
     p.window = window;
     p.n_sinks = n_sinks;
-    p.chunk = pl.chunk;
-    p.nsplit = pl.nsplit;
+    p.heads = G < 16 ? G : 16;
+    p.groups = groups;
     p.vmax = (pl.vmax + 3) / 4 * 4;
+    p.whole = pl.whole ? 1 : 0;
+    p.shares = pl.shares;
     p.out_fp32 = out_fp32 ? 1 : 0;
     const int mode = decode_mode(pool);
     p.sl2_self = scale * kPgLog2e;
@@ -313,31 +341,29 @@ int unipin_paged_decode_attn(const void* q, const void* k_self, const void* v_se
     p.k_scale = pool->k_scale;
     p.v_scale = pool->v_scale;
     p.status = dev_status;
-    if (pl.split) {
+    if (!pl.whole) {
         char* ws = static_cast<char*>(workspace);
-        const size_t rows = (size_t)R * H;
         p.part_o = reinterpret_cast<float*>(ws);
-        ws += align256(rows * pl.nsplit * D * 4);
-        p.part_ml = reinterpret_cast<float*>(ws);
-        ws += align256(rows * pl.nsplit * 2 * 4);
+        p.part_ml = reinterpret_cast<float*>(ws + w.ml);
+        p.first_unit = reinterpret_cast<int*>(ws + w.first);
         if (weights) {
-            p.scores = reinterpret_cast<float*>(ws);
+            p.row_lse = reinterpret_cast<float*>(ws + w.lse);
+            p.scores = reinterpret_cast<float*>(ws + w.scores);
             p.key_weights = layer_weights(pool, key_weights, layer);
         }
     }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const dim3 grid((unsigned)pl.nsplit, (unsigned)gy, (unsigned)R);
     const bool wide = G > 8;
-    if (D == 32) rc = launch_decode_mode<32>(mode, wide, grid, p, s);
-    else if (D == 64) rc = launch_decode_mode<64>(mode, wide, grid, p, s);
-    else rc = launch_decode_mode<128>(mode, wide, grid, p, s);
-    if (rc != UNIPIN_OK || !pl.split) return rc;
+    if (D == 32) rc = launch_decode_mode<32>(mode, wide, p, s);
+    else if (D == 64) rc = launch_decode_mode<64>(mode, wide, p, s);
+    else rc = launch_decode_mode<128>(mode, wide, p, s);
+    if (rc != UNIPIN_OK || pl.whole) return rc;
     const long long nw = weights ? (p.vmax + kPgWeightRows - 1) / kPgWeightRows : 0;
     const dim3 jgrid((unsigned)(H + pool->H * nw), (unsigned)R, 1);
     const size_t jsmem = weights ? (size_t)G * 4 : 0;
-    if (D == 32) return launch_dependent(paged_join_kernel<32>, jgrid, kPgThreads, jsmem, s, p);
-    if (D == 64) return launch_dependent(paged_join_kernel<64>, jgrid, kPgThreads, jsmem, s, p);
-    return launch_dependent(paged_join_kernel<128>, jgrid, kPgThreads, jsmem, s, p);
+    if (D == 32) return launch_dependent(paged_join_kernel<32>, jgrid, 32 * kPgJoinWarps, jsmem, s, p);
+    if (D == 64) return launch_dependent(paged_join_kernel<64>, jgrid, 32 * kPgJoinWarps, jsmem, s, p);
+    return launch_dependent(paged_join_kernel<128>, jgrid, 32 * kPgJoinWarps, jsmem, s, p);
 }
 
 int unipin_paged_evict(const unipin_kvpool* pool, int layer, float* key_weights, const int* page_table,

@@ -15,21 +15,28 @@
 // Bound: memory.  Each visible K and V row is read once for the G query heads
 // that share it: 2 D elements for 4 D G flops.  So the kernel is built around
 // loads in flight, not around the tensor cores:
-//   - a work item is (request, key/value head, 16 query heads of the group,
-//     chunk of visible rows); a warp takes every fourth tile of 16 rows of its
-//     block's chunk on its own, with no barrier in its loop;
-//   - each lane copies with cp.async exactly the bytes its MMA fragments need
-//     into its own slots of a ring of stages and reads them back itself, so the
-//     ring needs no barrier, no swizzle and no padding (lane-contiguous 16-byte
-//     slots), works for any page size, and a page that ends inside a tile costs
-//     nothing;
-//   - S = Q K^T by mma.m16n8k16 with the query heads as M (16, or 8 used) and
-//     eight keys as N.  The sum over d may be taken in any order, so lane (g, t)
-//     takes consecutive elements of key g as its share of the K index and Q is
-//     loaded in the same order: no shuffle, no ldmatrix;
-//   - O += P V the same way: P's fragment is S's accumulator layout; lane (g, t)
-//     holds consecutive elements of the value rows 2t, 2t+1, 2t+8, 2t+9, and a
-//     byte permute pairs two rows per register.
+//   - the work is cut into units of 128 visible rows of one (request, key/value
+//     head, up to 16 query heads of the group); the units of all requests, in
+//     order, go to one wave of blocks in equal contiguous shares, whatever the
+//     requests' lengths.  (One block per chunk of a request left a third of the
+//     time to the blocks' starts and ends.)  A block that holds all of a row's
+//     units finishes the row; the others' pieces are joined by a second kernel;
+//   - a warp takes 16 rows of each of its block's units on its own, through a ring
+//     of stages of its own: no block-wide barrier within a row, and the copies run
+//     on across the ends of rows and requests.  Neighbouring lanes copy (cp.async)
+//     neighbouring 16-byte chunks of a row, so each sector crosses from L2 once;
+//     rows are looked up one by one, so any page size works and a page that ends
+//     inside a tile costs nothing; chunk c of row r lies at c ^ f(r), which keeps
+//     copies and fragment reads free of bank conflicts;
+//   - S^T = K Q^T by mma.m16n8k16 with 16 keys as M and eight query heads as N
+//     (K by ldmatrix);
+//   - O^T += V^T P^T with 16 head-dim elements as M (V by ldmatrix.trans): P^T's
+//     fragment is the transpose of S^T's (movmatrix).  (With the heads as M, half
+//     of each product and of O's registers went to rows 8 .. 15 that eight heads or
+//     fewer do not fill.)
+//   - E4M3 codes come as pairs of codes in a 16-bit element: for K the four codes
+//     of a register are four consecutive d, and Q is read in that order; for V a
+//     transposed register holds two d of two rows, and a byte permute sorts them.
 // mma.sync and not tcgen05: at 16 query rows or fewer per key the tensor work is
 // under a tenth of the tensor cores' rate at the full memory rate, and a TMEM
 // accumulator would put a chain of barriers (load, S, softmax, P, P.V) into
@@ -57,10 +64,10 @@
 
 namespace unipin {
 
-constexpr int kPgWarps = 4;
+constexpr int kPgWarps = 8;
 constexpr int kPgThreads = 32 * kPgWarps;
 constexpr int kPgKeys = 16;                      // rows of a warp's tile
-constexpr int kPgSpan = kPgWarps * kPgKeys;      // rows a block takes per step
+constexpr int kPgUnit = kPgWarps * kPgKeys;      // rows of a unit
 constexpr float kPgLog2e = 1.4426950408889634f;
 constexpr float kPgRescaleLog2 = 8.0f;           // O is rescaled only when a row max grows by > 2^8
 
@@ -70,20 +77,20 @@ template <int D, int kMode>
 struct PgCfg {
     static constexpr int kElt = kMode == kPgBf16 ? 2 : 1;
     static constexpr int kRowBytes = D * kElt;
-    // a lane's share of a K row (a quarter) and of a V row (an eighth), in pieces of at most 16 bytes
-    static constexpr int kKB = kRowBytes / 4 < 16 ? kRowBytes / 4 : 16;
-    static constexpr int kKPieces = kRowBytes / 4 / kKB;
-    static constexpr int kKElems = kKB / kElt;
-    static constexpr int kVB = kRowBytes / 8 < 16 ? kRowBytes / 8 : 16;
-    static constexpr int kVPieces = kRowBytes / 8 / kVB;
-    static constexpr int kVElems = kVB / kElt;
+    static constexpr int kChunks = kRowBytes / 16;          // 16-byte chunks of a row
+    static constexpr int kRowsPerCopy = 32 / kChunks;       // rows that one copy of a warp covers
     static constexpr int kStageBytes = 32 * kRowBytes;      // K and V of 16 rows
-    // Enough bytes in flight per SM for the memory latency (about 64 KB): 2 blocks of 4 warps
-    // at the widest row, more blocks at narrower ones.
-    static constexpr int kStages = kRowBytes >= 256 ? 3 : 4;
+    // Bytes in flight per SM for the memory latency: 8 warps x 2 stages x 8 KB at the widest row (one
+    // block per SM), 16 warps x 2 .. 5 stages x 1 .. 4 KB at narrower ones (two blocks).
+    static constexpr int kStages = kRowBytes >= 128 ? 3 : (kRowBytes == 64 ? 4 : 6);
+    static constexpr int kBlocksPerSm = kRowBytes >= 256 ? 1 : 2;
     static constexpr int kRingBytes = kPgWarps * kStages * kStageBytes;
-    static constexpr int kJoinBytes = kPgWarps * 16 * (D + 2) * 4;   // the warps' O, m, l at the end
-    static constexpr int kSmemBytes = kRingBytes > kJoinBytes ? kRingBytes : kJoinBytes;
+    static constexpr int kRedHeads = kRowBytes == 128 && D == 128 ? 2 : 4;   // heads that the warps join at a time
+    static constexpr int kOffQ = kRingBytes;                           // [16][D] bf16
+    static constexpr int kOffRed = kOffQ + 16 * D * 2;                 // [warp][kRedHeads][D] fp32
+    static constexpr int kOffMl = kOffRed + kPgWarps * kRedHeads * D * 4;   // [warp][16][2] fp32
+    static constexpr int kSmemBytes = kOffMl + kPgWarps * 16 * 2 * 4;
+    static_assert((kSmemBytes + 1024) * kBlocksPerSm <= 228 * 1024, "shared memory budget");
 };
 
 struct PgParams {
@@ -96,12 +103,20 @@ struct PgParams {
     const int* lens;               // [R]
     void* out;                     // [R, H, D]
     float* key_weights;            // the layer's [S, H_kv, ps] or null
-    float* part_o;                 // [R * H, nsplit, D]
-    float* part_ml;                // [R * H, nsplit, 2]: (m in log2 units, l); l = -1: rejected
+    float* part_o;                 // [2 * blocks, heads of a unit, D]: pieces of rows (see PgPlace), or null
+    float* part_ml;                // [2 * blocks, heads of a unit, 2]: (m in log2 units, l); l = -1: rejected
+    int* first_unit;               // [R + 1] first unit of each request (block 0 writes it for the join)
+    float* row_lse;                // [R * H] log2 of a finished row's weight sum; +inf: rejected (key_weights)
     float* scores;                 // [R * H, vmax] log2-unit scores of the visible rows (key_weights)
     int R, H, Hkv, G, S, ps, max_pages, max_len;
+    uint32_t ps_mul;               // j / ps = umulhi(j, ps_mul) >> ps_shift; 0: ps = 1
+    int ps_shift;
     int window, n_sinks;
-    int chunk, nsplit, vmax;
+    int heads;                     // query heads of a unit: min(G, 16)
+    int groups;                    // units' head groups per key/value head
+    int vmax;
+    int whole;                     // shares end at row ends: nothing is joined
+    int shares;                    // blocks of the main kernel
     int out_fp32;
     float sl2;                     // scale * log2(e), times k_scale over power-of-two E4M3 pools
     float sl2_self;                // scale * log2(e)
@@ -129,15 +144,40 @@ __device__ __forceinline__ PgRows pg_rows(const PgParams& p, int r)
     return x;
 }
 
-template <int kBytes>
+// Units of a row with `vis` visible rows (one where there is none: the row is still written).
+__device__ __forceinline__ int pg_units(int vis) { return max((vis + kPgUnit - 1) / kPgUnit, 1); }
+
+__device__ __forceinline__ int pg_page(const PgParams& p, int j)
+{
+    return p.ps_mul ? (int)(__umulhi((uint32_t)j, p.ps_mul) >> p.ps_shift) : j;
+}
+
+// A place in the sequence of units: request r, head group y (key/value head major), unit t of u.
+struct PgPlace {
+    int r, y, t, u;
+    PgRows rows;
+    __device__ void enter(const PgParams& p)
+    {
+        if (r < p.R) {
+            rows = pg_rows(p, r);
+            u = pg_units(rows.vis);
+        }
+    }
+    __device__ void next(const PgParams& p)
+    {
+        if (++t < u) return;
+        t = 0;
+        if (++y < p.Hkv * p.groups) return;
+        y = 0;
+        ++r;
+        enter(p);
+    }
+};
+
+// Sixteen bytes into shared memory, or zeros.
 __device__ __forceinline__ void pg_copy(uint32_t dst, const void* src, bool live)
 {
-    const int n = live ? kBytes : 0;           // 0: the slot is filled with zeros
-    if constexpr (kBytes == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes), "r"(n)
-                     : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
 
 __device__ __forceinline__ void pg_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -148,17 +188,25 @@ __device__ __forceinline__ void pg_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// N bytes of this lane's slot into 32-bit registers.
-template <int kBytes>
-__device__ __forceinline__ void pg_read(uint32_t addr, uint32_t* r)
+// Four 8 x 8 matrices of 16-bit elements, one row address per lane.
+__device__ __forceinline__ void pg_ldmatrix(uint32_t addr, uint32_t (&r)[4])
 {
-    if constexpr (kBytes == 16)
-        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-    else if constexpr (kBytes == 8)
-        asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
-    else
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r[0]) : "r"(addr) : "memory");
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+__device__ __forceinline__ void pg_ldmatrix_trans(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+// Where the 16-byte chunk c of row r of a tile lies (in chunks): eight rows' chunk c, and a row's eight
+// neighbouring chunks, fall into different bank groups.
+template <int kChunks>
+__host__ __device__ constexpr int pg_swizzle(int r, int c)
+{
+    return r * kChunks + (c ^ (kChunks >= 8 ? r & 7 : (kChunks == 4 ? (r >> 1) & 3 : (r >> 2) & 1)));
 }
 
 // D (16 x 8, f32) += A (16 x 16) B (16 x 8); bfloat16 or float16 operands.
@@ -178,31 +226,18 @@ __device__ __forceinline__ void pg_mma(float (&d)[4], uint32_t a0, uint32_t a1, 
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t pg_prmt(uint32_t a, uint32_t b, uint32_t sel)
-{
-    return __byte_perm(a, b, sel);
-}
-
-// Two E4M3 codes (the low two bytes) as float16 pair: exact.
-__device__ __forceinline__ uint32_t pg_half2_from_e4m3(uint32_t codes)
-{
-    uint32_t h2;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)codes));
-    return h2;
-}
-
-// Two E4M3 codes as the bfloat16 pair attention reads: bf16(value * scale).
-__device__ __forceinline__ uint32_t pg_bf2_from_e4m3(uint32_t codes, float scale)
-{
-    const uint32_t h2 = pg_half2_from_e4m3(codes);
-    const __half2 h = *reinterpret_cast<const __half2*>(&h2);
-    return pack_bf16x2(__fmul_rn(__low2float(h), scale), __fmul_rn(__high2float(h), scale));
-}
-
+// Four E4M3 codes as two pairs of operands: float16 (exact), or bf16(value * scale), what attention reads.
 template <int kMode>
-__device__ __forceinline__ uint32_t pg_expand(uint32_t codes, float scale)
+__device__ __forceinline__ void pg_expand(uint32_t codes, float scale, uint32_t& lo, uint32_t& hi)
 {
-    return kMode == kPgE4M3Pow2 ? pg_half2_from_e4m3(codes) : pg_bf2_from_e4m3(codes, scale);
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi) : "r"(codes));
+    if constexpr (kMode == kPgE4M3Any) {
+        const __half2 a = *reinterpret_cast<const __half2*>(&lo), b = *reinterpret_cast<const __half2*>(&hi);
+        lo = pack_bf16x2(__fmul_rn(__low2float(a), scale), __fmul_rn(__high2float(a), scale));
+        hi = pack_bf16x2(__fmul_rn(__low2float(b), scale), __fmul_rn(__high2float(b), scale));
+    }
 }
 
 __device__ __forceinline__ uint32_t pg_pack_p(float lo, float hi, bool half)
@@ -248,16 +283,17 @@ __device__ __forceinline__ float pg_self_score(const PgParams& p, int r, int h, 
 }
 
 // One warp finishes query row (r, h): o (this lane's elements, relative to m) and l of the cached
-// rows, the own key merged in, divided and stored.  A row that sees nothing is zeros.
+// rows, the own key merged in, divided and stored.  A row that sees nothing is zeros.  Returns log2 of
+// the sum of the row's weights.
 template <int D>
-__device__ __forceinline__ void pg_finish_row(const PgParams& p, int r, int h, int lane, float m, float l,
+__device__ __forceinline__ float pg_finish_row(const PgParams& p, int r, int h, int lane, float m, float l,
                                               float (&o)[D / 32])
 {
     constexpr int E = D / 32;
-    float a = 1.f, b = 0.f;
+    float a = 1.f, b = 0.f, mf = m;
     if (p.k_self) {
         const float ss = pg_self_score<D>(p, r, h, lane);
-        const float mf = fmaxf(m, ss);
+        mf = fmaxf(m, ss);
         a = m == -INFINITY ? 0.f : ex2_approx(m - mf);
         b = ss == -INFINITY ? 0.f : ex2_approx(ss - mf);
         if (ss != ss) b = ss;                 // a NaN score makes the row NaN
@@ -273,6 +309,7 @@ __device__ __forceinline__ void pg_finish_row(const PgParams& p, int r, int h, i
         res[e] = x * inv;
     }
     pg_store_row<E>(p.out, p.out_fp32, ((size_t)r * p.H + h) * D + lane * E, res);
+    return mf + log2f(total);                     // -inf where the row sees nothing
 }
 
 template <int D>
@@ -284,55 +321,193 @@ __device__ __forceinline__ void pg_zero_row(const PgParams& p, int r, int h, int
     pg_store_row<D / 32>(p.out, p.out_fp32, ((size_t)r * p.H + h) * D + lane * (D / 32), z);
 }
 
-// Grid (nsplit, H_kv * column groups, R).  kWide: the block's query heads may be more than 8 (rows 8..15
-// of the MMA carry heads too).
-template <int D, int kMode, bool kWide>
-__global__ void __launch_bounds__(kPgThreads) paged_decode_kernel(const PgParams p)
+
+// Transpose of an 8 x 8 matrix of 16-bit elements, two per lane.
+__device__ __forceinline__ uint32_t pg_transpose(uint32_t a)
+{
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+
+struct PgScan {
+    int warp_sum[kPgWarps];
+    int r, first;
+};
+
+// Units of a share: equal shares of all units, the last ones less or none.
+__device__ __forceinline__ int pg_share(int total, int shares) { return (total + shares - 1) / shares; }
+
+// The units [x, x1) of share `b` and the place of unit x, by a scan over all requests' lengths, which
+// every block makes for itself (4 R bytes; unit numbers fit 31 bits, the host sees to it).  With
+// `first_unit` the first unit of every request is written there, and behind them their total.
+__device__ __forceinline__ void pg_find(const PgParams& p, PgScan& sc, int* first_unit, int b, int& x, int& x1,
+                                        PgPlace& at)
+{
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int y_all = p.Hkv * p.groups;
+    const int per = (p.R + kPgThreads - 1) / kPgThreads;
+    const int r0 = min(tid * per, p.R), r1 = min(r0 + per, p.R);   // this thread's requests
+    int sum = 0;
+    for (int r = r0; r < r1; ++r) sum += pg_units(pg_rows(p, r).vis) * y_all;
+    int incl = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += up;
+    }
+    if (lane == 31) sc.warp_sum[warp] = incl;
+    __syncthreads();
+    int base = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kPgWarps; ++w) {
+        if (w < warp) base += sc.warp_sum[w];
+        total += sc.warp_sum[w];
+    }
+    const int share = pg_share(total, p.shares);
+    x = (int)min((long long)b * share, (long long)total);
+    x1 = (int)min((long long)x + share, (long long)total);
+    int first = base + incl - sum;
+    if (first_unit || (first <= x && x < first + sum)) {
+        for (int r = r0; r < r1; ++r) {
+            const int n = pg_units(pg_rows(p, r).vis) * y_all;
+            if (first_unit) first_unit[r] = first;
+            if (first <= x && x < first + n) {
+                sc.r = r;
+                sc.first = first;
+            }
+            first += n;
+        }
+    }
+    if (first_unit && tid == 0) first_unit[p.R] = total;
+    __syncthreads();
+    if (x >= x1) return;
+    at.r = sc.r;
+    at.enter(p);
+    at.y = (x - sc.first) / at.u;
+    at.t = (x - sc.first) - at.y * at.u;
+}
+
+// One wave of blocks, block b: units [b share, (b + 1) share).  kNG: groups of eight query heads (1 or 2).
+template <int D, int kMode, int kNG>
+__global__ void __launch_bounds__(kPgThreads, PgCfg<D, kMode>::kBlocksPerSm) paged_decode_kernel(const PgParams p)
 {
     using C = PgCfg<D, kMode>;
     constexpr bool kHalf = kMode == kPgE4M3Pow2;
-    constexpr int NT = D / 8;                       // n-tiles of O
-    extern __shared__ __align__(16) uint8_t smem[];
+    constexpr int MT = D / 16;                      // k-steps of S^T, m-tiles of O^T
+    extern __shared__ __align__(1024) uint8_t smem[];   // (fragment addresses are formed by xor)
+    __shared__ PgScan scan;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int g = lane / 4, t = lane % 4;
-    const int r = blockIdx.z;
-    const int groups = (p.G + 15) / 16;
-    const int hkv = blockIdx.y / groups;
-    const int cg = blockIdx.y - hkv * groups;
-    const int h0 = hkv * p.G + cg * 16;             // first query head of the block
-    const int nh = min(16, p.G - cg * 16);
-    const PgRows rows = pg_rows(p, r);
-    const bool split = p.part_ml != nullptr;
-    const int v0 = blockIdx.x * p.chunk;
-    if (v0 >= rows.vis && (split || blockIdx.x > 0) && rows.ok) return;   // the join asks for chunks < vis only
-    if (!rows.ok && blockIdx.x > 0) return;
-    const int v1 = min(v0 + p.chunk, rows.vis);
-    bool bad = !rows.ok;
+    PgPlace at;
+    int x, x1;
+    pg_find(p, scan, blockIdx.x == 0 ? p.first_unit : nullptr, blockIdx.x, x, x1, at);
+    // whole rows: from the first that begins in the share to the last that does
+    if (p.whole)
+        for (; x < x1 && at.t != 0; ++x) at.next(p);
+    if (x >= x1) return;
+    const uint32_t ring = smem_u32(smem) + warp * C::kStages * C::kStageBytes;
+    __nv_bfloat16* sQ = reinterpret_cast<__nv_bfloat16*>(smem + C::kOffQ);
+    float* sRed = reinterpret_cast<float*>(smem + C::kOffRed);
+    float* sMl = reinterpret_cast<float*>(smem + C::kOffMl);
+    const uint32_t last = (uint32_t)p.S * p.Hkv * (uint32_t)p.ps;   // rows of the layer (host: fits 32 bits)
 
-    // ---- Q fragments: row g (and g + 8), in the order the K fragments take d
-    constexpr int QP = C::kKElems / 2;              // pairs per K piece
-    uint32_t qa[C::kKPieces][QP], qb[kWide ? C::kKPieces : 1][QP];
-    float fac0 = p.sl2, fac1 = p.sl2;               // score factor of rows g and g + 8
-    {
-        const __nv_bfloat16* q0 = p.q + ((size_t)r * p.H + h0 + g) * D;
-        const __nv_bfloat16* q1 = q0 + 8 * (size_t)D;
+    // ---- the copies, kStages - 1 units ahead of the products
+    PgPlace ld = at;
+    int xl = x;
+    bool ld_end = false;                            // the share's last unit has been asked for
+    uint32_t bad_stages = 0;                        // stages with a page id out of range
+    // lane's row of unit `ld` in the layer's plane, or `last` where there is none
+    auto key_row = [&]() -> uint32_t {
+        const int v = ld.t * kPgUnit + warp * kPgKeys + (lane & 15);
+        if (ld_end || v >= ld.rows.vis) return last;
+        const int j = ld.rows.row(v);
+        const int pg = pg_page(p, j);
+        const int page = __ldg(p.table + (size_t)ld.r * p.max_pages + pg);
+        if (page < 0 || page >= p.S) return 0xffffffffu;
+        return ((uint32_t)page * p.Hkv + ld.y / p.groups) * (uint32_t)p.ps + (uint32_t)(j - pg * p.ps);
+    };
+    auto ld_next = [&]() {
+        if (ld_end) return;
+        ld.next(p);
+        ++xl;
+        ld_end = xl >= x1 && (!p.whole || ld.t == 0);
+    };
+    auto issue = [&](int stage, uint32_t row) {
+        const uint32_t st = ring + stage * C::kStageBytes;
+        const bool bad = __any_sync(0xffffffffu, row == 0xffffffffu);
+        bad_stages = (bad_stages & ~(1u << stage)) | ((uint32_t)bad << stage);
+        const int c = lane % C::kChunks, r0 = lane / C::kChunks;
 #pragma unroll
-        for (int c = 0; c < C::kKPieces; ++c)
+        for (int i = 0; i < kPgKeys / C::kRowsPerCopy; ++i) {
+            const int tr = i * C::kRowsPerCopy + r0;
+            const uint32_t kr = __shfl_sync(0xffffffffu, row, tr);
+            const size_t src = (size_t)(kr < last ? kr : 0u) * C::kRowBytes + c * 16;
+            const uint32_t dst = st + pg_swizzle<C::kChunks>(tr, c) * 16;
+            pg_copy(dst, p.pool_k + src, kr < last);
+            pg_copy(dst + C::kStageBytes / 2, p.pool_v + src, kr < last);
+        }
+    };
+
 #pragma unroll
-            for (int i = 0; i < QP; ++i) {
-                const int d = (c * 4 + t) * C::kKElems + 2 * i;
-                qa[c][i] = g < nh ? *reinterpret_cast<const uint32_t*>(q0 + d) : 0u;
-                if (kWide) qb[c][i] = g + 8 < nh ? *reinterpret_cast<const uint32_t*>(q1 + d) : 0u;
+    for (int i = 0; i < C::kStages - 1; ++i) {
+        issue(i, key_row());
+        pg_commit();
+        ld_next();
+    }
+    uint32_t next_row = key_row();                  // its page lookup overlaps a unit's work
+    ld_next();
+
+    // ---- query rows: this unit's in shared memory, the next row's on the way in a register
+    const int y_all = p.Hkv * p.groups;
+    // thread i's 16 bytes of the query rows of head group y of request r
+    auto q_fetch = [&](int r, int y) -> uint4 {
+        const int hk = y / p.groups, cg = y - hk * p.groups;
+        const int nh = min(p.heads, p.G - cg * 16);
+        const int hh = threadIdx.x / (D / 8), c = threadIdx.x % (D / 8);
+        if (r >= p.R || hh >= nh) return make_uint4(0u, 0u, 0u, 0u);
+        return __ldg(reinterpret_cast<const uint4*>(p.q + ((size_t)r * p.H + hk * p.G + cg * 16 + hh) * D) + c);
+    };
+    if (threadIdx.x < 2 * D) reinterpret_cast<uint4*>(sQ)[threadIdx.x] = q_fetch(at.r, at.y);   // 16 rows x D / 8
+    __syncthreads();
+
+    int stage = 0;
+    while (x < x1) {
+        // ---- a row: units t .. of (r, y) that are this block's
+        const int hk = at.y / p.groups;
+        const int h0 = hk * p.G + (at.y - hk * p.groups) * 16;
+        const int nh = min(p.heads, p.G - (at.y - hk * p.groups) * 16);
+        const int r = at.r, t_first = at.t, units = p.whole ? at.u - at.t : min(at.u - at.t, x1 - x);
+        const PgRows rows = at.rows;
+        const bool all = t_first == 0 && units == at.u;   // else a piece of the row
+        const uint4 q_next = at.y + 1 < y_all ? q_fetch(r, at.y + 1) : q_fetch(r + 1, 0);
+
+        // Q fragments: head g (and g + 8) as N, d in the order of the K fragments
+        uint32_t qf[kNG][MT][2];
+        float fac[kNG][2];                          // score factors of heads 2t, 2t + 1 (+ 8)
+#pragma unroll
+        for (int n = 0; n < kNG; ++n) {
+            const __nv_bfloat16* q0 = sQ + (n * 8 + g) * D;
+#pragma unroll
+            for (int c = 0; c < MT; ++c) {
+                if constexpr (kMode == kPgBf16) {
+                    qf[n][c][0] = *reinterpret_cast<const uint32_t*>(q0 + c * 16 + 2 * t);
+                    qf[n][c][1] = *reinterpret_cast<const uint32_t*>(q0 + c * 16 + 8 + 2 * t);
+                } else {
+                    const uint2 x2 = *reinterpret_cast<const uint2*>(q0 + c * 16 + 4 * t);
+                    qf[n][c][0] = x2.x;
+                    qf[n][c][1] = x2.y;
+                }
             }
-        if constexpr (kHalf) {
-            auto to_half = [&](auto& qq, float& fac) {
+            fac[n][0] = fac[n][1] = p.sl2;
+            if constexpr (kHalf) {
                 float top = 0.f;
 #pragma unroll
-                for (int c = 0; c < C::kKPieces; ++c)
+                for (int c = 0; c < MT; ++c)
 #pragma unroll
-                    for (int i = 0; i < QP; ++i) {
-                        top = fmaxf(top, fabsf(__uint_as_float(qq[c][i] << 16)));
-                        top = fmaxf(top, fabsf(__uint_as_float(qq[c][i] & 0xffff0000u)));
+                    for (int i = 0; i < 2; ++i) {
+                        top = fmaxf(top, fabsf(__uint_as_float(qf[n][c][i] << 16)));
+                        top = fmaxf(top, fabsf(__uint_as_float(qf[n][c][i] & 0xffff0000u)));
                     }
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -341,297 +516,287 @@ __global__ void __launch_bounds__(kPgThreads) paged_decode_kernel(const PgParams
                 e = max(e, -100);                                          // keeps both powers finite
                 const float up = __uint_as_float((uint32_t)(9 - e + 127) << 23);   // 2^(9-e), 9-e in [-118, 109]
 #pragma unroll
-                for (int c = 0; c < C::kKPieces; ++c)
+                for (int c = 0; c < MT; ++c)
 #pragma unroll
-                    for (int i = 0; i < QP; ++i) {
-                        const __half2 h = __floats2half2_rn(__uint_as_float(qq[c][i] << 16) * up,
-                                                            __uint_as_float(qq[c][i] & 0xffff0000u) * up);
-                        qq[c][i] = *reinterpret_cast<const uint32_t*>(&h);
+                    for (int i = 0; i < 2; ++i) {
+                        const __half2 h = __floats2half2_rn(__uint_as_float(qf[n][c][i] << 16) * up,
+                                                            __uint_as_float(qf[n][c][i] & 0xffff0000u) * up);
+                        qf[n][c][i] = *reinterpret_cast<const uint32_t*>(&h);
                     }
-                fac *= __uint_as_float((uint32_t)(e - 9 + 127) << 23);
-            };
-            to_half(qa, fac0);
-            if (kWide) to_half(qb, fac1);
-        }
-    }
-
-    float o[NT][4];
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-
-    const uint32_t ring = smem_u32(smem) + warp * C::kStages * C::kStageBytes;
-    const int ntile = rows.ok && v1 > v0 ? (v1 - v0 + kPgSpan - 1 - warp * kPgKeys) / kPgSpan : 0;   // this warp's tiles
-    const int* table = p.table + (size_t)r * p.max_pages;
-    const uint32_t last = (uint32_t)p.S * p.Hkv * (uint32_t)p.ps;   // rows of the layer (host: fits 32 bits)
-
-    // lane's key of tile i: its row in the layer's plane, or `last` where there is none
-    auto key_row = [&](int i) -> uint32_t {
-        const int v = v0 + i * kPgSpan + warp * kPgKeys + (lane & 15);
-        if (i >= ntile || v >= v1) return last;
-        const int j = rows.row(v);
-        const int pg = j / p.ps;
-        const int page = __ldg(table + pg);
-        if (page < 0 || page >= p.S) {
-            bad = true;
-            return last;
-        }
-        return ((uint32_t)page * p.Hkv + hkv) * (uint32_t)p.ps + (uint32_t)(j - pg * p.ps);
-    };
-    auto issue = [&](int i, uint32_t row) {
-        const uint32_t st = ring + (i % C::kStages) * C::kStageBytes;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {               // K rows g, g + 8
-            const uint32_t kr = __shfl_sync(0xffffffffu, row, g + 8 * x);
-            const uint8_t* src = p.pool_k + (size_t)(kr < last ? kr : 0u) * C::kRowBytes + t * C::kKB;
-#pragma unroll
-            for (int c = 0; c < C::kKPieces; ++c)
-                pg_copy<C::kKB>(st + (x * C::kKPieces + c) * 32 * C::kKB + lane * C::kKB, src + c * 4 * C::kKB,
-                                kr < last);
-        }
-        const uint32_t sv = st + 2 * C::kKPieces * 32 * C::kKB;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {               // V rows 2t, 2t + 1, 2t + 8, 2t + 9
-            const uint32_t vr = __shfl_sync(0xffffffffu, row, 2 * t + (x & 1) + 8 * (x >> 1));
-            const uint8_t* src = p.pool_v + (size_t)(vr < last ? vr : 0u) * C::kRowBytes + g * C::kVB;
-#pragma unroll
-            for (int c = 0; c < C::kVPieces; ++c)
-                pg_copy<C::kVB>(sv + (x * C::kVPieces + c) * 32 * C::kVB + lane * C::kVB, src + c * 8 * C::kVB,
-                                vr < last);
-        }
-    };
-
-#pragma unroll
-    for (int i = 0; i < C::kStages - 1; ++i) {
-        issue(i, key_row(i));
-        pg_commit();
-    }
-    uint32_t next_row = key_row(C::kStages - 1);
-    for (int i = 0; i < ntile; ++i) {
-        pg_wait<C::kStages - 2>();                  // tile i has landed (this lane's own copies)
-        issue(i + C::kStages - 1, next_row);        // into the stage that tile i - 1 has left
-        pg_commit();
-        next_row = key_row(i + C::kStages);         // its page lookup overlaps this tile's work
-        const uint32_t st = ring + (i % C::kStages) * C::kStageBytes;
-        float s[2][4];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            uint32_t kf[C::kKPieces][C::kKB / 4];
-#pragma unroll
-            for (int c = 0; c < C::kKPieces; ++c)
-                pg_read<C::kKB>(st + (x * C::kKPieces + c) * 32 * C::kKB + lane * C::kKB, kf[c]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[x][e] = 0.f;
-#pragma unroll
-            for (int c = 0; c < C::kKPieces; ++c)
-#pragma unroll
-                for (int i2 = 0; i2 < QP; i2 += 2) {
-                    uint32_t b0, b1;
-                    if constexpr (kMode == kPgBf16) {
-                        b0 = kf[c][i2];
-                        b1 = kf[c][i2 + 1];
-                    } else {                        // four codes per register
-                        b0 = pg_expand<kMode>(kf[c][i2 / 2], p.k_scale);
-                        b1 = pg_expand<kMode>(kf[c][i2 / 2] >> 16, p.k_scale);
-                    }
-                    pg_mma<kHalf>(s[x], qa[c][i2], kWide ? qb[c][i2] : 0u, qa[c][i2 + 1], kWide ? qb[c][i2 + 1] : 0u,
-                                  b0, b1);
-                }
-        }
-        const int vt = v0 + i * kPgSpan + warp * kPgKeys;   // visible index of the tile's first key
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            s[x][0] *= fac0;
-            s[x][1] *= fac0;
-            s[x][2] *= fac1;
-            s[x][3] *= fac1;
-        }
-        if (p.scores) {
-            // rows g (and g + 8) of the group's scores, two keys per lane
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int v = vt + 8 * x + 2 * t;
-#pragma unroll
-                for (int half = 0; half < (kWide ? 2 : 1); ++half) {
-                    if (g + 8 * half >= nh) continue;
-                    float* dst = p.scores + ((size_t)r * p.H + h0 + g + 8 * half) * p.vmax + v;
-                    if (v + 1 < v1) *reinterpret_cast<float2*>(dst) = make_float2(s[x][2 * half], s[x][2 * half + 1]);
-                    else if (v < v1) *dst = s[x][2 * half];
-                }
+                const float down = __uint_as_float((uint32_t)(e - 9 + 127) << 23);
+                fac[n][0] *= __shfl_sync(0xffffffffu, down, 8 * t);        // of head 2t: lane (2t, any)
+                fac[n][1] *= __shfl_sync(0xffffffffu, down, 8 * t + 4);
             }
         }
-        if (vt + kPgKeys > v1) {                    // the chunk ends inside the tile
+
+        float o[kNG][MT][4];
+        float m[kNG][2], l[kNG][2];                 // of heads 2t, 2t + 1 (+ 8)
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+        for (int n = 0; n < kNG; ++n) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (vt + 8 * x + 2 * t + (e & 1) >= v1) s[x][e] = -INFINITY;
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
+            m[n][0] = m[n][1] = -INFINITY;
+            l[n][0] = l[n][1] = 0.f;
         }
-        float t0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-        float t1 = kWide ? fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3])) : -INFINITY;
-        if (__any_sync(0xffffffffu, t0 > m0 + kPgRescaleLog2 || t1 > m1 + kPgRescaleLog2)) {
-            t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 1));
-            t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 2));
-            const float n0 = fmaxf(m0, t0);
-            const float c0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - n0);
-            m0 = n0;
-            l0 *= c0;
-            float c1 = 0.f;
-            if (kWide) {
-                t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 1));
-                t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 2));
-                const float n1 = fmaxf(m1, t1);
-                c1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - n1);
-                m1 = n1;
-                l1 *= c1;
-            }
+        bool bad = !rows.ok;
+
+        for (int i = 0; i < units; ++i) {
+            pg_wait<C::kStages - 2>();              // the unit has landed: this lane's copies,
+            __syncwarp();                           // and the other lanes'
+            bad |= (bad_stages >> stage) & 1u;
+            issue(stage == 0 ? C::kStages - 1 : stage - 1, next_row);   // the stage that the unit before has left
+            pg_commit();
+            next_row = key_row();
+            ld_next();
+            const uint32_t st = ring + stage * C::kStageBytes;
+            stage = stage + 1 == C::kStages ? 0 : stage + 1;
+            const int vt = (t_first + i) * kPgUnit + warp * kPgKeys;   // visible index of the tile's first key
+            if (vt >= rows.vis) continue;
+            float s[kNG][4];
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                o[j][0] *= c0;
-                o[j][1] *= c0;
-                if (kWide) {
-                    o[j][2] *= c1;
-                    o[j][3] *= c1;
-                }
-            }
-        }
-        const float u0 = m0 == -INFINITY ? 0.f : m0, u1 = m1 == -INFINITY ? 0.f : m1;
-        uint32_t pa[2], pb[2] = {0u, 0u};
+            for (int n = 0; n < kNG; ++n)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const float e0 = ex2_approx(s[x][0] - u0), e1 = ex2_approx(s[x][1] - u0);
-            l0 += e0 + e1;
-            pa[x] = pg_pack_p(e0, e1, kHalf);
-            if (kWide) {
-                const float e2 = ex2_approx(s[x][2] - u1), e3 = ex2_approx(s[x][3] - u1);
-                l1 += e2 + e3;
-                pb[x] = pg_pack_p(e2, e3, kHalf);
-            }
-        }
-        // ---- O += P V: element j of the lane's share of rows 2t, 2t+1 (b0) and 2t+8, 2t+9 (b1)
-        const uint32_t sv = st + 2 * C::kKPieces * 32 * C::kKB;
-#pragma unroll
-        for (int c = 0; c < C::kVPieces; ++c) {
-            uint32_t vf[4][C::kVB / 4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-                pg_read<C::kVB>(sv + (x * C::kVPieces + c) * 32 * C::kVB + lane * C::kVB, vf[x]);
+                for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+            // K: matrices (rows 0-7, 8-15) x (chunk, next chunk)
+            const int kr = (lane & 7) + (lane & 8), kc = lane >> 4;
+            const uint32_t ka = st + pg_swizzle<C::kChunks>(kr, kc) * 16;
             if constexpr (kMode == kPgBf16) {
 #pragma unroll
-                for (int j = 0; j < C::kVElems; ++j) {
-                    const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
-                    pg_mma<kHalf>(o[c * C::kVElems + j], pa[0], pb[0], pa[1], pb[1],
-                                  pg_prmt(vf[0][j / 2], vf[1][j / 2], sel), pg_prmt(vf[2][j / 2], vf[3][j / 2], sel));
+                for (int c = 0; c < MT; ++c) {
+                    uint32_t a[4];
+                    pg_ldmatrix(ka ^ (c * 32), a);
+#pragma unroll
+                    for (int n = 0; n < kNG; ++n)
+                        pg_mma<kHalf>(s[n], a[0], a[1], a[2], a[3], qf[n][c][0], qf[n][c][1]);
                 }
             } else {
 #pragma unroll
-                for (int j = 0; j < C::kVElems; j += 2) {
-                    // bytes (row a [j], row b [j], row a [j+1], row b [j+1])
-                    const uint32_t sel = (j & 2) ? 0x7362u : 0x5140u;
-                    const uint32_t lo = pg_prmt(vf[0][j / 4], vf[1][j / 4], sel);
-                    const uint32_t hi = pg_prmt(vf[2][j / 4], vf[3][j / 4], sel);
-                    pg_mma<kHalf>(o[c * C::kVElems + j], pa[0], pb[0], pa[1], pb[1],
-                                  pg_expand<kMode>(lo, p.v_scale), pg_expand<kMode>(hi, p.v_scale));
-                    pg_mma<kHalf>(o[c * C::kVElems + j + 1], pa[0], pb[0], pa[1], pb[1],
-                                  pg_expand<kMode>(lo >> 16, p.v_scale), pg_expand<kMode>(hi >> 16, p.v_scale));
+                for (int c = 0; c < MT; c += 2) {
+                    uint32_t a[4];
+                    pg_ldmatrix(ka ^ (c * 16), a);
+#pragma unroll
+                    for (int i2 = 0; i2 < 2; ++i2) {
+                        uint32_t a0, a1, a2, a3;
+                        pg_expand<kMode>(a[2 * i2], p.k_scale, a0, a2);
+                        pg_expand<kMode>(a[2 * i2 + 1], p.k_scale, a1, a3);
+#pragma unroll
+                        for (int n = 0; n < kNG; ++n)
+                            pg_mma<kHalf>(s[n], a0, a1, a2, a3, qf[n][c + i2][0], qf[n][c + i2][1]);
+                    }
+                }
+            }
+            // s[n]: keys g, g, g + 8, g + 8 of heads 2t, 2t + 1, 2t, 2t + 1 (+ 8 n)
+            bool grow = false;
+            float top[kNG][2];
+#pragma unroll
+            for (int n = 0; n < kNG; ++n) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[n][e] *= fac[n][e & 1];
+                if (p.scores) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int hh = n * 8 + 2 * t + (e & 1), v = vt + g + 8 * (e >> 1);
+                        if (hh < nh && v < rows.vis) p.scores[((size_t)r * p.H + h0 + hh) * p.vmax + v] = s[n][e];
+                    }
+                }
+                if (vt + kPgKeys > rows.vis) {      // the row ends inside the tile
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (vt + g + 8 * (e >> 1) >= rows.vis) s[n][e] = -INFINITY;
+                }
+                top[n][0] = fmaxf(s[n][0], s[n][2]);
+                top[n][1] = fmaxf(s[n][1], s[n][3]);
+                grow |= top[n][0] > m[n][0] + kPgRescaleLog2 || top[n][1] > m[n][1] + kPgRescaleLog2;
+            }
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                for (int n = 0; n < kNG; ++n) {
+                    float f[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float x2 = top[n][e];
+                        x2 = fmaxf(x2, __shfl_xor_sync(0xffffffffu, x2, 4));
+                        x2 = fmaxf(x2, __shfl_xor_sync(0xffffffffu, x2, 8));
+                        x2 = fmaxf(x2, __shfl_xor_sync(0xffffffffu, x2, 16));
+                        const float to = fmaxf(m[n][e], x2);
+                        f[e] = m[n][e] == -INFINITY ? 0.f : ex2_approx(m[n][e] - to);
+                        m[n][e] = to;
+                        l[n][e] *= f[e];
+                    }
+#pragma unroll
+                    for (int i2 = 0; i2 < MT; ++i2)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[n][i2][e] *= f[e & 1];
+                }
+            }
+            uint32_t pb[kNG][2];
+#pragma unroll
+            for (int n = 0; n < kNG; ++n) {
+                const float u0 = m[n][0] == -INFINITY ? 0.f : m[n][0], u1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+                const float e0 = ex2_approx(s[n][0] - u0), e1 = ex2_approx(s[n][1] - u1);
+                const float e2 = ex2_approx(s[n][2] - u0), e3 = ex2_approx(s[n][3] - u1);
+                l[n][0] += e0 + e2;
+                l[n][1] += e1 + e3;
+                pb[n][0] = pg_transpose(pg_pack_p(e0, e1, kHalf));
+                pb[n][1] = pg_transpose(pg_pack_p(e2, e3, kHalf));
+            }
+            // ---- O^T += V^T P^T
+            if constexpr (kMode == kPgBf16) {
+                // matrices (rows 0-7) x (chunk, next), then rows 8-15: dims g, g + 8 of a 16
+                const uint32_t va = st + C::kStageBytes / 2 +
+                                    pg_swizzle<C::kChunks>((lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1) * 16;
+#pragma unroll
+                for (int c = 0; c < MT; ++c) {
+                    uint32_t a[4];
+                    pg_ldmatrix_trans(va ^ (c * 32), a);
+#pragma unroll
+                    for (int n = 0; n < kNG; ++n)
+                        pg_mma<kHalf>(o[n][c], a[0], a[1], a[2], a[3], pb[n][0], pb[n][1]);
+                }
+            } else {
+                // as K, transposed: a register has codes 2g, 2g + 1 of a chunk, of rows 2t and 2t + 1
+                const uint32_t va = ka + C::kStageBytes / 2;
+#pragma unroll
+                for (int c = 0; c < MT; c += 2) {
+                    uint32_t a[4];
+                    pg_ldmatrix_trans(va ^ (c * 16), a);
+#pragma unroll
+                    for (int i2 = 0; i2 < 2; ++i2) {
+                        uint32_t a0, a1, a2, a3;
+                        pg_expand<kMode>(__byte_perm(a[2 * i2], 0u, 0x3120u), p.v_scale, a0, a1);
+                        pg_expand<kMode>(__byte_perm(a[2 * i2 + 1], 0u, 0x3120u), p.v_scale, a2, a3);
+#pragma unroll
+                        for (int n = 0; n < kNG; ++n)
+                            pg_mma<kHalf>(o[n][c + i2], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+                    }
                 }
             }
         }
+
+        // ---- the warps' O, m, l joined through shared memory, C::kRedHeads heads at a time
+        constexpr int E = D / 32;
+        [[maybe_unused]] const float vs = kMode == kPgE4M3Pow2 ? p.v_scale : 1.f;
+#pragma unroll
+        for (int n = 0; n < kNG; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float sum = l[n][e];
+                sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+                if (g == 0) {
+                    sMl[(warp * 16 + n * 8 + 2 * t + e) * 2] = m[n][e];
+                    sMl[(warp * 16 + n * 8 + 2 * t + e) * 2 + 1] = sum;
+                }
+            }
+        for (int hr = 0; hr < nh; hr += C::kRedHeads) {
+#pragma unroll
+            for (int n = 0; n < kNG; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int hh = n * 8 + 2 * t + e - hr;
+                    if (hh < 0 || hh >= C::kRedHeads) continue;
+                    float* dst = sRed + (warp * C::kRedHeads + hh) * D;
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) {
+                        if constexpr (kMode == kPgBf16) {
+                            dst[i * 16 + g] = o[n][i][e];
+                            dst[i * 16 + 8 + g] = o[n][i][e + 2];
+                        } else {
+                            *reinterpret_cast<float2*>(dst + i * 16 + 2 * g) =
+                                make_float2(o[n][i][e] * vs, o[n][i][e + 2] * vs);
+                        }
+                    }
+                }
+            bad = __syncthreads_or(bad);
+            if (hr == 0 && threadIdx.x < 2 * D) reinterpret_cast<uint4*>(sQ)[threadIdx.x] = q_next;
+            for (int hh = warp; hh < min(C::kRedHeads, nh - hr); hh += kPgWarps) {
+                const int head = hr + hh;           // within the unit's heads
+                float mm = -INFINITY, ll = 0.f, acc[E];
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll
+                for (int w = 0; w < kPgWarps; ++w) mm = fmaxf(mm, sMl[(w * 16 + head) * 2]);
+#pragma unroll
+                for (int w = 0; w < kPgWarps; ++w) {
+                    const float mw = sMl[(w * 16 + head) * 2];
+                    // a warp without a key contributes nothing; one whose every score is -inf contributes
+                    // nothing either, but a NaN in it must stay
+                    const float f = mw == -INFINITY ? 1.f : ex2_approx(mw - mm);
+                    ll = fmaf(sMl[(w * 16 + head) * 2 + 1], f, ll);
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        acc[e] = fmaf(sRed[(w * C::kRedHeads + hh) * D + lane * E + e], f, acc[e]);
+                }
+                if (!all) {
+                    // a block's first piece, of a row that began before it, goes to slot 2b, its last to 2b + 1
+                    const size_t slot = ((size_t)blockIdx.x * 2 + (t_first == 0 ? 1 : 0)) * p.heads + head;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) p.part_o[slot * D + lane * E + e] = acc[e];
+                    if (lane == 0) {
+                        p.part_ml[slot * 2] = mm;
+                        p.part_ml[slot * 2 + 1] = bad ? -1.f : ll;
+                    }
+                } else {
+                    float lse = INFINITY;
+                    if (bad) pg_zero_row<D>(p, r, h0 + head, lane);
+                    else lse = pg_finish_row<D>(p, r, h0 + head, lane, mm, ll, acc);
+                    if (p.row_lse && lane == 0) p.row_lse[(size_t)r * p.H + h0 + head] = lse;
+                }
+            }
+            __syncthreads();                        // sRed and sMl may be written again
+        }
+        if (bad && threadIdx.x == 0) report(p.status, (int)UNIPIN_ERR_OUT_OF_RANGE);
+        x += units;
+        for (int i = 0; i < units; ++i) at.next(p);
     }
     pg_wait<0>();
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-    if (kWide) {
-        l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-        l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-    }
-
-    // ---- the four warps' O, m, l joined through shared memory
-    bad = __syncthreads_or(bad);                     // every warp has left its ring
-    if (bad && threadIdx.x == 0) report(p.status, (int)UNIPIN_ERR_OUT_OF_RANGE);
-    float* so = reinterpret_cast<float*>(smem);      // [warp][16][D]
-    float* sml = so + kPgWarps * 16 * D;             // [warp][16][2]
-    const float vs = kMode == kPgE4M3Pow2 ? p.v_scale : 1.f;
-#pragma unroll
-    for (int half = 0; half < (kWide ? 2 : 1); ++half) {
-        float* dst = so + (warp * 16 + g + 8 * half) * D;
-#pragma unroll
-        for (int c = 0; c < C::kVPieces; ++c)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-                for (int j = 0; j < C::kVElems; ++j)
-                    dst[(c * 8 + 2 * t + e) * C::kVElems + j] = o[c * C::kVElems + j][2 * half + e] * vs;
-        if (t == 0) {
-            sml[(warp * 16 + g + 8 * half) * 2] = half ? m1 : m0;
-            sml[(warp * 16 + g + 8 * half) * 2 + 1] = half ? l1 : l0;
-        }
-    }
-    __syncthreads();
-    constexpr int E = D / 32;
-    for (int row = warp; row < nh; row += kPgWarps) {
-        const int h = h0 + row;
-        float m = -INFINITY, l = 0.f, acc[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll
-        for (int w = 0; w < kPgWarps; ++w) m = fmaxf(m, sml[(w * 16 + row) * 2]);
-#pragma unroll
-        for (int w = 0; w < kPgWarps; ++w) {
-            const float mw = sml[(w * 16 + row) * 2];
-            const float f = mw == -INFINITY ? 0.f : ex2_approx(mw - m);
-            // a warp without a key contributes nothing; one whose every score is -inf contributes
-            // nothing either, but a NaN in it must stay
-            l = fmaf(sml[(w * 16 + row) * 2 + 1], mw == -INFINITY ? 1.f : f, l);
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                acc[e] = fmaf(so[(w * 16 + row) * D + lane * E + e], mw == -INFINITY ? 1.f : f, acc[e]);
-        }
-        if (split) {
-            const size_t at = ((size_t)r * p.H + h) * p.nsplit + blockIdx.x;
-            float* po = p.part_o + at * D + lane * E;
-#pragma unroll
-            for (int e = 0; e < E; ++e) po[e] = acc[e];
-            if (lane == 0) {
-                p.part_ml[at * 2] = m;
-                p.part_ml[at * 2 + 1] = bad ? -1.f : l;
-            }
-        } else if (bad) {
-            pg_zero_row<D>(p, r, h, lane);
-        } else {
-            pg_finish_row<D>(p, r, h, lane, m, l, acc);
-        }
-    }
 }
 
-// Joins the chunks of each query row, and adds the weights of the cached rows into key_weights.
-// Grid (H + H_kv * weight blocks, R), 128 threads: a block x < H finishes query head x of request r; the
-// others take kPgWeightRows visible rows of one key/value head each.
+// Joins the pieces of each query row, and adds the weights of the cached rows into key_weights.
+// Grid (H + H_kv * weight blocks, R), 128 threads: a block x < H finishes query head x of request r (if it
+// is in pieces); the others take kPgWeightRows visible rows of one key/value head each.
 constexpr int kPgWeightRows = 1024;
+constexpr int kPgJoinWarps = 4;
+
+// The pieces of a query row: those of blocks b0 .. b1 (one block: the row is finished already).
+struct PgPieces {
+    int b0, b1, heads, head;
+    __device__ PgPieces(const PgParams& p, int r, int h, int vis)
+    {
+        const int share = pg_share(p.first_unit[p.R], p.shares);
+        const int hk = h / p.G, rest = h - hk * p.G, u = pg_units(vis);
+        const int start = p.first_unit[r] + (hk * p.groups + rest / 16) * u;
+        b0 = start / share;
+        b1 = (start + u - 1) / share;
+        heads = p.heads;
+        head = rest % 16;
+    }
+    __device__ size_t slot(int b) const { return ((size_t)b * 2 + (b == b0 ? 1 : 0)) * heads + head; }
+};
 
 template <int D>
-__global__ void __launch_bounds__(kPgThreads) paged_join_kernel(const PgParams p)
+__global__ void __launch_bounds__(32 * kPgJoinWarps) paged_join_kernel(const PgParams p)
 {
     constexpr int E = D / 32;
-    __shared__ float so[kPgWarps][D];
-    __shared__ float sml[kPgWarps][2];
+    __shared__ float so[kPgJoinWarps][D];
+    __shared__ float sml[kPgJoinWarps];
     extern __shared__ float s_lse[];                // [G] (weight blocks)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int r = blockIdx.y;
     const PgRows rows = pg_rows(p, r);
-    const int nchunk = (rows.vis + p.chunk - 1) / p.chunk;
-    const bool head_block = blockIdx.x < (unsigned)p.H;
-    if (head_block) {
+    if (blockIdx.x < (unsigned)p.H) {
         const int h = blockIdx.x;
-        const size_t at = ((size_t)r * p.H + h) * p.nsplit;
+        const PgPieces pc(p, r, h, rows.vis);
+        if (pc.b0 == pc.b1) return;
         float m = -INFINITY;
         bool bad = !rows.ok;
-        for (int c = lane; c < nchunk; c += 32) {
-            m = fmaxf(m, p.part_ml[(at + c) * 2]);
-            bad |= p.part_ml[(at + c) * 2 + 1] == -1.f;
+        for (int b = pc.b0 + lane; b <= pc.b1; b += 32) {
+            m = fmaxf(m, p.part_ml[pc.slot(b) * 2]);
+            bad |= p.part_ml[pc.slot(b) * 2 + 1] == -1.f;
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
@@ -643,21 +808,23 @@ __global__ void __launch_bounds__(kPgThreads) paged_join_kernel(const PgParams p
         float l = 0.f, acc[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = 0.f;
-        for (int c = warp; c < nchunk; c += kPgWarps) {
-            const float mc = p.part_ml[(at + c) * 2];
+#pragma unroll 4
+        for (int b = pc.b0 + warp; b <= pc.b1; b += kPgJoinWarps) {
+            const size_t slot = pc.slot(b);
+            const float mc = p.part_ml[slot * 2];
             const float f = mc == -INFINITY ? 1.f : ex2_approx(mc - m);   // -inf: zeros (or NaN), kept
-            l = fmaf(p.part_ml[(at + c) * 2 + 1], f, l);
+            l = fmaf(p.part_ml[slot * 2 + 1], f, l);
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = fmaf(p.part_o[(at + c) * D + lane * E + e], f, acc[e]);
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(p.part_o[slot * D + lane * E + e], f, acc[e]);
         }
 #pragma unroll
         for (int e = 0; e < E; ++e) so[warp][lane * E + e] = acc[e];
-        if (lane == 0) sml[warp][0] = l;
+        if (lane == 0) sml[warp] = l;
         __syncthreads();
         if (warp > 0) return;
 #pragma unroll
-        for (int w = 1; w < kPgWarps; ++w) {
-            l += sml[w][0];
+        for (int w = 1; w < kPgJoinWarps; ++w) {
+            l += sml[w];
 #pragma unroll
             for (int e = 0; e < E; ++e) acc[e] += so[w][lane * E + e];
         }
@@ -671,40 +838,48 @@ __global__ void __launch_bounds__(kPgThreads) paged_join_kernel(const PgParams p
     const int vb = (x - hkv * nw) * kPgWeightRows;
     if (vb >= rows.vis) return;
     bool bad = false;
-    for (int gg = warp; gg < p.G; gg += kPgWarps) {
+    for (int gg = warp; gg < p.G; gg += kPgJoinWarps) {
         const int h = hkv * p.G + gg;
-        const size_t at = ((size_t)r * p.H + h) * p.nsplit;
-        float m = -INFINITY;
-        for (int c = lane; c < nchunk; c += 32) {
-            m = fmaxf(m, p.part_ml[(at + c) * 2]);
-            bad |= p.part_ml[(at + c) * 2 + 1] == -1.f;
-        }
+        const PgPieces pc(p, r, h, rows.vis);
+        float lse;
+        if (pc.b0 == pc.b1) {
+            lse = p.row_lse[(size_t)r * p.H + h];
+            bad |= lse == INFINITY;
+        } else {
+            float m = -INFINITY;
+            for (int b = pc.b0 + lane; b <= pc.b1; b += 32) {
+                m = fmaxf(m, p.part_ml[pc.slot(b) * 2]);
+                bad |= p.part_ml[pc.slot(b) * 2 + 1] == -1.f;
+            }
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-        const float ss = p.k_self ? pg_self_score<D>(p, r, h, lane) : -INFINITY;
-        m = fmaxf(m, ss);
-        float l = 0.f;
-        for (int c = lane; c < nchunk; c += 32) {
-            const float mc = p.part_ml[(at + c) * 2];
-            l = fmaf(p.part_ml[(at + c) * 2 + 1], mc == -INFINITY ? 1.f : ex2_approx(mc - m), l);
-        }
+            for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+            const float ss = p.k_self ? pg_self_score<D>(p, r, h, lane) : -INFINITY;
+            m = fmaxf(m, ss);
+            float l = 0.f;
+            for (int b = pc.b0 + lane; b <= pc.b1; b += 32) {
+                const float mc = p.part_ml[pc.slot(b) * 2];
+                l = fmaf(p.part_ml[pc.slot(b) * 2 + 1], mc == -INFINITY ? 1.f : ex2_approx(mc - m), l);
+            }
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-        if (ss != -INFINITY) l += ex2_approx(ss - m);
-        if (lane == 0) s_lse[gg] = m + log2f(l);    // -inf where the row sees nothing
+            for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+            if (ss != -INFINITY) l += ex2_approx(ss - m);
+            lse = m + log2f(l);                     // -inf where the row sees nothing
+        }
+        if (lane == 0) s_lse[gg] = lse;
     }
     if (__syncthreads_or(bad)) return;
     const int* table = p.table + (size_t)r * p.max_pages;
-    for (int v = vb + threadIdx.x; v < min(vb + kPgWeightRows, rows.vis); v += kPgThreads) {
+    for (int v = vb + threadIdx.x; v < min(vb + kPgWeightRows, rows.vis); v += 32 * kPgJoinWarps) {
         float w = 0.f;
         for (int gg = 0; gg < p.G; ++gg) {
             const float s = p.scores[((size_t)r * p.H + hkv * p.G + gg) * p.vmax + v];
             w += s == -INFINITY ? 0.f : ex2_approx(s - s_lse[gg]);
         }
         const int j = rows.row(v);
-        const int page = __ldg(table + j / p.ps);
-        float* dst = p.key_weights + ((size_t)page * p.Hkv + hkv) * p.ps + j % p.ps;
-        atomicAdd(dst, w);                         // requests may share pages (a common prefix)
+        const int pg = pg_page(p, j);
+        const int page = __ldg(table + pg);
+        atomicAdd(p.key_weights + ((size_t)page * p.Hkv + hkv) * p.ps + (j - pg * p.ps), w);
+        // (atomic: requests may share pages, a common prefix)
     }
 }
 
