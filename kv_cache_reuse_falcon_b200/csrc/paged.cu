@@ -133,7 +133,8 @@ struct DecodePlan {
 int decode_blocks_per_sm(const unipin_kvpool* pool)
 {
     const int row_bytes = (int)(pool->D * elt_bytes(pool));
-    return row_bytes >= 256 ? PgCfg<128, kPgBf16>::kBlocksPerSm : PgCfg<64, kPgBf16>::kBlocksPerSm;
+    if (row_bytes >= 256) return PgCfg<128, kPgBf16>::kBlocksPerSm;
+    return row_bytes == 128 ? PgCfg<64, kPgBf16>::kBlocksPerSm : PgCfg<32, kPgBf16>::kBlocksPerSm;
 }
 
 // One wave of blocks.  Rows stay whole (no partials, no second launch) where they are short: at four

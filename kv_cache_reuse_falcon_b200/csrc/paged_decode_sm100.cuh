@@ -21,7 +21,7 @@
 //     requests' lengths.  (One block per chunk of a request left a third of the
 //     time to the blocks' starts and ends.)  A block that holds all of a row's
 //     units finishes the row; the others' pieces are joined by a second kernel;
-//   - a warp takes 16 rows of each of its block's units on its own, through a ring
+//   - a warp takes 32 rows of each of its block's units on its own, through a ring
 //     of stages of its own: no block-wide barrier within a row, and the copies run
 //     on across the ends of rows and requests.  Neighbouring lanes copy (cp.async)
 //     neighbouring 16-byte chunks of a row, so each sector crosses from L2 once;
@@ -64,9 +64,9 @@
 
 namespace unipin {
 
-constexpr int kPgWarps = 8;
+constexpr int kPgWarps = 4;
 constexpr int kPgThreads = 32 * kPgWarps;
-constexpr int kPgKeys = 16;                      // rows of a warp's tile
+constexpr int kPgKeys = 32;                      // rows of a warp's tile: one per lane
 constexpr int kPgUnit = kPgWarps * kPgKeys;      // rows of a unit
 constexpr float kPgLog2e = 1.4426950408889634f;
 constexpr float kPgRescaleLog2 = 8.0f;           // O is rescaled only when a row max grows by > 2^8
@@ -79,13 +79,13 @@ struct PgCfg {
     static constexpr int kRowBytes = D * kElt;
     static constexpr int kChunks = kRowBytes / 16;          // 16-byte chunks of a row
     static constexpr int kRowsPerCopy = 32 / kChunks;       // rows that one copy of a warp covers
-    static constexpr int kStageBytes = 32 * kRowBytes;      // K and V of 16 rows
-    // Bytes in flight per SM for the memory latency: 8 warps x 2 stages x 8 KB at the widest row (one
-    // block per SM), 16 warps x 2 .. 5 stages x 1 .. 4 KB at narrower ones (two blocks).
-    static constexpr int kStages = kRowBytes >= 128 ? 3 : (kRowBytes == 64 ? 4 : 6);
-    static constexpr int kBlocksPerSm = kRowBytes >= 256 ? 1 : 2;
+    static constexpr int kStageBytes = 2 * kPgKeys * kRowBytes;   // K and V of a tile
+    // Bytes in flight per SM for the memory latency: 128 KB at rows of 64 bytes and more (two of three
+    // stages of 4, 8 or 16 warps), 96 KB below.
+    static constexpr int kStages = kRowBytes >= 64 ? 3 : 4;
+    static constexpr int kBlocksPerSm = kRowBytes >= 256 ? 1 : (kRowBytes == 128 ? 2 : 4);
     static constexpr int kRingBytes = kPgWarps * kStages * kStageBytes;
-    static constexpr int kRedHeads = kRowBytes == 128 && D == 128 ? 2 : 4;   // heads that the warps join at a time
+    static constexpr int kRedHeads = 4;                                // heads that the warps join at a time
     static constexpr int kOffQ = kRingBytes;                           // [16][D] bf16
     static constexpr int kOffRed = kOffQ + 16 * D * 2;                 // [warp][kRedHeads][D] fp32
     static constexpr int kOffMl = kOffRed + kPgWarps * kRedHeads * D * 4;   // [warp][16][2] fp32
@@ -152,9 +152,9 @@ __device__ __forceinline__ int pg_page(const PgParams& p, int j)
     return p.ps_mul ? (int)(__umulhi((uint32_t)j, p.ps_mul) >> p.ps_shift) : j;
 }
 
-// A place in the sequence of units: request r, head group y (key/value head major), unit t of u.
+// A place in the sequence of units: request r, key/value head hk, head group cg, unit t of u.
 struct PgPlace {
-    int r, y, t, u;
+    int r, hk, cg, t, u;
     PgRows rows;
     __device__ void enter(const PgParams& p)
     {
@@ -163,14 +163,20 @@ struct PgPlace {
             u = pg_units(rows.vis);
         }
     }
-    __device__ void next(const PgParams& p)
+    // the first unit of the next row
+    __device__ void next_row(const PgParams& p)
     {
-        if (++t < u) return;
         t = 0;
-        if (++y < p.Hkv * p.groups) return;
-        y = 0;
+        if (++cg < p.groups) return;
+        cg = 0;
+        if (++hk < p.Hkv) return;
+        hk = 0;
         ++r;
         enter(p);
+    }
+    __device__ void next(const PgParams& p)
+    {
+        if (++t == u) next_row(p);
     }
 };
 
@@ -178,6 +184,11 @@ struct PgPlace {
 __device__ __forceinline__ void pg_copy(uint32_t dst, const void* src, bool live)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+
+__device__ __forceinline__ void pg_copy(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
 __device__ __forceinline__ void pg_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -384,8 +395,10 @@ __device__ __forceinline__ void pg_find(const PgParams& p, PgScan& sc, int* firs
     if (x >= x1) return;
     at.r = sc.r;
     at.enter(p);
-    at.y = (x - sc.first) / at.u;
-    at.t = (x - sc.first) - at.y * at.u;
+    const int y = (x - sc.first) / at.u;
+    at.hk = y / p.groups;
+    at.cg = y - at.hk * p.groups;
+    at.t = (x - sc.first) - y * at.u;
 }
 
 // One wave of blocks, block b: units [b share, (b + 1) share).  kNG: groups of eight query heads (1 or 2).
@@ -410,77 +423,99 @@ __global__ void __launch_bounds__(kPgThreads, PgCfg<D, kMode>::kBlocksPerSm) pag
     __nv_bfloat16* sQ = reinterpret_cast<__nv_bfloat16*>(smem + C::kOffQ);
     float* sRed = reinterpret_cast<float*>(smem + C::kOffRed);
     float* sMl = reinterpret_cast<float*>(smem + C::kOffMl);
-    const uint32_t last = (uint32_t)p.S * p.Hkv * (uint32_t)p.ps;   // rows of the layer (host: fits 32 bits)
 
     // ---- the copies, kStages - 1 units ahead of the products
     PgPlace ld = at;
     int xl = x;
     bool ld_end = false;                            // the share's last unit has been asked for
     uint32_t bad_stages = 0;                        // stages with a page id out of range
-    // lane's row of unit `ld` in the layer's plane, or `last` where there is none
-    auto key_row = [&]() -> uint32_t {
-        const int v = ld.t * kPgUnit + warp * kPgKeys + (lane & 15);
-        if (ld_end || v >= ld.rows.vis) return last;
-        const int j = ld.rows.row(v);
-        const int pg = pg_page(p, j);
-        const int page = __ldg(p.table + (size_t)ld.r * p.max_pages + pg);
-        if (page < 0 || page >= p.S) return 0xffffffffu;
-        return ((uint32_t)page * p.Hkv + ld.y / p.groups) * (uint32_t)p.ps + (uint32_t)(j - pg * p.ps);
+    // a tile's rows on their way to `issue`: this lane's row in the layer's plane
+    uint32_t row = 0;
+    bool row_live = false, row_bad = false;
+    auto look_up = [&]() {
+        const int v = ld.t * kPgUnit + warp * kPgKeys + lane;
+        row = 0;
+        row_live = !ld_end && v < ld.rows.vis;
+        row_bad = false;
+        if (row_live) {
+            const int j = ld.rows.row(v);
+            const int pg = pg_page(p, j);
+            const int page = __ldg(p.table + (size_t)ld.r * p.max_pages + pg);
+            row_bad = page < 0 || page >= p.S;
+            if (row_bad) row_live = false;
+            else row = ((uint32_t)page * p.Hkv + ld.hk) * (uint32_t)p.ps + (uint32_t)(j - pg * p.ps);
+        }
+        if (!ld_end) {
+            ld.next(p);
+            ++xl;
+            ld_end = xl >= x1 && (!p.whole || ld.t == 0);
+        }
     };
-    auto ld_next = [&]() {
-        if (ld_end) return;
-        ld.next(p);
-        ++xl;
-        ld_end = xl >= x1 && (!p.whole || ld.t == 0);
-    };
-    auto issue = [&](int stage, uint32_t row) {
+    const int cc = lane % C::kChunks, cr = lane / C::kChunks;   // the chunk of the row that this lane copies
+    const uint8_t* src_k = p.pool_k + cc * 16;
+    const uint8_t* src_v = p.pool_v + cc * 16;
+    auto issue = [&](int stage) {
         const uint32_t st = ring + stage * C::kStageBytes;
-        const bool bad = __any_sync(0xffffffffu, row == 0xffffffffu);
+        const uint32_t live = __ballot_sync(0xffffffffu, row_live);
+        const bool bad = __any_sync(0xffffffffu, row_bad);
         bad_stages = (bad_stages & ~(1u << stage)) | ((uint32_t)bad << stage);
-        const int c = lane % C::kChunks, r0 = lane / C::kChunks;
 #pragma unroll
         for (int i = 0; i < kPgKeys / C::kRowsPerCopy; ++i) {
-            const int tr = i * C::kRowsPerCopy + r0;
-            const uint32_t kr = __shfl_sync(0xffffffffu, row, tr);
-            const size_t src = (size_t)(kr < last ? kr : 0u) * C::kRowBytes + c * 16;
-            const uint32_t dst = st + pg_swizzle<C::kChunks>(tr, c) * 16;
-            pg_copy(dst, p.pool_k + src, kr < last);
-            pg_copy(dst + C::kStageBytes / 2, p.pool_v + src, kr < last);
+            const int tr = i * C::kRowsPerCopy + cr;
+            const uint64_t at_row = (uint64_t)__shfl_sync(0xffffffffu, row, tr) * C::kRowBytes;
+            const uint32_t dst = st + pg_swizzle<C::kChunks>(tr, cc) * 16;
+            if (live == 0xffffffffu) {
+                pg_copy(dst, src_k + at_row);
+                pg_copy(dst + C::kStageBytes / 2, src_v + at_row);
+            } else {
+                pg_copy(dst, src_k + at_row, (live >> tr) & 1u);
+                pg_copy(dst + C::kStageBytes / 2, src_v + at_row, (live >> tr) & 1u);
+            }
         }
     };
 
+    look_up();
 #pragma unroll
     for (int i = 0; i < C::kStages - 1; ++i) {
-        issue(i, key_row());
+        issue(i);
         pg_commit();
-        ld_next();
+        look_up();                                  // (the next one's: its page lookup overlaps a unit's work)
     }
-    uint32_t next_row = key_row();                  // its page lookup overlaps a unit's work
-    ld_next();
 
     // ---- query rows: this unit's in shared memory, the next row's on the way in a register
-    const int y_all = p.Hkv * p.groups;
-    // thread i's 16 bytes of the query rows of head group y of request r
-    auto q_fetch = [&](int r, int y) -> uint4 {
-        const int hk = y / p.groups, cg = y - hk * p.groups;
+    constexpr int kQVecs = (2 * D + kPgThreads - 1) / kPgThreads;   // 16 rows x D / 8 vectors
+    // this thread's vectors of the query rows of a place
+    auto q_fetch = [&](int r, int hk, int cg, uint4 (&v)[kQVecs]) {
         const int nh = min(p.heads, p.G - cg * 16);
-        const int hh = threadIdx.x / (D / 8), c = threadIdx.x % (D / 8);
-        if (r >= p.R || hh >= nh) return make_uint4(0u, 0u, 0u, 0u);
-        return __ldg(reinterpret_cast<const uint4*>(p.q + ((size_t)r * p.H + hk * p.G + cg * 16 + hh) * D) + c);
+#pragma unroll
+        for (int i = 0; i < kQVecs; ++i) {
+            const int hh = (threadIdx.x + i * kPgThreads) / (D / 8), c = (threadIdx.x + i * kPgThreads) % (D / 8);
+            v[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < p.R && hh < nh)
+                v[i] = __ldg(reinterpret_cast<const uint4*>(p.q + ((size_t)r * p.H + hk * p.G + cg * 16 + hh) * D) + c);
+        }
     };
-    if (threadIdx.x < 2 * D) reinterpret_cast<uint4*>(sQ)[threadIdx.x] = q_fetch(at.r, at.y);   // 16 rows x D / 8
+    auto q_store = [&](const uint4 (&v)[kQVecs]) {
+#pragma unroll
+        for (int i = 0; i < kQVecs; ++i)
+            if (threadIdx.x + i * kPgThreads < 2 * D) reinterpret_cast<uint4*>(sQ)[threadIdx.x + i * kPgThreads] = v[i];
+    };
+    uint4 q_next[kQVecs];
+    q_fetch(at.r, at.hk, at.cg, q_next);
+    q_store(q_next);
     __syncthreads();
 
     int stage = 0;
     while (x < x1) {
         // ---- a row: units t .. of (r, y) that are this block's
-        const int hk = at.y / p.groups;
-        const int h0 = hk * p.G + (at.y - hk * p.groups) * 16;
-        const int nh = min(p.heads, p.G - (at.y - hk * p.groups) * 16);
+        const int h0 = at.hk * p.G + at.cg * 16;
+        const int nh = min(p.heads, p.G - at.cg * 16);
         const int r = at.r, t_first = at.t, units = p.whole ? at.u - at.t : min(at.u - at.t, x1 - x);
         const PgRows rows = at.rows;
         const bool all = t_first == 0 && units == at.u;   // else a piece of the row
-        const uint4 q_next = at.y + 1 < y_all ? q_fetch(r, at.y + 1) : q_fetch(r + 1, 0);
+        x += units;
+        at.next_row(p);                             // (a share that ends inside a row ends with it)
+        q_fetch(at.r, at.hk, at.cg, q_next);
 
         // Q fragments: head g (and g + 8) as N, d in the order of the K fragments
         uint32_t qf[kNG][MT][2];
@@ -546,69 +581,84 @@ __global__ void __launch_bounds__(kPgThreads, PgCfg<D, kMode>::kBlocksPerSm) pag
             pg_wait<C::kStages - 2>();              // the unit has landed: this lane's copies,
             __syncwarp();                           // and the other lanes'
             bad |= (bad_stages >> stage) & 1u;
-            issue(stage == 0 ? C::kStages - 1 : stage - 1, next_row);   // the stage that the unit before has left
+            issue(stage == 0 ? C::kStages - 1 : stage - 1);   // the stage that the unit before has left
             pg_commit();
-            next_row = key_row();
-            ld_next();
+            look_up();
             const uint32_t st = ring + stage * C::kStageBytes;
             stage = stage + 1 == C::kStages ? 0 : stage + 1;
             const int vt = (t_first + i) * kPgUnit + warp * kPgKeys;   // visible index of the tile's first key
             if (vt >= rows.vis) continue;
-            float s[kNG][4];
+            constexpr int KT = kPgKeys / 16;        // m-tiles of S^T, k-steps of O^T
+            float s[kNG][KT][4];
 #pragma unroll
             for (int n = 0; n < kNG; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+                for (int k = 0; k < KT; ++k)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[n][k][e] = 0.f;
             // K: matrices (rows 0-7, 8-15) x (chunk, next chunk)
-            const int kr = (lane & 7) + (lane & 8), kc = lane >> 4;
-            const uint32_t ka = st + pg_swizzle<C::kChunks>(kr, kc) * 16;
-            if constexpr (kMode == kPgBf16) {
+            const uint32_t ka = st + pg_swizzle<C::kChunks>((lane & 7) + (lane & 8), lane >> 4) * 16;
 #pragma unroll
-                for (int c = 0; c < MT; ++c) {
-                    uint32_t a[4];
-                    pg_ldmatrix(ka ^ (c * 32), a);
+            for (int k = 0; k < KT; ++k) {
+                const uint32_t kk = ka + k * 16 * C::kRowBytes;
+                if constexpr (kMode == kPgBf16) {
 #pragma unroll
-                    for (int n = 0; n < kNG; ++n)
-                        pg_mma<kHalf>(s[n], a[0], a[1], a[2], a[3], qf[n][c][0], qf[n][c][1]);
-                }
-            } else {
-#pragma unroll
-                for (int c = 0; c < MT; c += 2) {
-                    uint32_t a[4];
-                    pg_ldmatrix(ka ^ (c * 16), a);
-#pragma unroll
-                    for (int i2 = 0; i2 < 2; ++i2) {
-                        uint32_t a0, a1, a2, a3;
-                        pg_expand<kMode>(a[2 * i2], p.k_scale, a0, a2);
-                        pg_expand<kMode>(a[2 * i2 + 1], p.k_scale, a1, a3);
+                    for (int c = 0; c < MT; ++c) {
+                        uint32_t a[4];
+                        pg_ldmatrix(kk ^ (c * 32), a);
 #pragma unroll
                         for (int n = 0; n < kNG; ++n)
-                            pg_mma<kHalf>(s[n], a0, a1, a2, a3, qf[n][c + i2][0], qf[n][c + i2][1]);
+                            pg_mma<kHalf>(s[n][k], a[0], a[1], a[2], a[3], qf[n][c][0], qf[n][c][1]);
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < MT; c += 2) {
+                        uint32_t a[4];
+                        pg_ldmatrix(kk ^ (c * 16), a);
+#pragma unroll
+                        for (int i2 = 0; i2 < 2; ++i2) {
+                            uint32_t a0, a1, a2, a3;
+                            pg_expand<kMode>(a[2 * i2], p.k_scale, a0, a2);
+                            pg_expand<kMode>(a[2 * i2 + 1], p.k_scale, a1, a3);
+#pragma unroll
+                            for (int n = 0; n < kNG; ++n)
+                                pg_mma<kHalf>(s[n][k], a0, a1, a2, a3, qf[n][c + i2][0], qf[n][c + i2][1]);
+                        }
                     }
                 }
             }
-            // s[n]: keys g, g, g + 8, g + 8 of heads 2t, 2t + 1, 2t, 2t + 1 (+ 8 n)
+            // s[n][k]: keys 16k + (g, g, g + 8, g + 8) of heads 2t, 2t + 1, 2t, 2t + 1 (+ 8 n)
             bool grow = false;
             float top[kNG][2];
 #pragma unroll
             for (int n = 0; n < kNG; ++n) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[n][e] *= fac[n][e & 1];
+                for (int k = 0; k < KT; ++k)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[n][k][e] *= fac[n][e & 1];
                 if (p.scores) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int hh = n * 8 + 2 * t + (e & 1), v = vt + g + 8 * (e >> 1);
-                        if (hh < nh && v < rows.vis) p.scores[((size_t)r * p.H + h0 + hh) * p.vmax + v] = s[n][e];
-                    }
+                    for (int k = 0; k < KT; ++k)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int hh = n * 8 + 2 * t + (e & 1), v = vt + k * 16 + g + 8 * (e >> 1);
+                            if (hh < nh && v < rows.vis) p.scores[((size_t)r * p.H + h0 + hh) * p.vmax + v] = s[n][k][e];
+                        }
                 }
                 if (vt + kPgKeys > rows.vis) {      // the row ends inside the tile
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (vt + g + 8 * (e >> 1) >= rows.vis) s[n][e] = -INFINITY;
+                    for (int k = 0; k < KT; ++k)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (vt + k * 16 + g + 8 * (e >> 1) >= rows.vis) s[n][k][e] = -INFINITY;
                 }
-                top[n][0] = fmaxf(s[n][0], s[n][2]);
-                top[n][1] = fmaxf(s[n][1], s[n][3]);
-                grow |= top[n][0] > m[n][0] + kPgRescaleLog2 || top[n][1] > m[n][1] + kPgRescaleLog2;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    top[n][e] = fmaxf(s[n][0][e], s[n][0][e + 2]);
+#pragma unroll
+                    for (int k = 1; k < KT; ++k) top[n][e] = max3f(top[n][e], s[n][k][e], s[n][k][e + 2]);
+                    grow |= top[n][e] > m[n][e] + kPgRescaleLog2;
+                }
             }
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -631,16 +681,19 @@ __global__ void __launch_bounds__(kPgThreads, PgCfg<D, kMode>::kBlocksPerSm) pag
                         for (int e = 0; e < 4; ++e) o[n][i2][e] *= f[e & 1];
                 }
             }
-            uint32_t pb[kNG][2];
+            uint32_t pb[kNG][KT][2];
 #pragma unroll
             for (int n = 0; n < kNG; ++n) {
                 const float u0 = m[n][0] == -INFINITY ? 0.f : m[n][0], u1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
-                const float e0 = ex2_approx(s[n][0] - u0), e1 = ex2_approx(s[n][1] - u1);
-                const float e2 = ex2_approx(s[n][2] - u0), e3 = ex2_approx(s[n][3] - u1);
-                l[n][0] += e0 + e2;
-                l[n][1] += e1 + e3;
-                pb[n][0] = pg_transpose(pg_pack_p(e0, e1, kHalf));
-                pb[n][1] = pg_transpose(pg_pack_p(e2, e3, kHalf));
+#pragma unroll
+                for (int k = 0; k < KT; ++k) {
+                    const float e0 = ex2_approx(s[n][k][0] - u0), e1 = ex2_approx(s[n][k][1] - u1);
+                    const float e2 = ex2_approx(s[n][k][2] - u0), e3 = ex2_approx(s[n][k][3] - u1);
+                    l[n][0] += e0 + e2;
+                    l[n][1] += e1 + e3;
+                    pb[n][k][0] = pg_transpose(pg_pack_p(e0, e1, kHalf));
+                    pb[n][k][1] = pg_transpose(pg_pack_p(e2, e3, kHalf));
+                }
             }
             // ---- O^T += V^T P^T
             if constexpr (kMode == kPgBf16) {
@@ -648,30 +701,34 @@ __global__ void __launch_bounds__(kPgThreads, PgCfg<D, kMode>::kBlocksPerSm) pag
                 const uint32_t va = st + C::kStageBytes / 2 +
                                     pg_swizzle<C::kChunks>((lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1) * 16;
 #pragma unroll
-                for (int c = 0; c < MT; ++c) {
-                    uint32_t a[4];
-                    pg_ldmatrix_trans(va ^ (c * 32), a);
+                for (int k = 0; k < KT; ++k)
 #pragma unroll
-                    for (int n = 0; n < kNG; ++n)
-                        pg_mma<kHalf>(o[n][c], a[0], a[1], a[2], a[3], pb[n][0], pb[n][1]);
-                }
+                    for (int c = 0; c < MT; ++c) {
+                        uint32_t a[4];
+                        pg_ldmatrix_trans((va + k * 16 * C::kRowBytes) ^ (c * 32), a);
+#pragma unroll
+                        for (int n = 0; n < kNG; ++n)
+                            pg_mma<kHalf>(o[n][c], a[0], a[1], a[2], a[3], pb[n][k][0], pb[n][k][1]);
+                    }
             } else {
                 // as K, transposed: a register has codes 2g, 2g + 1 of a chunk, of rows 2t and 2t + 1
                 const uint32_t va = ka + C::kStageBytes / 2;
 #pragma unroll
-                for (int c = 0; c < MT; c += 2) {
-                    uint32_t a[4];
-                    pg_ldmatrix_trans(va ^ (c * 16), a);
+                for (int k = 0; k < KT; ++k)
 #pragma unroll
-                    for (int i2 = 0; i2 < 2; ++i2) {
-                        uint32_t a0, a1, a2, a3;
-                        pg_expand<kMode>(__byte_perm(a[2 * i2], 0u, 0x3120u), p.v_scale, a0, a1);
-                        pg_expand<kMode>(__byte_perm(a[2 * i2 + 1], 0u, 0x3120u), p.v_scale, a2, a3);
+                    for (int c = 0; c < MT; c += 2) {
+                        uint32_t a[4];
+                        pg_ldmatrix_trans((va + k * 16 * C::kRowBytes) ^ (c * 16), a);
 #pragma unroll
-                        for (int n = 0; n < kNG; ++n)
-                            pg_mma<kHalf>(o[n][c + i2], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+                        for (int i2 = 0; i2 < 2; ++i2) {
+                            uint32_t a0, a1, a2, a3;
+                            pg_expand<kMode>(__byte_perm(a[2 * i2], 0u, 0x3120u), p.v_scale, a0, a1);
+                            pg_expand<kMode>(__byte_perm(a[2 * i2 + 1], 0u, 0x3120u), p.v_scale, a2, a3);
+#pragma unroll
+                            for (int n = 0; n < kNG; ++n)
+                                pg_mma<kHalf>(o[n][c + i2], a0, a1, a2, a3, pb[n][k][0], pb[n][k][1]);
+                        }
                     }
-                }
             }
         }
 
@@ -711,7 +768,7 @@ __global__ void __launch_bounds__(kPgThreads, PgCfg<D, kMode>::kBlocksPerSm) pag
                     }
                 }
             bad = __syncthreads_or(bad);
-            if (hr == 0 && threadIdx.x < 2 * D) reinterpret_cast<uint4*>(sQ)[threadIdx.x] = q_next;
+            if (hr == 0) q_store(q_next);
             for (int hh = warp; hh < min(C::kRedHeads, nh - hr); hh += kPgWarps) {
                 const int head = hr + hh;           // within the unit's heads
                 float mm = -INFINITY, ll = 0.f, acc[E];
@@ -749,8 +806,6 @@ __global__ void __launch_bounds__(kPgThreads, PgCfg<D, kMode>::kBlocksPerSm) pag
             __syncthreads();                        // sRed and sMl may be written again
         }
         if (bad && threadIdx.x == 0) report(p.status, (int)UNIPIN_ERR_OUT_OF_RANGE);
-        x += units;
-        for (int i = 0; i < units; ++i) at.next(p);
     }
     pg_wait<0>();
 }
