@@ -130,15 +130,20 @@ struct DecodePlan {
     bool whole;    // every row within one block: no join kernel
 };
 
-int decode_blocks_per_sm(const unipin_kvpool* pool)
+struct DecodeShape {
+    int blocks_per_sm, unit;
+};
+
+DecodeShape decode_shape(const unipin_kvpool* pool)
 {
     const int row_bytes = (int)(pool->D * elt_bytes(pool));
-    if (row_bytes >= 256) return PgCfg<128, kPgBf16>::kBlocksPerSm;
-    return row_bytes == 128 ? PgCfg<64, kPgBf16>::kBlocksPerSm : PgCfg<32, kPgBf16>::kBlocksPerSm;
+    if (row_bytes >= 256) return {PgCfg<128, kPgBf16>::kBlocksPerSm, PgCfg<128, kPgBf16>::kUnit};
+    if (row_bytes == 128) return {PgCfg<64, kPgBf16>::kBlocksPerSm, PgCfg<64, kPgBf16>::kUnit};
+    return {PgCfg<32, kPgBf16>::kBlocksPerSm, PgCfg<32, kPgBf16>::kUnit};
 }
 
-// One wave of blocks.  Rows stay whole (no partials, no second launch) where they are short: at four
-// units (512 visible rows) a block's sweep takes less time than the join's launch, and without
+// One wave of blocks.  Rows stay whole (no partials, no second launch) where they are short: up to 512
+// visible rows a block's sweep takes less time than the join's launch, and without
 // parallelism to gain the join would only add to it.
 DecodePlan decode_plan(const unipin_kvpool* pool, int R, int H, int max_len, int window, int n_sinks, bool weights,
                        int sms)
@@ -149,9 +154,10 @@ DecodePlan decode_plan(const unipin_kvpool* pool, int R, int H, int max_len, int
     pl.vmax = (int)vmax;
     const int G = H / pool->H;
     const long long pairs = (long long)R * pool->H * ((G + 15) / 16);
-    const long long units = vmax > 0 ? (vmax + kPgUnit - 1) / kPgUnit : 1;
-    pl.whole = !weights && units <= 4;
-    const long long slots = (long long)sms * decode_blocks_per_sm(pool);
+    const DecodeShape shape = decode_shape(pool);
+    const long long units = vmax > 0 ? (vmax + shape.unit - 1) / shape.unit : 1;
+    pl.whole = !weights && vmax <= 512;
+    const long long slots = (long long)sms * shape.blocks_per_sm;
     const long long most = pl.whole ? pairs : pairs * units;
     pl.shares = (int)(most < slots ? most : slots);
     return pl;
@@ -301,7 +307,7 @@ int unipin_paged_decode_attn(const void* q, const void* k_self, const void* v_se
     const bool weights = key_weights != nullptr;
     DecodePlan pl = decode_plan(pool, R, H, max_len, window, n_sinks, weights, current_sms());
     // rows and units are numbered with 31 bits
-    const long long units = (long long)R * pool->H * groups * ((pl.vmax + kPgUnit - 1) / kPgUnit + 1);
+    const long long units = (long long)R * pool->H * groups * ((pl.vmax + 63) / 64 + 1);
     if (R > 65535 || max_len > (1 << 30) || units >= (1ll << 31)) return UNIPIN_ERR_INVALID_ARG;
     rc = ensure_paged();
     if (rc != UNIPIN_OK) return rc;
@@ -331,6 +337,7 @@ int unipin_paged_decode_attn(const void* q, const void* k_self, const void* v_se
     p.window = window;
     p.n_sinks = n_sinks;
     p.heads = G < 16 ? G : 16;
+    p.unit_shift = decode_shape(pool).unit == 64 ? 6 : 7;
     p.groups = groups;
     p.vmax = (pl.vmax + 3) / 4 * 4;
     p.whole = pl.whole ? 1 : 0;

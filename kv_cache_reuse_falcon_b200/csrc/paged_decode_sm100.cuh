@@ -66,8 +66,6 @@ namespace unipin {
 
 constexpr int kPgWarps = 4;
 constexpr int kPgThreads = 32 * kPgWarps;
-constexpr int kPgKeys = 32;                      // rows of a warp's tile: one per lane
-constexpr int kPgUnit = kPgWarps * kPgKeys;      // rows of a unit
 constexpr float kPgLog2e = 1.4426950408889634f;
 constexpr float kPgRescaleLog2 = 8.0f;           // O is rescaled only when a row max grows by > 2^8
 
@@ -77,15 +75,19 @@ template <int D, int kMode>
 struct PgCfg {
     static constexpr int kElt = kMode == kPgBf16 ? 2 : 1;
     static constexpr int kRowBytes = D * kElt;
+    // rows of a warp's tile: 32 (one look-up per lane; what a tile costs whatever its rows is halved against
+    // 16), at the widest rows 16, for three blocks per SM
+    static constexpr int kKeys = kRowBytes >= 256 ? 16 : 32;
+    static constexpr int kUnit = kPgWarps * kKeys;          // rows of a unit
     static constexpr int kChunks = kRowBytes / 16;          // 16-byte chunks of a row
     static constexpr int kRowsPerCopy = 32 / kChunks;       // rows that one copy of a warp covers
-    static constexpr int kStageBytes = 2 * kPgKeys * kRowBytes;   // K and V of a tile
-    // Bytes in flight per SM for the memory latency: 128 KB at rows of 64 bytes and more (two of three
-    // stages of 4, 8 or 16 warps), 96 KB below.
-    static constexpr int kStages = kRowBytes >= 64 ? 3 : 4;
-    static constexpr int kBlocksPerSm = kRowBytes >= 256 ? 1 : (kRowBytes == 128 ? 2 : 4);
+    static constexpr int kStageBytes = 2 * kKeys * kRowBytes;   // K and V of a tile
+    // Bytes in flight per SM for the memory latency: about 100 KB (one stage of two or two of three of 12
+    // or 16 warps).
+    static constexpr int kStages = kRowBytes >= 128 ? 2 : (kRowBytes == 64 ? 3 : 4);
+    static constexpr int kBlocksPerSm = kRowBytes >= 128 ? 3 : 4;
     static constexpr int kRingBytes = kPgWarps * kStages * kStageBytes;
-    static constexpr int kRedHeads = 4;                                // heads that the warps join at a time
+    static constexpr int kRedHeads = D == 128 ? 2 : 4;                              // heads that the warps join at a time
     static constexpr int kOffQ = kRingBytes;                           // [16][D] bf16
     static constexpr int kOffRed = kOffQ + 16 * D * 2;                 // [warp][kRedHeads][D] fp32
     static constexpr int kOffMl = kOffRed + kPgWarps * kRedHeads * D * 4;   // [warp][16][2] fp32
@@ -111,6 +113,7 @@ struct PgParams {
     int R, H, Hkv, G, S, ps, max_pages, max_len;
     uint32_t ps_mul;               // j / ps = umulhi(j, ps_mul) >> ps_shift; 0: ps = 1
     int ps_shift;
+    int unit_shift;                // log2 of a unit's rows
     int window, n_sinks;
     int heads;                     // query heads of a unit: min(G, 16)
     int groups;                    // units' head groups per key/value head
@@ -145,7 +148,10 @@ __device__ __forceinline__ PgRows pg_rows(const PgParams& p, int r)
 }
 
 // Units of a row with `vis` visible rows (one where there is none: the row is still written).
-__device__ __forceinline__ int pg_units(int vis) { return max((vis + kPgUnit - 1) / kPgUnit, 1); }
+__device__ __forceinline__ int pg_units(const PgParams& p, int vis)
+{
+    return max((vis + (1 << p.unit_shift) - 1) >> p.unit_shift, 1);
+}
 
 __device__ __forceinline__ int pg_page(const PgParams& p, int j)
 {
@@ -160,7 +166,7 @@ struct PgPlace {
     {
         if (r < p.R) {
             rows = pg_rows(p, r);
-            u = pg_units(rows.vis);
+            u = pg_units(p, rows.vis);
         }
     }
     // the first unit of the next row
@@ -360,7 +366,7 @@ __device__ __forceinline__ void pg_find(const PgParams& p, PgScan& sc, int* firs
     const int per = (p.R + kPgThreads - 1) / kPgThreads;
     const int r0 = min(tid * per, p.R), r1 = min(r0 + per, p.R);   // this thread's requests
     int sum = 0;
-    for (int r = r0; r < r1; ++r) sum += pg_units(pg_rows(p, r).vis) * y_all;
+    for (int r = r0; r < r1; ++r) sum += pg_units(p, pg_rows(p, r).vis) * y_all;
     int incl = sum;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -381,7 +387,7 @@ __device__ __forceinline__ void pg_find(const PgParams& p, PgScan& sc, int* firs
     int first = base + incl - sum;
     if (first_unit || (first <= x && x < first + sum)) {
         for (int r = r0; r < r1; ++r) {
-            const int n = pg_units(pg_rows(p, r).vis) * y_all;
+            const int n = pg_units(p, pg_rows(p, r).vis) * y_all;
             if (first_unit) first_unit[r] = first;
             if (first <= x && x < first + n) {
                 sc.r = r;
@@ -419,6 +425,7 @@ __global__ void __launch_bounds__(kPgThreads, PgCfg<D, kMode>::kBlocksPerSm) pag
     if (p.whole)
         for (; x < x1 && at.t != 0; ++x) at.next(p);
     if (x >= x1) return;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join waits for this kernel's end itself
     const uint32_t ring = smem_u32(smem) + warp * C::kStages * C::kStageBytes;
     __nv_bfloat16* sQ = reinterpret_cast<__nv_bfloat16*>(smem + C::kOffQ);
     float* sRed = reinterpret_cast<float*>(smem + C::kOffRed);
@@ -433,7 +440,7 @@ __global__ void __launch_bounds__(kPgThreads, PgCfg<D, kMode>::kBlocksPerSm) pag
     uint32_t row = 0;
     bool row_live = false, row_bad = false;
     auto look_up = [&]() {
-        const int v = ld.t * kPgUnit + warp * kPgKeys + lane;
+        const int v = ld.t * C::kUnit + warp * C::kKeys + lane % C::kKeys;
         row = 0;
         row_live = !ld_end && v < ld.rows.vis;
         row_bad = false;
@@ -460,11 +467,11 @@ __global__ void __launch_bounds__(kPgThreads, PgCfg<D, kMode>::kBlocksPerSm) pag
         const bool bad = __any_sync(0xffffffffu, row_bad);
         bad_stages = (bad_stages & ~(1u << stage)) | ((uint32_t)bad << stage);
 #pragma unroll
-        for (int i = 0; i < kPgKeys / C::kRowsPerCopy; ++i) {
+        for (int i = 0; i < C::kKeys / C::kRowsPerCopy; ++i) {
             const int tr = i * C::kRowsPerCopy + cr;
             const uint64_t at_row = (uint64_t)__shfl_sync(0xffffffffu, row, tr) * C::kRowBytes;
             const uint32_t dst = st + pg_swizzle<C::kChunks>(tr, cc) * 16;
-            if (live == 0xffffffffu) {
+            if (live == 0xffffffffu) {            // (16-row tiles: the upper lanes look up the same rows)
                 pg_copy(dst, src_k + at_row);
                 pg_copy(dst + C::kStageBytes / 2, src_v + at_row);
             } else {
@@ -516,6 +523,11 @@ __global__ void __launch_bounds__(kPgThreads, PgCfg<D, kMode>::kBlocksPerSm) pag
         x += units;
         at.next_row(p);                             // (a share that ends inside a row ends with it)
         q_fetch(at.r, at.hk, at.cg, q_next);
+        if (p.k_self && all && threadIdx.x < 2) {   // read when the row is finished
+            const size_t own = ((size_t)r * p.Hkv + h0 / p.G) * D;
+            asm volatile("prefetch.global.L1 [%0];" ::"l"((threadIdx.x ? p.v_self : p.k_self) + own));
+            if (D == 128) asm volatile("prefetch.global.L1 [%0];" ::"l"((threadIdx.x ? p.v_self : p.k_self) + own + 64));
+        }
 
         // Q fragments: head g (and g + 8) as N, d in the order of the K fragments
         uint32_t qf[kNG][MT][2];
@@ -586,9 +598,9 @@ __global__ void __launch_bounds__(kPgThreads, PgCfg<D, kMode>::kBlocksPerSm) pag
             look_up();
             const uint32_t st = ring + stage * C::kStageBytes;
             stage = stage + 1 == C::kStages ? 0 : stage + 1;
-            const int vt = (t_first + i) * kPgUnit + warp * kPgKeys;   // visible index of the tile's first key
+            const int vt = (t_first + i) * C::kUnit + warp * C::kKeys;   // visible index of the tile's first key
             if (vt >= rows.vis) continue;
-            constexpr int KT = kPgKeys / 16;        // m-tiles of S^T, k-steps of O^T
+            constexpr int KT = C::kKeys / 16;        // m-tiles of S^T, k-steps of O^T
             float s[kNG][KT][4];
 #pragma unroll
             for (int n = 0; n < kNG; ++n)
@@ -645,7 +657,7 @@ __global__ void __launch_bounds__(kPgThreads, PgCfg<D, kMode>::kBlocksPerSm) pag
                             if (hh < nh && v < rows.vis) p.scores[((size_t)r * p.H + h0 + hh) * p.vmax + v] = s[n][k][e];
                         }
                 }
-                if (vt + kPgKeys > rows.vis) {      // the row ends inside the tile
+                if (vt + C::kKeys > rows.vis) {      // the row ends inside the tile
 #pragma unroll
                     for (int k = 0; k < KT; ++k)
 #pragma unroll
@@ -813,7 +825,7 @@ __global__ void __launch_bounds__(kPgThreads, PgCfg<D, kMode>::kBlocksPerSm) pag
 // Joins the pieces of each query row, and adds the weights of the cached rows into key_weights.
 // Grid (H + H_kv * weight blocks, R), 128 threads: a block x < H finishes query head x of request r (if it
 // is in pieces); the others take kPgWeightRows visible rows of one key/value head each.
-constexpr int kPgWeightRows = 1024;
+constexpr int kPgWeightRows = 512;
 constexpr int kPgJoinWarps = 4;
 
 // The pieces of a query row: those of blocks b0 .. b1 (one block: the row is finished already).
@@ -822,7 +834,7 @@ struct PgPieces {
     __device__ PgPieces(const PgParams& p, int r, int h, int vis)
     {
         const int share = pg_share(p.first_unit[p.R], p.shares);
-        const int hk = h / p.G, rest = h - hk * p.G, u = pg_units(vis);
+        const int hk = h / p.G, rest = h - hk * p.G, u = pg_units(p, vis);
         const int start = p.first_unit[r] + (hk * p.groups + rest / 16) * u;
         b0 = start / share;
         b1 = (start + u - 1) / share;
@@ -839,10 +851,10 @@ __global__ void __launch_bounds__(32 * kPgJoinWarps) paged_join_kernel(const PgP
     __shared__ float so[kPgJoinWarps][D];
     __shared__ float sml[kPgJoinWarps];
     extern __shared__ float s_lse[];                // [G] (weight blocks)
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int r = blockIdx.y;
     const PgRows rows = pg_rows(p, r);
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // (behind it: what the main kernel wrote)
     if (blockIdx.x < (unsigned)p.H) {
         const int h = blockIdx.x;
         const PgPieces pc(p, r, h, rows.vis);
@@ -924,18 +936,29 @@ __global__ void __launch_bounds__(32 * kPgJoinWarps) paged_join_kernel(const PgP
     }
     if (__syncthreads_or(bad)) return;
     const int* table = p.table + (size_t)r * p.max_pages;
-    for (int v = vb + threadIdx.x; v < min(vb + kPgWeightRows, rows.vis); v += 32 * kPgJoinWarps) {
-        float w = 0.f;
-        for (int gg = 0; gg < p.G; ++gg) {
-            const float s = p.scores[((size_t)r * p.H + hkv * p.G + gg) * p.vmax + v];
-            w += s == -INFINITY ? 0.f : ex2_approx(s - s_lse[gg]);
-        }
-        const int j = rows.row(v);
-        const int pg = pg_page(p, j);
-        const int page = __ldg(table + pg);
-        atomicAdd(p.key_weights + ((size_t)page * p.Hkv + hkv) * p.ps + (j - pg * p.ps), w);
-        // (atomic: requests may share pages, a common prefix)
+    static_assert(kPgWeightRows == 4 * 32 * kPgJoinWarps, "four rows per thread");
+    const int v = vb + 4 * threadIdx.x;
+    if (v >= rows.vis) return;
+    float w[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int gg = 0; gg < p.G; ++gg) {
+        // (vmax is a multiple of four; scores behind the last row are not used)
+        const float4 x4 = *reinterpret_cast<const float4*>(p.scores + ((size_t)r * p.H + hkv * p.G + gg) * p.vmax + v);
+        const float s[4] = {x4.x, x4.y, x4.z, x4.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] += s[i] == -INFINITY ? 0.f : ex2_approx(s[i] - s_lse[gg]);
     }
+    float* dst[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int j = rows.row(min(v + i, rows.vis - 1));
+        const int pg = pg_page(p, j);
+        dst[i] = p.key_weights + ((size_t)__ldg(table + pg) * p.Hkv + hkv) * p.ps + (j - pg * p.ps);
+    }
+    // atomic: requests may share pages (a common prefix)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (v + i < rows.vis) atomicAdd(dst[i], w[i]);
 }
 
 }  // namespace unipin
