@@ -204,6 +204,14 @@ __device__ __forceinline__ bool wb_item(const WbParams& p, unsigned block, WbIte
     return true;
 }
 
+// All ones in the low (high) half where a (b) is negative.
+__device__ __forceinline__ uint32_t wb_sign_pair(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("prmt.b32 %0, %1, %2, 0xffbb;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
 // One softmax pass over half a streamed tile: P and dS of this thread's resident row over 32 of the 64
 // streamed rows, from S and dP in TMEM (32 columns at tS and at tS + 64) and back as bfloat16 pairs over
 // the first 16 of those columns.  `see`: the columns that are allowed pairs.  kKV: -lse and -Dvec per
@@ -216,6 +224,13 @@ __device__ __forceinline__ void wb_softmax(uint32_t tS, float sl2, const float* 
     const uint64_t nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd);
     const bool full = __all_sync(0xffffffffu, see == ~0u);
     uint32_t sr[32], dr[32], pk[16], dk[16];
+    if (!__any_sync(0xffffffffu, see != 0u)) {       // no pair of these 32 x 32
+#pragma unroll
+        for (int i = 0; i < 16; ++i) pk[i] = 0u;
+        if (kKV) tmem_st16_nowait(tS, pk);
+        tmem_st16(tS + kWinStr, pk);
+        return;
+    }
     tmem_ld32x2(tS, sr, tS + kWinStr, dr);
 #pragma unroll
     for (int e = 0; e < 32; e += 4) {
@@ -236,12 +251,14 @@ __device__ __forceinline__ void wb_softmax(uint32_t tS, float sl2, const float* 
             float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
             d0 *= p0;
             d1 *= p1;
-            if (!full) {
-                if (!(see >> i & 1u)) p0 = d0 = 0.f;
-                if (!(see >> (i + 1) & 1u)) p1 = d1 = 0.f;
-            }
             pk[i / 2] = pack_bf16x2(p0, p1);
             dk[i / 2] = pack_bf16x2(d0, d1);
+            if (!full) {
+                // bits i, i + 1 of `see` as the signs of two bytes, spread over the pair's halves
+                const uint32_t pair = wb_sign_pair(see << (31 - i), see << (30 - i));
+                pk[i / 2] &= pair;
+                dk[i / 2] &= pair;
+            }
         }
     }
     if (kKV) tmem_st16_nowait(tS, pk);
@@ -371,7 +388,7 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
         // S and dP of tile i (landed) into its stage, whose P and dS no product reads any more
         auto scores = [&](int i) {
             const int st = i % C::kSlots;
-            if (leader) {
+            if (elect_one()) {
                 const uint32_t tS = tmem + (i % C::kStages) * 128;
                 const uint64_t slot = (uint64_t)((st * C::kSlotBytes) >> 4);
 #pragma unroll
@@ -402,7 +419,7 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
                  __all_sync(0xffffffffu, mbar_wait(p_ready + x, (i / C::kStages) & 1, ctl));
             if (!ok) break;
             tc_fence_after_sync();
-            if (leader) {
+            if (elect_one()) {
                 const uint64_t slot = (uint64_t)((st * C::kSlotBytes) >> 4);
 #pragma unroll
                 for (int kk = 0; kk < kWinStr / 16; ++kk) {
@@ -425,7 +442,7 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
                 scores(i + C::kStages);
             }
         }
-        if (leader) {
+        if (elect_one()) {
             umma_commit(bar_drain);
             mbar_wait_drain(bar_drain, 0, p.wait_limit_ns);
         }
@@ -481,7 +498,7 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
                 if (!(ok = warp_group_sync(grp + x, ngrp, ctl, lane))) break;
             }
             const int c0 = row0 + half * 32;         // streamed row of this half's first column
-            const uint32_t see = (uint32_t)win_see(lo - c0, hi - c0, sk - c0);
+            const uint32_t see = win_see32(lo - c0, hi - c0, sk - c0);
             ok = __all_sync(0xffffffffu, mbar_wait(s_ready + x, k & 1, ctl));
             if (!ok) break;
             tc_fence_after_sync();

@@ -79,6 +79,17 @@ __device__ __forceinline__ uint64_t win_see(int lo, int hi, int sk)
     return win_below(hi) & (~win_below(lo) | win_below(sk));
 }
 
+// The same of 32 columns.
+__device__ __forceinline__ uint32_t win_below32(int n)
+{
+    return n >= 32 ? ~0u : (1u << max(n, 0)) - 1u;
+}
+
+__device__ __forceinline__ uint32_t win_see32(int lo, int hi, int sk)
+{
+    return win_below32(hi) & (~win_below32(lo) | win_below32(sk));
+}
+
 // Eight bfloat16 (16 bytes) as floats.
 __device__ __forceinline__ void win_unpack8(uint4 x, float (&f)[8])
 {

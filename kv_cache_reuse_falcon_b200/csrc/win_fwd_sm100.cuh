@@ -183,7 +183,8 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
     uint64_t* k_empty = bars + 10;
     uint64_t* v_full = bars + 13;
     uint64_t* v_empty = bars + 16;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 19);
+    uint64_t* o_done = bars + 19;      // the last P V: O is final
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 20);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const bool leader = lane == 0;
     WaitCtl ctl{abort_flag, p.status, p.wait_limit_ns, (int)UNIPIN_ERR_DEVICE_TIMEOUT};
@@ -198,6 +199,7 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
         mbar_init(bar_q, 1);
         mbar_init(bar_drain, 1);
         mbar_init(pv_done, 1);
+        mbar_init(o_done, 1);
         for (int x = 0; x < 2; ++x) {
             mbar_init(s_ready + x, 1);
             mbar_init(p_ready + x, 4);
@@ -273,7 +275,7 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
         };
         // S of tile i (landed) into its stage, whose P no product reads any more
         auto scores = [&](int i) {
-            if (leader) {
+            if (elect_one()) {
                 const uint64_t slot = (uint64_t)((i % C::kKSlots * C::kKvTile) >> 4);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
@@ -299,7 +301,7 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
                  __all_sync(0xffffffffu, mbar_wait(p_ready + x, (i / C::kStages) & 1, ctl));
             if (!ok) break;
             tc_fence_after_sync();
-            if (leader) {
+            if (elect_one()) {
                 const uint64_t slot = (uint64_t)((i % C::kVSlots * C::kKvTile) >> 4);
 #pragma unroll
                 for (int kk = 0; kk < kWinStr / 16; ++kk)
@@ -308,6 +310,7 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
                                  (i > 0 || kk > 0) ? 1u : 0u);
                 umma_commit(v_empty + i % C::kVSlots);
                 umma_commit(pv_done);
+                if (i + 1 == total) umma_commit(o_done);
             }
             if (i + C::kStages < total) {
                 // only products into one accumulator are sure to run in order: S over P waits for P V
@@ -317,7 +320,7 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
                 scores(i + C::kStages);
             }
         }
-        if (leader) {
+        if (elect_one()) {
             umma_commit(bar_drain);
             mbar_wait_drain(bar_drain, 0, p.wait_limit_ns);
         }
@@ -433,7 +436,7 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
             if (lane == 0) mbar_arrive(p_ready + x);
         }
         if (ok && total > 0) {
-            ok = __all_sync(0xffffffffu, mbar_wait(pv_done, (total - 1) & 1, ctl));
+            ok = __all_sync(0xffffffffu, mbar_wait(o_done, 0, ctl));
             tc_fence_after_sync();
         }
         if (ok) {
