@@ -198,8 +198,8 @@ int unipin_windowed_prefill_attn(const void* q, const void* k, const void* v, vo
  *   dq             [T, H, D], dk and dv [T, H_kv, D]: fp32 if grad_fp32 else bf16 (sums
  *                  are fp32, rounded once).  No atomics: the same inputs give the same
  *                  bits.
- *   workspace      unipin_windowed_prefill_bwd_workspace_size(total_tokens, H) bytes,
- *                  16-byte aligned; not shared by overlapping calls
+ *   workspace      unipin_windowed_prefill_bwd_workspace_size(...) bytes, 16-byte aligned
+ *                  (row statistics and partial sums); not shared by overlapping calls
  * B <= 65535.  Other arguments and errors as unipin_masked_prefill_bwd.  A segment
  * whose history length is out of range gets zero gradients; rows behind the last
  * segment are left as they are.
@@ -210,8 +210,9 @@ int unipin_windowed_prefill_bwd(const void* q, const void* k, const void* v, con
                                 int window, int n_sinks, float scale, void* workspace, size_t workspace_bytes,
                                 int* dev_status, void* stream);
 
-/* Bytes of workspace unipin_windowed_prefill_bwd needs: 8 * total_tokens * H, rounded up to 16. */
-size_t unipin_windowed_prefill_bwd_workspace_size(int total_tokens, int H);
+/* Bytes of workspace unipin_windowed_prefill_bwd needs for these arguments. */
+size_t unipin_windowed_prefill_bwd_workspace_size(int B, int H, int H_kv, int D, int max_seqlen, int total_tokens,
+                                                  int window, int n_sinks);
 
 /*
  * Pool write ([review] §2.4: retrieval writes the past K/V of every layer

@@ -120,7 +120,7 @@ def _load(path: str = _LIB_PATH):
     lib.unipin_windowed_prefill_bwd.argtypes = [P, P, P, P, P, P, P, P, P, I, P, P, I, I, I, I, I, I, I, I, F, P, SZ,
                                                 P, P]
     lib.unipin_windowed_prefill_bwd.restype = I
-    lib.unipin_windowed_prefill_bwd_workspace_size.argtypes = [I, I]
+    lib.unipin_windowed_prefill_bwd_workspace_size.argtypes = [I, I, I, I, I, I, I, I]
     lib.unipin_windowed_prefill_bwd_workspace_size.restype = SZ
     lib.unipin_paged_pool_write.argtypes = [P, I, P, P, P, P, P, I, P, I, I, I, P, P, P]
     lib.unipin_paged_pool_write.restype = I
@@ -520,8 +520,11 @@ def windowed_prefill_attn(q, k, v, cu_seqlens, past_lens, max_seqlen: int, windo
     return out
 
 
-def windowed_prefill_bwd_workspace_size(total_tokens: int, H: int) -> int:
-    return int(LIB.unipin_windowed_prefill_bwd_workspace_size(int(total_tokens), int(H)))
+def windowed_prefill_bwd_workspace_size(B: int, H: int, H_kv: int, D: int, max_seqlen: int, total_tokens: int,
+                                        window: Optional[int], n_sinks: int = 0) -> int:
+    """Workspace bytes of windowed_prefill_bwd."""
+    window, n_sinks = _window(window, n_sinks)
+    return LIB.unipin_windowed_prefill_bwd_workspace_size(B, H, H_kv, D, int(max_seqlen), total_tokens, window, n_sinks)
 
 
 def windowed_prefill_bwd(q, k, v, out, dout, lse, cu_seqlens, past_lens, max_seqlen: int, window: Optional[int],
@@ -555,7 +558,10 @@ def windowed_prefill_bwd(q, k, v, out, dout, lse, cu_seqlens, past_lens, max_seq
         dv = torch.empty((T, H_kv, D), dtype=kind, device=device)
     else:
         _fits(dv, "dv", kind, (T, H_kv, D))
-    ws, ws_bytes = _workspace(workspace, windowed_prefill_bwd_workspace_size(T, H), device)
+    nbytes = 0
+    if isinstance(workspace, str):
+        nbytes = LIB.unipin_windowed_prefill_bwd_workspace_size(B, H, H_kv, D, int(max_seqlen), T, window, n_sinks)
+    ws, ws_bytes = _workspace(workspace, nbytes, device)
     dev = _one_device(q, k, v, out, dout, lse, cu_seqlens, past_lens, dq, dk, dv, ws, dev_status)
     _call(dev, stream, LIB.unipin_windowed_prefill_bwd, "unipin_windowed_prefill_bwd", q.data_ptr(), k.data_ptr(),
           v.data_ptr(), out.data_ptr(), dout.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),

@@ -287,6 +287,49 @@ int launch_win_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
     return cudaGetLastError() == cudaSuccess ? UNIPIN_OK : UNIPIN_ERR_CUDA;
 }
 
+struct WbPlan {
+    int tiles, sink_tiles, sink_pieces, win_pieces;
+    long long n_kv, n_dq;                           // blocks of either kind
+    long long n_counters;
+    size_t dvec, dself, counters, part, bytes;      // places in the workspace
+};
+
+// The sweep of a key tile is cut where one would outlast the others: into pieces of at least half the steps
+// that an SM takes on average (a step: 64 rows of one query head), and of 16 steps, which take longer than
+// a piece's sums cost.  All rows see a tile with sinks; others those within the window, and candidates,
+// of which the host does not know the number.
+WbPlan win_bwd_plan(int B, int H, int H_kv, int D, int max_seqlen, int total_tokens, int window, int n_sinks)
+{
+    WbPlan pl = {};
+    const long long G = H / H_kv, rows = max_seqlen;
+    const long long near = rows < (long long)window + 192 ? rows : (long long)window + 192;
+    const long long sinks = n_sinks < rows ? n_sinks : rows;
+    pl.tiles = (int)((rows + kWinRes - 1) / kWinRes);
+    pl.sink_tiles = (int)((sinks + kWinRes - 1) / kWinRes);
+    const long long far_steps = G * ((rows + kWinStr - 1) / kWinStr), near_steps = G * ((near + kWinStr - 1) / kWinStr);
+    const long long dq_steps = (long long)B * H * pl.tiles * ((near + kWinStr - 1) / kWinStr + pl.sink_tiles * 2);
+    const long long all = (long long)B * H_kv * (pl.sink_tiles * far_steps + (pl.tiles - pl.sink_tiles) * near_steps) + dq_steps;
+    const long long sms = kNumSmsHint;              // (not the device's own: the workspace must not depend on it)
+    long long most = all / (2 * sms);
+    if (most < 16) most = 16;
+    pl.sink_pieces = pl.sink_tiles > 0 ? (int)((far_steps + most - 1) / most) : 1;
+    pl.win_pieces = (int)((near_steps + most - 1) / most);
+    pl.n_kv = (long long)B * H_kv *
+              ((long long)pl.sink_tiles * pl.sink_pieces + (long long)(pl.tiles - pl.sink_tiles) * pl.win_pieces);
+    pl.n_dq = (long long)B * H * pl.tiles;
+    const bool cut = pl.sink_pieces > 1 || pl.win_pieces > 1;
+    pl.n_counters = cut ? (long long)B * H_kv * pl.tiles * 2 : 0;
+    auto room = [&](size_t n) { const size_t at = pl.bytes; pl.bytes += (n + 255) / 256 * 256; return at; };
+    pl.dvec = room((size_t)total_tokens * H * 4);
+    pl.dself = room((size_t)total_tokens * H * 4);
+    pl.counters = room((size_t)pl.n_counters * 4);
+    const size_t slots = !cut ? 0
+                              : (size_t)B * H_kv * ((size_t)pl.sink_tiles * pl.sink_pieces +
+                                                    (size_t)(pl.tiles - pl.sink_tiles) * pl.win_pieces);
+    pl.part = room(slots * 2 * kWinRes * D * 4);
+    return pl;
+}
+
 template <int D>
 int launch_win_bwd(const CUtensorMap (&m)[8], const WbParams& p, unsigned prep_blocks, unsigned blocks, cudaStream_t s)
 {
@@ -952,10 +995,13 @@ int unipin_windowed_prefill_attn(const void* q, const void* k, const void* v, vo
     return launch_win_fwd<128>(tq, tk, tv, p, s);
 }
 
-size_t unipin_windowed_prefill_bwd_workspace_size(int total_tokens, int H)
+size_t unipin_windowed_prefill_bwd_workspace_size(int B, int H, int H_kv, int D, int max_seqlen, int total_tokens,
+                                                  int window, int n_sinks)
 {
-    if (total_tokens < 0 || H < 1) return 0;
-    return ((size_t)total_tokens * H * 2 * sizeof(float) + 15) / 16 * 16;
+    if (B < 1 || H < 1 || H_kv < 1 || H % H_kv != 0 || !supported_d(D) || max_seqlen < 1 || total_tokens < 0 ||
+        window < 1 || n_sinks < 0)
+        return 0;
+    return win_bwd_plan(B, H, H_kv, D, max_seqlen, total_tokens, window, n_sinks).bytes;
 }
 
 int unipin_windowed_prefill_bwd(const void* q, const void* k, const void* v, const void* out, const void* dout,
@@ -971,15 +1017,15 @@ int unipin_windowed_prefill_bwd(const void* q, const void* k, const void* v, con
     if (B == 0 || total_tokens == 0 || max_seqlen == 0) return UNIPIN_OK;
     if (!q || !k || !v || !out || !dout || !lse || !dq || !dk || !dv || !cu_seqlens || !past_lens || !workspace)
         return UNIPIN_ERR_INVALID_ARG;
-    if (workspace_bytes < unipin_windowed_prefill_bwd_workspace_size(total_tokens, H)) return UNIPIN_ERR_INVALID_ARG;
+    const WbPlan pl = win_bwd_plan(B, H, H_kv, D, max_seqlen, total_tokens, window, n_sinks);
+    if (workspace_bytes < pl.bytes) return UNIPIN_ERR_INVALID_ARG;
     for (const void* ptr : {q, k, v, out, dout, (const void*)dq, (const void*)dk, (const void*)dv,
                             (const void*)workspace})
         if (!aligned16(ptr)) return UNIPIN_ERR_MISALIGNED;
     if ((reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return UNIPIN_ERR_MISALIGNED;
-    const long long tiles = ((long long)max_seqlen + kWinRes - 1) / kWinRes;
-    const long long n_kv = tiles * B * H_kv, n_dq = tiles * B * H;
-    const long long prep = ((long long)max_seqlen * H_kv * (D / 8) + kWbPrepThreads - 1) / kWbPrepThreads;
-    if (B > 65535 || n_kv + n_dq >= (1ll << 31) || prep >= (1ll << 31)) return UNIPIN_ERR_INVALID_ARG;
+    const long long prep = ((long long)max_seqlen + kWbPrepRows - 1) / kWbPrepRows;
+    // blocks are numbered with 31 bits
+    if (B > 65535 || pl.n_kv + pl.n_dq >= (1ll << 31)) return UNIPIN_ERR_INVALID_ARG;
     int rc = ensure_device();
     if (rc != UNIPIN_OK) return rc;
 
@@ -993,8 +1039,16 @@ int unipin_windowed_prefill_bwd(const void* q, const void* k, const void* v, con
     p.dq = dq;
     p.dk = dk;
     p.dv = dv;
-    p.dvec = static_cast<float*>(workspace);
-    p.dself = p.dvec + (size_t)total_tokens * H;
+    char* ws = static_cast<char*>(workspace);
+    p.dvec = reinterpret_cast<float*>(ws + pl.dvec);
+    p.dself = reinterpret_cast<float*>(ws + pl.dself);
+    p.counters = reinterpret_cast<unsigned*>(ws + pl.counters);
+    p.n_counters = pl.n_counters;
+    p.part = reinterpret_cast<float*>(ws + pl.part);
+    p.tiles = pl.tiles;
+    p.sink_tiles = pl.sink_tiles;
+    p.sink_pieces = pl.sink_pieces;
+    p.win_pieces = pl.win_pieces;
     p.cu = cu_seqlens;
     p.past = past_lens;
     p.B = B;
@@ -1006,7 +1060,7 @@ int unipin_windowed_prefill_bwd(const void* q, const void* k, const void* v, con
     p.window = window;
     p.n_sinks = n_sinks;
     p.grad_fp32 = grad_fp32 ? 1 : 0;
-    p.n_kv = (unsigned)n_kv;
+    p.n_kv = (unsigned)pl.n_kv;
     p.scale = scale;
     p.sl2 = scale * kLog2e;
     p.status = dev_status;
@@ -1021,7 +1075,7 @@ int unipin_windowed_prefill_bwd(const void* q, const void* k, const void* v, con
         if ((rc = make_token_map(&m[4 * i + 3], v, total_tokens, H_kv, D, rows)) != UNIPIN_OK) return rc;
     }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const unsigned blocks = (unsigned)(n_kv + n_dq);
+    const unsigned blocks = (unsigned)(pl.n_kv + pl.n_dq);
     if (D == 32) return launch_win_bwd<32>(m, p, (unsigned)prep, blocks, s);
     if (D == 64) return launch_win_bwd<64>(m, p, (unsigned)prep, blocks, s);
     return launch_win_bwd<128>(m, p, (unsigned)prep, blocks, s);

@@ -19,6 +19,8 @@
 //     stay in shared memory; the 64-row tiles of Q and dO of the rows that see
 //     them are streamed, for each of the G query heads in turn:
 //       S^T = K Q^T, dP^T = V dO^T;  dV += P^T dO, dK += dS^T Q
+//     A long sweep (a tile with sinks is seen by every row) is cut into pieces whose
+//     float32 sums are added up, in order, by the piece that ends last.
 //   dQ block: 128 rows of (segment, query head).  Q and dO stay, the 64-row tiles
 //     of K and V that the rows see are streamed:
 //       S = Q K^T, dP = dO V^T;      dQ += dS K
@@ -92,9 +94,14 @@ struct WbParams {
     void* dv;
     float* dvec;                // [T, H] workspace
     float* dself;               // [T, H] workspace: dS of a candidate's own key
+    float* part;                // workspace: pieces' sums [slot][dV, dK][128][D]
+    unsigned* counters;         // workspace: ended pieces of (segment, kv head, key tile, dV or dK)
+    long long n_counters;
     const int* cu;
     const int* past;
     int B, H, Hkv, G, total_rows, max_rows;
+    int tiles, sink_tiles;      // key tiles of max_rows, and how many of them may hold a sink
+    int sink_pieces, win_pieces;   // most pieces of a KV block's sweep with and without sinks
     int window, n_sinks;
     int grad_fp32;
     unsigned n_kv;
@@ -104,79 +111,103 @@ struct WbParams {
 };
 
 constexpr int kWbPrepThreads = 256;
+constexpr int kWbPrepRows = 16;     // rows of a block
+constexpr int kWbPrepUnroll = 4;    // query rows of a thread at a time: loads in flight
 
-// Grid (blocks of (row, key/value head) pairs, B); D / 8 lanes per pair, 16 bytes of the row each.
+// Grid (blocks of rows, B); D / 8 lanes per query row, 16 bytes of it each.
 template <int D>
-__global__ void __launch_bounds__(kWbPrepThreads) win_bwd_prep_kernel(const WbParams p)
+__global__ void __launch_bounds__(kWbPrepThreads, 4) win_bwd_prep_kernel(const WbParams p)
 {
     constexpr int L = D / 8;
+    constexpr int kGroups = kWbPrepThreads / L;
+    for (long long i = ((long long)blockIdx.y * gridDim.x + blockIdx.x) * kWbPrepThreads + threadIdx.x; i < p.n_counters;
+         i += (long long)gridDim.x * gridDim.y * kWbPrepThreads)
+        p.counters[i] = 0u;
     const int b = blockIdx.y;
     const WinSegment s = win_segment(p.cu, p.past, b, p.max_rows, p.total_rows);
     if (!s.ok && blockIdx.x == 0 && threadIdx.x == 0) report(p.status, (int)UNIPIN_ERR_OUT_OF_RANGE);
-    if (!s.rows_ok) return;
-    const int c = threadIdx.x % L;
-    const long long x = (long long)blockIdx.x * (kWbPrepThreads / L) + threadIdx.x / L;
-    const bool live = x < (long long)s.len * p.Hkv;      // (shuffles below: the lanes of a pair agree)
-    const int row = live ? (int)(x / p.Hkv) : 0;
-    const int hk = live ? (int)(x - (long long)row * p.Hkv) : 0;
-    const long long tok = (long long)s.tok0 + row;
-    const size_t kv_at = ((size_t)tok * p.Hkv + hk) * D + c * 8;
+    const int r0 = blockIdx.x * kWbPrepRows, r1 = min(r0 + kWbPrepRows, s.len);
+    if (!s.rows_ok || r0 >= r1) return;
+    const int c = threadIdx.x % L, grp = threadIdx.x / L;
     if (!s.ok) {                                         // an out-of-range history length: zero gradients
         const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (live) {
-            win_store8(p.dk, p.grad_fp32, kv_at, z);
-            win_store8(p.dv, p.grad_fp32, kv_at, z);
-            for (int g = 0; g < p.G; ++g)
-                win_store8(p.dq, p.grad_fp32, ((size_t)tok * p.H + hk * p.G + g) * D + c * 8, z);
+        for (long long x = grp; x < (long long)(r1 - r0) * p.H; x += kGroups)
+            win_store8(p.dq, p.grad_fp32, (((size_t)s.tok0 + r0) * p.H + x) * D + c * 8, z);
+        for (long long x = grp; x < (long long)(r1 - r0) * p.Hkv; x += kGroups) {
+            win_store8(p.dk, p.grad_fp32, (((size_t)s.tok0 + r0) * p.Hkv + x) * D + c * 8, z);
+            win_store8(p.dv, p.grad_fp32, (((size_t)s.tok0 + r0) * p.Hkv + x) * D + c * 8, z);
         }
         return;
     }
-    const bool cand = live && row >= s.n;
-    float kf[8], vf[8], dk[8], dv[8];
+    auto dot_lanes = [&](float x) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dk[e] = dv[e] = kf[e] = vf[e] = 0.f;
-    if (cand) {
-        win_unpack8(__ldg(reinterpret_cast<const uint4*>(p.k + kv_at)), kf);
-        win_unpack8(__ldg(reinterpret_cast<const uint4*>(p.v + kv_at)), vf);
+        for (int off = L / 2; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+        return x;
+    };
+    auto dot8 = [&](uint4 a, uint4 b8) {
+        float x[8], y[8], d = 0.f;
+        win_unpack8(a, x);
+        win_unpack8(b8, y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d = fmaf(x[e], y[e], d);
+        return d;
+    };
+    // Dvec of the block's query rows, which lie side by side
+    {
+        const long long rows = (long long)(r1 - r0) * p.H;
+        const size_t q0 = ((size_t)s.tok0 + r0) * p.H;
+        for (long long x0 = grp; x0 - grp < rows; x0 += kGroups * kWbPrepUnroll) {
+            uint4 o4[kWbPrepUnroll], g4[kWbPrepUnroll];
+#pragma unroll
+            for (int i = 0; i < kWbPrepUnroll; ++i) {
+                const long long x = x0 + i * kGroups;
+                const size_t at = (q0 + (x < rows ? x : 0)) * D + c * 8;
+                o4[i] = __ldg(reinterpret_cast<const uint4*>(p.o + at));
+                g4[i] = __ldg(reinterpret_cast<const uint4*>(p.dout + at));
+            }
+#pragma unroll
+            for (int i = 0; i < kWbPrepUnroll; ++i) {
+                const long long x = x0 + i * kGroups;
+                const float d = dot_lanes(dot8(o4[i], g4[i]));
+                if (c == 0 && x < rows) p.dvec[q0 + x] = d;
+            }
+        }
     }
-    for (int g = 0; g < p.G; ++g) {
-        const size_t qr = (size_t)tok * p.H + hk * p.G + g;
-        float of[8], gf[8], qf[8];
+    // candidates: their own key
+    const int c0 = max(r0, s.n);
+    const int pairs = max(r1 - c0, 0) * p.Hkv;           // (at most 16 rows)
+    for (int x = grp; x - grp < pairs; x += kGroups) {
+        const bool live = x < pairs;
+        const int row = c0 + (live ? x / p.Hkv : 0), hk = live ? x % p.Hkv : 0;
+        const size_t tok = (size_t)s.tok0 + row, at = (tok * p.Hkv + hk) * D + c * 8;
+        const uint4 k4 = __ldg(reinterpret_cast<const uint4*>(p.k + at));
+        const uint4 v4 = __ldg(reinterpret_cast<const uint4*>(p.v + at));
+        float dk[8], dv[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) of[e] = gf[e] = qf[e] = 0.f;
-        if (live) {
-            win_unpack8(__ldg(reinterpret_cast<const uint4*>(p.o + qr * D + c * 8)), of);
-            win_unpack8(__ldg(reinterpret_cast<const uint4*>(p.dout + qr * D + c * 8)), gf);
-        }
-        if (cand) win_unpack8(__ldg(reinterpret_cast<const uint4*>(p.q + qr * D + c * 8)), qf);
-        float dvec = 0.f, qk = 0.f, gv = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            dvec = fmaf(gf[e], of[e], dvec);
-            qk = fmaf(qf[e], kf[e], qk);
-            gv = fmaf(gf[e], vf[e], gv);
-        }
-#pragma unroll
-        for (int off = L / 2; off > 0; off >>= 1) {
-            dvec += __shfl_xor_sync(0xffffffffu, dvec, off);
-            qk += __shfl_xor_sync(0xffffffffu, qk, off);
-            gv += __shfl_xor_sync(0xffffffffu, gv, off);
-        }
-        if (live && c == 0) p.dvec[qr] = dvec;
-        if (cand) {
-            const float w = ex2_approx(fmaf(qk, p.sl2, win_neg_lse(p.lse[qr])));
+        for (int e = 0; e < 8; ++e) dk[e] = dv[e] = 0.f;
+        for (int g = 0; g < p.G; ++g) {
+            const size_t qr = tok * p.H + hk * p.G + g;
+            const uint4 q4 = __ldg(reinterpret_cast<const uint4*>(p.q + qr * D + c * 8));
+            const uint4 o4 = __ldg(reinterpret_cast<const uint4*>(p.o + qr * D + c * 8));
+            const uint4 g4 = __ldg(reinterpret_cast<const uint4*>(p.dout + qr * D + c * 8));
+            const float lse = p.lse[qr];
+            const float dvec = dot_lanes(dot8(o4, g4)), qk = dot_lanes(dot8(q4, k4)), gv = dot_lanes(dot8(g4, v4));
+            const float w = ex2_approx(fmaf(qk, p.sl2, win_neg_lse(lse)));
             const float ds = w * (gv - dvec);
-            if (c == 0) p.dself[qr] = ds;
+            if (live && c == 0) p.dself[qr] = ds;
+            float qf[8], gf[8];
+            win_unpack8(q4, qf);
+            win_unpack8(g4, gf);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 dk[e] = fmaf(p.scale * ds, qf[e], dk[e]);
                 dv[e] = fmaf(w, gf[e], dv[e]);
             }
         }
-    }
-    if (cand) {
-        win_store8(p.dk, p.grad_fp32, kv_at, dk);
-        win_store8(p.dv, p.grad_fp32, kv_at, dv);
+        if (live) {
+            win_store8(p.dk, p.grad_fp32, at, dk);
+            win_store8(p.dv, p.grad_fp32, at, dv);
+        }
     }
 }
 
@@ -185,22 +216,54 @@ struct WbItem {
     int b, h;            // h: key/value head (KV) or query head (dQ)
     int r0;              // first resident row within the segment
     WinSweep sweep;      // the streamed tiles (KV: of each of the G query heads in turn)
+    int first, total;    // the block's part of them: its first, and how many
+    int piece, pieces;   // KV: which of how many pieces of the tile's sweep
+    size_t slot, tile;   // KV: number of the tile's first piece, and of the tile
 };
 
 template <bool kKV>
 __device__ __forceinline__ bool wb_item(const WbParams& p, unsigned block, WbItem& it, WinSegment& s)
 {
-    // tile-major: the longest sweeps (a KV block's first tile sees the most rows, the sink tile all) start first
+    // tile-major: the longest sweeps (a KV block's first tile sees the most rows, a tile with sinks all) start first
     const int heads = kKV ? p.Hkv : p.H;
     const unsigned bh_count = (unsigned)p.B * heads;
-    const int t = (int)(block / bh_count);
+    int t = (int)(block / bh_count);
     const unsigned bh = block - (unsigned)t * bh_count;
     it.b = (int)(bh / heads);
     it.h = (int)(bh - (unsigned)it.b * heads);
+    it.piece = 0;
+    int most = 1;
+    if (kKV) {
+        const int sinks = p.sink_tiles * p.sink_pieces;
+        if (t < sinks) {
+            most = p.sink_pieces;
+            it.piece = t % most;
+            t /= most;
+            it.slot = ((size_t)bh * p.sink_tiles + t) * most;
+        } else {
+            most = p.win_pieces;
+            t -= sinks;
+            it.piece = t % most;
+            t /= most;
+            it.slot = (size_t)bh_count * sinks + ((size_t)bh * (p.tiles - p.sink_tiles) + t) * most;
+            t += p.sink_tiles;
+        }
+        it.tile = (size_t)bh * p.tiles + t;
+    }
     it.r0 = t * kWinRes;
     s = win_segment(p.cu, p.past, it.b, p.max_rows, p.total_rows);
     if (!s.ok || it.r0 >= (kKV ? s.n : s.len)) return false;   // the prep kernel zeroed and reported bad segments
     it.sweep = kKV ? win_row_sweep(it.r0, s, p.window, p.n_sinks) : win_key_sweep(it.r0, s, p.window, p.n_sinks);
+    it.total = kKV ? it.sweep.cnt * p.G : it.sweep.cnt;
+    it.first = 0;
+    it.pieces = 1;
+    if (kKV && most > 1) {
+        const int all = it.total, each = (all + most - 1) / most;
+        it.pieces = (all + each - 1) / each;
+        it.first = it.piece * each;
+        it.total = min(each, all - it.first);
+        if (it.total <= 0) return false;      // a piece behind the sweep's end
+    }
     return true;
 }
 
@@ -285,7 +348,7 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
     const bool work = wb_item<kKV>(p, block, it, s);
     if (!work || failed == (int)UNIPIN_ERR_DEVICE_TIMEOUT) return;
     const int cnt = it.sweep.cnt;
-    const int total = kKV ? cnt * p.G : cnt;
+    const int total = it.total;
 
     uint8_t* sRes = smem;
     uint8_t* ring = smem + C::kOffRing;
@@ -301,6 +364,7 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
     uint64_t* empty = full + C::kSlots;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(empty + C::kSlots);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile int* last_piece = reinterpret_cast<volatile int*>(tmem_slot + 2);   // [2]
     WaitCtl ctl{abort_flag, p.status, p.wait_limit_ns, (int)UNIPIN_ERR_DEVICE_TIMEOUT};
     const bool leader = lane == 0;
     // streamed tile i = tile `idx` of query head `g` of the group, into its ring slot
@@ -315,7 +379,8 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
             tma_load_3d(dst + C::kStrTile + c * C::kStrBox, &tm_s1, full + st, c * C::kBoxElems, head, row);
         }
     };
-    int pi = 0, pg = 0;                // producer: next tile's place
+    int pg = kKV && it.first > 0 ? it.first / cnt : 0;
+    int pi = it.first - pg * cnt;      // producer: next tile's place
     if (warp == C::kSoftWarps) {
         if (leader) {
             mbar_init(bar_res, 1);
@@ -471,7 +536,7 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
         }
         // KV: -lse and -Dvec of a streamed tile's rows: threads 0..63 of the group's first half the one,
         // 64..127 the other; fetched one tile ahead
-        int idx = x, g = 0;                          // place of the group's tile
+        int idx = it.first + x, g = 0;               // place of the group's tile
         auto wrap = [&]() {
             while (idx >= cnt && g < p.G) idx -= cnt, ++g;
         };
@@ -535,10 +600,51 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
                 const bool is_dk = c_first >= D;
                 const float f = is_dk ? p.scale : 1.f;
                 void* out = is_dk ? p.dk : p.dv;
+                bool store = true;
+                float* part = nullptr;
+                if (it.pieces > 1) {
+                    // this piece's sums; the piece that ends last adds them all up, in order
+                    part = p.part + (it.slot * kWinRes + t) * (2 * D) + c_first;
+                    float* mine = part + (size_t)it.piece * (2 * kWinRes * D);
+#pragma unroll
+                    for (int c = 0; c < kPart; c += 32) {
+                        uint32_t a[32];
+                        tmem_ld32(lanes + C::kColAcc0 + c_first + c, a);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<uint4*>(mine + c + e) = make_uint4(a[e], a[e + 1], a[e + 2], a[e + 3]);
+                    }
+                    __threadfence();
+                    ok = warp_group_sync(grp + x, ngrp, ctl, lane);
+                    if (ok && threadIdx.x % 256 == 0) {
+                        const unsigned ended = atomicAdd(p.counters + it.tile * 2 + x, 1u);
+                        __threadfence();
+                        last_piece[x] = ended == (unsigned)(it.pieces - 1);
+                    }
+                    ok = ok && warp_group_sync(grp + x, ngrp, ctl, lane);
+                    store = ok && last_piece[x];
+                }
 #pragma unroll
                 for (int c = 0; c < kPart; c += 32) {
+                    if (!store) break;
                     uint32_t a[32];
-                    tmem_ld32(lanes + C::kColAcc0 + c_first + c, a);
+                    if (it.pieces > 1) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) a[e] = 0u;
+                        for (int y = 0; y < it.pieces; ++y) {
+                            const float* from = part + (size_t)y * (2 * kWinRes * D) + c;
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) {
+                                const float4 v = __ldcg(reinterpret_cast<const float4*>(from + e));
+                                a[e] = __float_as_uint(__uint_as_float(a[e]) + v.x);
+                                a[e + 1] = __float_as_uint(__uint_as_float(a[e + 1]) + v.y);
+                                a[e + 2] = __float_as_uint(__uint_as_float(a[e + 2]) + v.z);
+                                a[e + 3] = __float_as_uint(__uint_as_float(a[e + 3]) + v.w);
+                            }
+                        }
+                    } else {
+                        tmem_ld32(lanes + C::kColAcc0 + c_first + c, a);
+                    }
                     if (!live) continue;
 #pragma unroll
                     for (int e = 0; e < 32; e += 8) {

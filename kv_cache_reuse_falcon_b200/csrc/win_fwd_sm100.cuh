@@ -352,21 +352,32 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
             tc_fence_after_sync();
             uint32_t sc[kWinStr];
             tmem_ld64(tS, sc);
-            const uint64_t see = win_see(lo - row0, hi - row0, p.n_sinks - row0);
-            if (!__all_sync(0xffffffffu, see == ~0ull)) {
+            // a warp's 32 rows by 32 keys at a time: under a short window a good part of a tile's have no
+            // pair, and cost nothing
+            uint32_t see[2];
+            bool some[2];
+            float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                for (int e = 0; e < kWinStr; ++e)
-                    if (!((e < 32 ? (uint32_t)see : (uint32_t)(see >> 32)) >> (e & 31) & 1u)) sc[e] = 0xff800000u;   // -inf
-            }
-            float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+            for (int half = 0; half < 2; ++half) {
+                const int c0 = row0 + 32 * half;
+                see[half] = win_see32(lo - c0, hi - c0, p.n_sinks - c0);
+                some[half] = __any_sync(0xffffffffu, see[half] != 0u);
+                if (!some[half]) continue;
+                uint32_t* x = sc + 32 * half;
+                if (!__all_sync(0xffffffffu, see[half] == ~0u)) {
 #pragma unroll
-            for (int e = 0; e < kWinStr; e += 8) {
-                mx0 = max3f<true>(mx0, __uint_as_float(sc[e]), __uint_as_float(sc[e + 1]));
-                mx1 = max3f<true>(mx1, __uint_as_float(sc[e + 2]), __uint_as_float(sc[e + 3]));
-                mx2 = max3f<true>(mx2, __uint_as_float(sc[e + 4]), __uint_as_float(sc[e + 5]));
-                mx3 = max3f<true>(mx3, __uint_as_float(sc[e + 6]), __uint_as_float(sc[e + 7]));
+                    for (int e = 0; e < 32; ++e)
+                        if (!(see[half] >> e & 1u)) x[e] = 0xff800000u;   // -inf
+                }
+                float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    m0 = max3f<true>(m0, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                    m1 = max3f<true>(m1, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+                }
+                mx[half] = fmax_nan(m0, m1);
             }
-            const float m_tile = fmax_nan(fmax_nan(mx0, mx1), fmax_nan(mx2, mx3)) * sl2;
+            const float m_tile = fmax_nan(mx[0], mx[1]) * sl2;
             odd = odd || !(m_tile < INFINITY);
             // move the reference max only when some row of the warp would see P > 2^8
             if (__any_sync(0xffffffffu, m_tile > m + kWfRescaleLog2)) {
@@ -389,32 +400,33 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
                 m = m_new;
             }
             const float m_use = m == -INFINITY ? 0.f : m;
+            // 2^x by the MUFU alone: with the FMA-pipe polynomial for one pair in four, as in the masked
+            // prefill, the issue slots and not the MUFU were the limit here
             const uint64_t sc2 = f2_pack(sl2, sl2), nm2 = f2_pack(-m_use, -m_use);
-            uint64_t acc[2] = {0ull, 0ull};
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 uint32_t pk[16];
+                if (some[half]) {
+                    uint64_t acc[2] = {0ull, 0ull};
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    const int e = half * 32 + 2 * c;
-                    const uint64_t x2 = f2_fma(f2_pack(__uint_as_float(sc[e]), __uint_as_float(sc[e + 1])), sc2, nm2);
-                    float p0, p1;
-                    if ((c & 3) == 3) {              // one pair in four on the FMA pipe
-                        exp2_poly2(x2, p0, p1);
-                    } else {
-                        f2_unpack(x2, p0, p1);
+                    for (int c = 0; c < 16; ++c) {
+                        const int e = half * 32 + 2 * c;
+                        float p0, p1;
+                        f2_unpack(f2_fma(f2_pack(__uint_as_float(sc[e]), __uint_as_float(sc[e + 1])), sc2, nm2), p0, p1);
                         p0 = ex2_approx(p0);
                         p1 = ex2_approx(p1);
+                        acc[c & 1] = f2_add(acc[c & 1], f2_pack(p0, p1));
+                        pk[c] = pack_bf16x2(p0, p1);
                     }
-                    acc[c & 1] = f2_add(acc[c & 1], f2_pack(p0, p1));
-                    pk[c] = pack_bf16x2(p0, p1);
+                    float a, c;
+                    f2_unpack(f2_add(acc[0], acc[1]), a, c);
+                    l += a + c;
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) pk[c] = 0u;
                 }
-                tmem_st16(tS + half * 16, pk);
-            }
-            {
-                float a, c;
-                f2_unpack(f2_add(acc[0], acc[1]), a, c);
-                l += a + c;
+                if (half == 0) tmem_st16_nowait(tS, pk);
+                else tmem_st16(tS + 16, pk);
             }
             ok = __all_sync(0xffffffffu, mbar_wait(v_full + i % C::kVSlots, (i / C::kVSlots) & 1, ctl));
             if (!ok) break;
@@ -435,6 +447,12 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
             __syncwarp();
             if (lane == 0) mbar_arrive(p_ready + x);
         }
+        // the own value (half of it at D = 128, for the registers) is fetched before O is waited for
+        constexpr int kAhead = D / 8 < 8 ? D / 8 : 8;
+        uint4 own[kAhead];
+#pragma unroll
+        for (int c = 0; c < kAhead; ++c)
+            own[c] = self ? __ldg(reinterpret_cast<const uint4*>(p.v + at_kv * D) + c) : make_uint4(0u, 0u, 0u, 0u);
         if (ok && total > 0) {
             ok = __all_sync(0xffffffffu, mbar_wait(o_done, 0, ctl));
             tc_fence_after_sync();
@@ -452,6 +470,11 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
+                if (c * 4 == kAhead) {
+#pragma unroll
+                    for (int i = 0; i < kAhead; ++i)
+                        if (self) own[i] = __ldg(reinterpret_cast<const uint4*>(p.v + at_kv * D) + kAhead + i);
+                }
                 if (total > 0) {
                     tmem_ld32(tO + c * 32, o);       // warp-collective: every lane loads
                 } else {
@@ -465,7 +488,7 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
 #pragma unroll
                     for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(o[g * 8 + e]) * a;
                     if (self) {
-                        win_unpack8(__ldg(reinterpret_cast<const uint4*>(p.v + at_kv * D) + c * 4 + g), vf);
+                        win_unpack8(own[(c * 4 + g) % kAhead], vf);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) f[e] = fmaf(w, vf[e], f[e]);
                     }
