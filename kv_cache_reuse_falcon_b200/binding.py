@@ -447,9 +447,15 @@ def _one_device(*tensors) -> int:
     return d
 
 
-def _call(device: int, stream, f, where: str, *args):
-    """f(*args, stream) with `device` current, on `stream` (default: the device's current stream)."""
-    raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+def _call(device: int, stream, made, f, where: str, *args):
+    """f(*args, stream) with `device` current, on `stream` (default: the device's current stream).  `made`:
+    tensors allocated for this call, whose memory must not go to others before `stream` is done with them."""
+    raw = torch._C._cuda_getCurrentRawStream(device)
+    if stream is not None and stream.cuda_stream != raw:
+        raw = stream.cuda_stream
+        for t in made:
+            if t is not None:
+                t.record_stream(stream)
     if device == torch._C._cuda_getDevice():
         rc = f(*args, raw)
     else:
@@ -507,14 +513,16 @@ def windowed_prefill_attn(q, k, v, cu_seqlens, past_lens, max_seqlen: int, windo
     _fits(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,))
     window, n_sinks = _window(window, n_sinks)
     kind = torch.float32 if out_fp32 else torch.bfloat16
+    made = ()
     if out is None:
         out = torch.empty((T, H, D), dtype=kind, device=q.device)
+        made = (out,)
     else:
         _fits(out, "out", kind, (T, H, D))
     if lse is not None:
         _fits(lse, "lse", torch.float32, (T, H))
     dev = _one_device(q, k, v, cu_seqlens, past_lens, out, lse, dev_status)
-    _call(dev, stream, LIB.unipin_windowed_prefill_attn, "unipin_windowed_prefill_attn", q.data_ptr(), k.data_ptr(),
+    _call(dev, stream, made, LIB.unipin_windowed_prefill_attn, "unipin_windowed_prefill_attn", q.data_ptr(), k.data_ptr(),
           v.data_ptr(), out.data_ptr(), 1 if out_fp32 else 0, _adr(lse), cu_seqlens.data_ptr(), past_lens.data_ptr(),
           B, H, H_kv, D, int(max_seqlen), T, window, n_sinks, _scale(scale, D), _adr(dev_status))
     return out
@@ -563,7 +571,7 @@ def windowed_prefill_bwd(q, k, v, out, dout, lse, cu_seqlens, past_lens, max_seq
         nbytes = LIB.unipin_windowed_prefill_bwd_workspace_size(B, H, H_kv, D, int(max_seqlen), T, window, n_sinks)
     ws, ws_bytes = _workspace(workspace, nbytes, device)
     dev = _one_device(q, k, v, out, dout, lse, cu_seqlens, past_lens, dq, dk, dv, ws, dev_status)
-    _call(dev, stream, LIB.unipin_windowed_prefill_bwd, "unipin_windowed_prefill_bwd", q.data_ptr(), k.data_ptr(),
+    _call(dev, stream, (ws, dq, dk, dv), LIB.unipin_windowed_prefill_bwd, "unipin_windowed_prefill_bwd", q.data_ptr(), k.data_ptr(),
           v.data_ptr(), out.data_ptr(), dout.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
           1 if grad_fp32 else 0, cu_seqlens.data_ptr(), past_lens.data_ptr(), B, H, H_kv, D, int(max_seqlen), T,
           window, n_sinks, _scale(scale, D), _adr(ws), ws_bytes, _adr(dev_status))
@@ -585,7 +593,7 @@ def paged_pool_write(pool_k, pool_v, layer: int, k, v, cu_seqlens, new_lens, pag
     pages = _page_table(page_table, B)
     _key_weights(key_weights, pool)
     dev = _one_device(pool_k, pool_v, k, v, cu_seqlens, new_lens, page_table, first_rows, key_weights, dev_status)
-    _call(dev, stream, LIB.unipin_paged_pool_write, "unipin_paged_pool_write", ctypes.byref(pool), int(layer),
+    _call(dev, stream, (), LIB.unipin_paged_pool_write, "unipin_paged_pool_write", ctypes.byref(pool), int(layer),
           k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), new_lens.data_ptr(), page_table.data_ptr(), pages,
           first_rows.data_ptr(), B, int(max_new), T, _adr(key_weights), _adr(dev_status))
 
@@ -634,7 +642,7 @@ def paged_decode_attn(q, page_table, lens, pool_k, pool_v, layer: int, max_len: 
                                                                 int(key_weights is not None)))
     workspace, ws_bytes = _workspace(workspace, nbytes, q.device)
     dev = _one_device(q, k_self, v_self, page_table, lens, pool_k, pool_v, key_weights, out, workspace, dev_status)
-    _call(dev, stream, LIB.unipin_paged_decode_attn, "unipin_paged_decode_attn", q.data_ptr(), _adr(k_self),
+    _call(dev, stream, (out, workspace), LIB.unipin_paged_decode_attn, "unipin_paged_decode_attn", q.data_ptr(), _adr(k_self),
           _adr(v_self), out.data_ptr(), 1 if out_fp32 else 0, page_table.data_ptr(), pages, lens.data_ptr(), R, H, D,
           max_len, window, n_sinks, _scale(scale, D), ctypes.byref(pool), int(layer), _adr(key_weights),
           _adr(workspace), ws_bytes, _adr(dev_status))
@@ -662,7 +670,7 @@ def paged_evict(pool_k, pool_v, key_weights, layer: int, page_table, lens, max_l
     else:
         _fits(new_lens, "new_lens", torch.int32, (R,))
     dev = _one_device(pool_k, pool_v, key_weights, page_table, lens, kept, new_lens, dev_status)
-    _call(dev, stream, LIB.unipin_paged_evict, "unipin_paged_evict", ctypes.byref(pool), int(layer),
+    _call(dev, stream, (kept, new_lens), LIB.unipin_paged_evict, "unipin_paged_evict", ctypes.byref(pool), int(layer),
           key_weights.data_ptr(), page_table.data_ptr(), pages, lens.data_ptr(), R, int(max_len), budget,
           int(n_sinks), int(n_recent), kept.data_ptr(), new_lens.data_ptr(), _adr(dev_status))
     return kept, new_lens
