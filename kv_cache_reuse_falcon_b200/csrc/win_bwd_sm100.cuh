@@ -39,8 +39,11 @@
 // D = 128 two stages of S and dP and one block per SM: while one group of softmax
 // warps works on a tile the other's products run.  At D <= 64 one stage and two
 // blocks per SM, which also hides a block's first loads and its epilogue.
-// P and dS are rounded to bfloat16 (relative 2^-8 each) as tensor-core operands;
-// scores, P, dS and all sums are float32.
+// P and dS are rounded to bfloat16 (relative 2^-8 each) as tensor-core operands of
+// dV and dK; scores, P, dS and all sums are float32.  dQ takes dS as the sum of two
+// bfloat16 (relative 2^-15): its row's Dvec comes from an output that carries two
+// roundings already, and with a third dQ would be the least exact of the results
+// (relative error 2.5e-3 in place of 2.0e-3, where the output's own rounding is 1.7e-3).
 // Segments are kept apart: streamed rows behind the segment's (or behind its
 // history) are zeroed in shared memory before they meet a zero weight, so what
 // another segment holds cannot reach a gradient through 0 * NaN.
@@ -286,11 +289,11 @@ __device__ __forceinline__ void wb_softmax(uint32_t tS, float sl2, const float* 
     const uint64_t sc = f2_pack(sl2, sl2);
     const uint64_t nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd);
     const bool full = __all_sync(0xffffffffu, see == ~0u);
-    uint32_t sr[32], dr[32], pk[16], dk[16];
+    uint32_t sr[32], dr[32], pk[16], dk[16];             // (dQ: dS in two parts, the lower one in pk)
     if (!__any_sync(0xffffffffu, see != 0u)) {       // no pair of these 32 x 32
 #pragma unroll
         for (int i = 0; i < 16; ++i) pk[i] = 0u;
-        if (kKV) tmem_st16_nowait(tS, pk);
+        tmem_st16_nowait(tS, pk);
         tmem_st16(tS + kWinStr, pk);
         return;
     }
@@ -314,8 +317,15 @@ __device__ __forceinline__ void wb_softmax(uint32_t tS, float sl2, const float* 
             float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
             d0 *= p0;
             d1 *= p1;
-            pk[i / 2] = pack_bf16x2(p0, p1);
-            dk[i / 2] = pack_bf16x2(d0, d1);
+            if (kKV) {
+                pk[i / 2] = pack_bf16x2(p0, p1);
+                dk[i / 2] = pack_bf16x2(d0, d1);
+            } else {
+                // the upper 8 bits of dS, and the rest rounded to as many
+                const uint32_t b0 = __float_as_uint(d0), b1 = __float_as_uint(d1);
+                dk[i / 2] = __byte_perm(b0, b1, 0x7632);
+                pk[i / 2] = pack_bf16x2(d0 - __uint_as_float(b0 & 0xffff0000u), d1 - __uint_as_float(b1 & 0xffff0000u));
+            }
             if (!full) {
                 // bits i, i + 1 of `see` as the signs of two bytes, spread over the pair's halves
                 const uint32_t pair = wb_sign_pair(see << (31 - i), see << (30 - i));
@@ -324,7 +334,7 @@ __device__ __forceinline__ void wb_softmax(uint32_t tS, float sl2, const float* 
             }
         }
     }
-    if (kKV) tmem_st16_nowait(tS, pk);
+    tmem_st16_nowait(tS, pk);
     tmem_st16(tS + kWinStr, dk);
 }
 
@@ -494,6 +504,7 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
                     const uint32_t acc = (i > 0 || kk > 0) ? 1u : 0u;
                     if (kKV) umma_bf16_ts(tmem + C::kColAcc0, tS, d_g1 + off, idesc_g, acc);
                     umma_bf16_ts(tmem + C::kColAcc1, tS + kWinStr, d_g0 + off, idesc_g, acc);
+                    if (!kKV) umma_bf16_ts(tmem + C::kColAcc1, tS, d_g0 + off, idesc_g, 1u);   // the lower part
                 }
                 umma_commit(empty + st);
                 if (i + 1 == total) umma_commit(acc_done);
