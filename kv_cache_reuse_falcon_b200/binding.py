@@ -2,8 +2,8 @@
 
 Argument marshalling only: torch tensors supply device pointers and the
 current CUDA stream; every step of the computation runs in the CUDA kernels of
-``libunipin.so``.  If the library is missing or fails to load, importing this
-module raises: there is no fallback.
+``libunipin.so``.  If it or ``_calls.so`` is missing or fails to load, importing
+this module raises: there is no fallback.
 """
 
 from __future__ import annotations
@@ -150,6 +150,8 @@ def _load(path: str = _LIB_PATH):
 
 
 LIB = _load()
+
+from kv_cache_reuse_falcon_b200 import _calls  # noqa: E402  (links against the library loaded above)
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -418,70 +420,10 @@ def status_string(code: int) -> str:
 
 # ------------------------------------------------- sliding window and paged pools
 #
-# Serving calls these once per layer and step on small inputs, where the checks below are most of a
-# call: they look at each property of a tensor once.
+# Serving makes these calls once per layer and step on small inputs, where checking the tensors one property
+# at a time from Python is most of a call: csrc/calls.cpp checks them (ValueError) and calls the entry point.
 
 NO_WINDOW = 2 ** 31 - 1    # window of an unrestricted call
-
-
-def _fits(t: torch.Tensor, name: str, dtype: torch.dtype, shape):
-    """A contiguous tensor of this type and shape (that it is on the device, _one_device sees)."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous CUDA %s tensor %s" % (name, dtype, list(shape)))
-
-
-def _token_rows(t: torch.Tensor, name: str):
-    """The shape of a contiguous bfloat16 tensor [T, H, D]."""
-    if t.dtype is not torch.bfloat16 or t.dim() != 3 or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous CUDA bfloat16 tensor [T, H, D]" % name)
-    return t.shape
-
-
-def _one_device(*tensors) -> int:
-    """The index of the CUDA device that every given tensor (None: not given) lies on."""
-    d = tensors[0].get_device()
-    for t in tensors:
-        if t is not None and t.get_device() != d or d < 0:
-            raise ValueError("the tensors must lie on one CUDA device: %s"
-                             % [str(x.device) for x in tensors if x is not None])
-    return d
-
-
-def _call(device: int, stream, made, f, where: str, *args):
-    """f(*args, stream) with `device` current, on `stream` (default: the device's current stream).  `made`:
-    tensors allocated for this call, whose memory must not go to others before `stream` is done with them."""
-    raw = torch._C._cuda_getCurrentRawStream(device)
-    if stream is not None and stream.cuda_stream != raw:
-        raw = stream.cuda_stream
-        for t in made:
-            if t is not None:
-                t.record_stream(stream)
-    if device == torch._C._cuda_getDevice():
-        rc = f(*args, raw)
-    else:
-        with torch.cuda.device(device):
-            rc = f(*args, raw)
-    if rc != UNIPIN_OK:
-        raise UnipinError(rc, where)
-
-
-def _page_table(page_table: torch.Tensor, rows: int) -> int:
-    if page_table.dtype is not torch.int32 or page_table.dim() != 2 or page_table.size(0) != rows \
-            or not page_table.is_contiguous():
-        raise ValueError("page_table must be a contiguous CUDA int32 tensor [%d, max_pages]" % rows)
-    return page_table.size(1)
-
-
-def _batch(t: torch.Tensor, name: str) -> int:
-    """The length of an int32 vector with an entry per request."""
-    if t.dtype is not torch.int32 or t.dim() != 1 or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous CUDA int32 vector" % name)
-    return t.size(0)
-
-
-def _key_weights(key_weights: Optional[torch.Tensor], pool: KVPool):
-    if key_weights is not None:
-        _fits(key_weights, "key_weights", torch.float32, (pool.L, pool.S, pool.H, pool.n_cap))
 
 
 def _window(window: Optional[int], n_sinks: int):
@@ -491,40 +433,16 @@ def _window(window: Optional[int], n_sinks: int):
     return window, int(n_sinks)
 
 
-def _adr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
-
-
-def _scale(scale: Optional[float], D: int) -> float:
-    return 1.0 / math.sqrt(D) if scale is None else float(scale)
-
-
 def windowed_prefill_attn(q, k, v, cu_seqlens, past_lens, max_seqlen: int, window: Optional[int], n_sinks: int = 0,
                           out=None, out_fp32: bool = True, scale: Optional[float] = None, dev_status=None, stream=None,
                           lse=None):
     """The masked prefill under a sliding window: with pos = i for a past row and pos = n_b for a
     candidate, past keys with pos - j < window (None: all) or j < n_sinks, and a candidate's own key.
     `lse` (fp32 [T, H]) takes the per-row log-sum-exp (base 2) that windowed_prefill_bwd needs."""
-    T, H, D = _token_rows(q, "q")
-    H_kv = _token_rows(k, "k")[1]
-    _fits(k, "k", torch.bfloat16, (T, H_kv, D))
-    _fits(v, "v", torch.bfloat16, (T, H_kv, D))
-    B = _batch(past_lens, "past_lens")
-    _fits(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,))
-    window, n_sinks = _window(window, n_sinks)
-    kind = torch.float32 if out_fp32 else torch.bfloat16
-    made = ()
-    if out is None:
-        out = torch.empty((T, H, D), dtype=kind, device=q.device)
-        made = (out,)
-    else:
-        _fits(out, "out", kind, (T, H, D))
-    if lse is not None:
-        _fits(lse, "lse", torch.float32, (T, H))
-    dev = _one_device(q, k, v, cu_seqlens, past_lens, out, lse, dev_status)
-    _call(dev, stream, made, LIB.unipin_windowed_prefill_attn, "unipin_windowed_prefill_attn", q.data_ptr(), k.data_ptr(),
-          v.data_ptr(), out.data_ptr(), 1 if out_fp32 else 0, _adr(lse), cu_seqlens.data_ptr(), past_lens.data_ptr(),
-          B, H, H_kv, D, int(max_seqlen), T, window, n_sinks, _scale(scale, D), _adr(dev_status))
+    rc, out = _calls.prefill(q, k, v, cu_seqlens, past_lens, max_seqlen, window, n_sinks, out, out_fp32, scale,
+                             dev_status, stream, lse)
+    if rc != UNIPIN_OK:
+        raise UnipinError(rc, "unipin_windowed_prefill_attn")
     return out
 
 
@@ -542,39 +460,10 @@ def windowed_prefill_bwd(q, k, v, out, dout, lse, cu_seqlens, past_lens, max_seq
     windowed_prefill_attn for the upstream gradient dout.
 
     `out` is the forward's bf16 output and `lse` the row statistic the forward wrote."""
-    T, H, D = _token_rows(q, "q")
-    H_kv = _token_rows(k, "k")[1]
-    _fits(k, "k", torch.bfloat16, (T, H_kv, D))
-    _fits(v, "v", torch.bfloat16, (T, H_kv, D))
-    _fits(out, "out", torch.bfloat16, (T, H, D))
-    _fits(dout, "dout", torch.bfloat16, (T, H, D))
-    _fits(lse, "lse", torch.float32, (T, H))
-    B = _batch(past_lens, "past_lens")
-    _fits(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,))
-    window, n_sinks = _window(window, n_sinks)
-    kind = torch.float32 if grad_fp32 else torch.bfloat16
-    device = q.device
-    if dq is None:
-        dq = torch.empty((T, H, D), dtype=kind, device=device)
-    else:
-        _fits(dq, "dq", kind, (T, H, D))
-    if dk is None:
-        dk = torch.empty((T, H_kv, D), dtype=kind, device=device)
-    else:
-        _fits(dk, "dk", kind, (T, H_kv, D))
-    if dv is None:
-        dv = torch.empty((T, H_kv, D), dtype=kind, device=device)
-    else:
-        _fits(dv, "dv", kind, (T, H_kv, D))
-    nbytes = 0
-    if isinstance(workspace, str):
-        nbytes = LIB.unipin_windowed_prefill_bwd_workspace_size(B, H, H_kv, D, int(max_seqlen), T, window, n_sinks)
-    ws, ws_bytes = _workspace(workspace, nbytes, device)
-    dev = _one_device(q, k, v, out, dout, lse, cu_seqlens, past_lens, dq, dk, dv, ws, dev_status)
-    _call(dev, stream, (ws, dq, dk, dv), LIB.unipin_windowed_prefill_bwd, "unipin_windowed_prefill_bwd", q.data_ptr(), k.data_ptr(),
-          v.data_ptr(), out.data_ptr(), dout.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-          1 if grad_fp32 else 0, cu_seqlens.data_ptr(), past_lens.data_ptr(), B, H, H_kv, D, int(max_seqlen), T,
-          window, n_sinks, _scale(scale, D), _adr(ws), ws_bytes, _adr(dev_status))
+    rc, dq, dk, dv = _calls.prefill_bwd(q, k, v, out, dout, lse, cu_seqlens, past_lens, max_seqlen, window, n_sinks,
+                                        scale, grad_fp32, dq, dk, dv, workspace, dev_status, stream)
+    if rc != UNIPIN_OK:
+        raise UnipinError(rc, "unipin_windowed_prefill_bwd")
     return dq, dk, dv
 
 
@@ -582,20 +471,10 @@ def paged_pool_write(pool_k, pool_v, layer: int, k, v, cu_seqlens, new_lens, pag
                      key_weights=None, dev_status=None, stream=None, pool_scales=None):
     """The first new_lens[b] tokens of each segment into rows first_rows[b], first_rows[b] + 1, ... of
     request b's pages (a paged pool [L, S pages, H, rows of a page, D]); their key_weights become 0."""
-    pool = _pool(pool_k, pool_v, pool_scales)
-    T = _token_rows(k, "k")[0]
-    shape = (T, pool.H, pool.D)
-    _fits(k, "k", torch.bfloat16, shape)
-    _fits(v, "v", torch.bfloat16, shape)
-    B = _batch(new_lens, "new_lens")
-    _fits(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,))
-    _fits(first_rows, "first_rows", torch.int32, (B,))
-    pages = _page_table(page_table, B)
-    _key_weights(key_weights, pool)
-    dev = _one_device(pool_k, pool_v, k, v, cu_seqlens, new_lens, page_table, first_rows, key_weights, dev_status)
-    _call(dev, stream, (), LIB.unipin_paged_pool_write, "unipin_paged_pool_write", ctypes.byref(pool), int(layer),
-          k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), new_lens.data_ptr(), page_table.data_ptr(), pages,
-          first_rows.data_ptr(), B, int(max_new), T, _adr(key_weights), _adr(dev_status))
+    rc = _calls.pool_write(pool_k, pool_v, layer, k, v, cu_seqlens, new_lens, page_table, first_rows, max_new,
+                           key_weights, dev_status, stream, pool_scales)
+    if rc != UNIPIN_OK:
+        raise UnipinError(rc, "unipin_paged_pool_write")
 
 
 def paged_decode_workspace_size(pool_k, pool_v, R: int, H: int, max_len: int, weights: bool = False,
@@ -615,37 +494,10 @@ def paged_decode_attn(q, page_table, lens, pool_k, pool_v, layer: int, max_len: 
     """One new token per request ([R, H, D]) over its cached rows 0 .. lens[r]-1: the last `window` rows
     (the token's own among them; None: all) and the first n_sinks, plus its own key and value where they
     are passed and not yet cached.  key_weights collects each row's attention weight."""
-    R, H, D = _token_rows(q, "q")
-    pool = _pool(pool_k, pool_v, pool_scales)
-    if pool.D != D or H % pool.H != 0:
-        raise ValueError("q must have the pool's head dim and a multiple of its %d heads" % pool.H)
-    if (k_self is None) != (v_self is None):
-        raise ValueError("k_self and v_self go together")
-    if k_self is not None:
-        shape = (R, pool.H, D)
-        _fits(k_self, "k_self", torch.bfloat16, shape)
-        _fits(v_self, "v_self", torch.bfloat16, shape)
-    _fits(lens, "lens", torch.int32, (R,))
-    pages = _page_table(page_table, R)
-    _key_weights(key_weights, pool)
-    window, n_sinks = _window(window, n_sinks)
-    max_len = int(max_len)
-    kind = torch.float32 if out_fp32 else torch.bfloat16
-    if out is None:
-        out = torch.empty((R, H, D), dtype=kind, device=q.device)
-    else:
-        _fits(out, "out", kind, (R, H, D))
-    nbytes = 0
-    if isinstance(workspace, str):
-        with torch.cuda.device(q.device):
-            nbytes = int(LIB.unipin_paged_decode_workspace_size(ctypes.byref(pool), R, H, max_len, window, n_sinks,
-                                                                int(key_weights is not None)))
-    workspace, ws_bytes = _workspace(workspace, nbytes, q.device)
-    dev = _one_device(q, k_self, v_self, page_table, lens, pool_k, pool_v, key_weights, out, workspace, dev_status)
-    _call(dev, stream, (out, workspace), LIB.unipin_paged_decode_attn, "unipin_paged_decode_attn", q.data_ptr(), _adr(k_self),
-          _adr(v_self), out.data_ptr(), 1 if out_fp32 else 0, page_table.data_ptr(), pages, lens.data_ptr(), R, H, D,
-          max_len, window, n_sinks, _scale(scale, D), ctypes.byref(pool), int(layer), _adr(key_weights),
-          _adr(workspace), ws_bytes, _adr(dev_status))
+    rc, out = _calls.decode(q, page_table, lens, pool_k, pool_v, layer, max_len, k_self, v_self, window, n_sinks,
+                            key_weights, out, out_fp32, scale, workspace, dev_status, stream, pool_scales)
+    if rc != UNIPIN_OK:
+        raise UnipinError(rc, "unipin_paged_decode_attn")
     return out
 
 
@@ -654,25 +506,10 @@ def paged_evict(pool_k, pool_v, key_weights, layer: int, page_table, lens, max_l
     """Requests with more than `budget` cached rows keep, per head, the first n_sinks, the last n_recent
     and the rows between with the largest key_weights; kept rows move to the front in their order.
     Returns (kept [R, H, budget] int32, the old row of each kept row or -1; new_lens [R] int32)."""
-    pool = _pool(pool_k, pool_v)
-    if key_weights is None:
-        raise ValueError("key_weights is required")
-    _key_weights(key_weights, pool)
-    R = _batch(lens, "lens")
-    pages = _page_table(page_table, R)
-    budget = int(budget)
-    if kept is None:
-        kept = torch.empty((R, pool.H, max(budget, 0)), dtype=torch.int32, device=lens.device)
-    else:
-        _fits(kept, "kept", torch.int32, (R, pool.H, budget))
-    if new_lens is None:
-        new_lens = torch.empty(R, dtype=torch.int32, device=lens.device)
-    else:
-        _fits(new_lens, "new_lens", torch.int32, (R,))
-    dev = _one_device(pool_k, pool_v, key_weights, page_table, lens, kept, new_lens, dev_status)
-    _call(dev, stream, (kept, new_lens), LIB.unipin_paged_evict, "unipin_paged_evict", ctypes.byref(pool), int(layer),
-          key_weights.data_ptr(), page_table.data_ptr(), pages, lens.data_ptr(), R, int(max_len), budget,
-          int(n_sinks), int(n_recent), kept.data_ptr(), new_lens.data_ptr(), _adr(dev_status))
+    rc, kept, new_lens = _calls.evict(pool_k, pool_v, key_weights, layer, page_table, lens, max_len, budget, n_sinks,
+                                      n_recent, kept, new_lens, dev_status, stream)
+    if rc != UNIPIN_OK:
+        raise UnipinError(rc, "unipin_paged_evict")
     return kept, new_lens
 
 

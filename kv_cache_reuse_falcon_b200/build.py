@@ -1,4 +1,5 @@
-"""Build the sm_100a shared library ``libunipin.so`` in-tree with nvcc."""
+"""Build the sm_100a shared library ``libunipin.so`` (nvcc) and the Python calls into it, ``_calls.so`` (g++,
+against the installed torch), in-tree."""
 
 from __future__ import annotations
 
@@ -12,6 +13,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libunipin.so")
+CALLS = os.path.join(PKG, "_calls.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -31,24 +33,56 @@ def _deps():
         + [os.path.join(INCLUDE, "unipin.h")]
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+def _calls_deps():
+    return [os.path.join(CSRC, "calls.cpp"), os.path.join(INCLUDE, "unipin.h")]
+
+
+def _newer(target, deps) -> bool:
+    if not os.path.exists(target):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    t = os.path.getmtime(target)
+    return all(os.path.getmtime(d) <= t for d in deps)
 
 
-def build(force: bool = False, verbose: bool = False, extra=None) -> str:
-    """Compile every .cu under csrc/ into libunipin.so (static cudart, no libcuda link)."""
-    if not force and up_to_date():
-        return LIB
-    nvcc = os.environ.get("NVCC", "nvcc")
-    tmp = LIB + ".tmp.%d" % os.getpid()
-    cmd = [nvcc] + NVCC_FLAGS + list(extra or []) + ["-I", INCLUDE, "-I", CSRC, "-o", tmp] + _sources()
+def up_to_date() -> bool:
+    return _newer(LIB, _deps()) and _newer(CALLS, _calls_deps())
+
+
+def _build_calls(verbose: bool):
+    import sysconfig
+
+    import torch
+    root = os.path.join(os.path.dirname(torch.__file__))
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    tmp = CALLS + ".tmp.%d" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI)]
+    for d in (os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+              sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE):
+        cmd += ["-I", d]
+    cmd += ["-o", tmp, os.path.join(CSRC, "calls.cpp"), "-L", PKG, "-l:libunipin.so", "-L", os.path.join(root, "lib"),
+            "-ltorch", "-ltorch_cpu", "-ltorch_python", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB)
+    os.replace(tmp, CALLS)
+
+
+def build(force: bool = False, verbose: bool = False, extra=None) -> str:
+    """Compile every .cu under csrc/ into libunipin.so (static cudart, no libcuda link) and calls.cpp into
+    _calls.so."""
+    if not force and up_to_date():
+        return LIB
+    if force or not _newer(LIB, _deps()):
+        nvcc = os.environ.get("NVCC", "nvcc")
+        tmp = LIB + ".tmp.%d" % os.getpid()
+        cmd = [nvcc] + NVCC_FLAGS + list(extra or []) + ["-I", INCLUDE, "-I", CSRC, "-o", tmp] + _sources()
+        if verbose:
+            print(" ".join(cmd), file=sys.stderr)
+        subprocess.run(cmd, check=True)
+        os.replace(tmp, LIB)
+    if force or not _newer(CALLS, _calls_deps()):
+        _build_calls(verbose)
     return LIB
 
 

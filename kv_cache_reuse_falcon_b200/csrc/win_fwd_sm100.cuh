@@ -18,7 +18,7 @@
 // (relative 2^-8), O += P V with P as A from TMEM.  At D = 128 S has two stages,
 // so the next tile's S is computed while the softmax works; at D <= 64 one, and
 // the other blocks' products run meanwhile.
-// Warps: softmax and epilogue (four, or eight at D = 128), TMA producer, MMA issuer (owns TMEM).
+// Warps: 0-3 softmax and epilogue, 4 TMA producer, 5 MMA issuer (owns TMEM).
 // What a row does not see reaches nothing of it: masked scores are replaced, and
 // rows of V that are no past key of the segment are zeroed in shared memory.  A
 // value that is NaN or infinite can still reach a row of its tile that the mask
@@ -50,16 +50,11 @@ struct WfCfg {
     static constexpr int kVSlots = D == 128 ? 2 : 3;
     static constexpr int kStages = D == 128 ? 2 : 1;               // of S
     static constexpr int kBlocksPerSm = D == 128 ? 2 : 3;
-    // threads per row, each with 64 / kHalves of a tile's keys: at D = 128, with two blocks per SM, two, which
-    // meet once per tile over the row maximum (one: 8 warps per SM, not enough to fill the issue slots)
-    static constexpr int kHalves = D == 128 ? 2 : 1;
-    static constexpr int kSoftWarps = 4 * kHalves;
-    static constexpr int kThreads = 32 * (kSoftWarps + 2);
+    static constexpr int kThreads = 192;
     static constexpr int kOffK = kQTile;
     static constexpr int kOffV = kOffK + kKSlots * kKvTile;
     static constexpr int kOffBar = kOffV + kVSlots * kKvTile;
-    static constexpr int kOffMax = kOffBar + 256;                  // [kHalves][128] halves of row maxima
-    static constexpr int kSmemBytes = kOffMax + (kHalves > 1 ? kHalves * kWinRes * 2 : 0);
+    static constexpr int kSmemBytes = kOffBar + 256;
     // TMEM columns: the S stages (P over the first half of each), then O
     static constexpr int kColO = kStages * kWinStr;
     static constexpr int kTmemCols = D == 128 ? 256 : 128;
@@ -104,17 +99,17 @@ __device__ __forceinline__ float wf_score(const __nv_bfloat16* q, const __nv_bfl
     return (a + b) * sl2;
 }
 
-// A row whose result is not finite, from its visible keys alone: O = sum_j 2^(s_j - lse) v_j, its vectors of
-// eight elements c0 .. c1 - 1 (one thread; rare, so not fast).
+// A row whose result is not finite, from its visible keys alone: O = sum_j 2^(s_j - lse) v_j, in pieces
+// of eight elements (one thread; rare, so not fast).
 template <int D>
-__device__ __noinline__ void win_row_again(const WfParams& p, int tok0, int n, int row, int h, float lse, int c0, int c1)
+__device__ __noinline__ void win_row_again(const WfParams& p, int tok0, int n, int row, int h, float lse)
 {
     const size_t tok = (size_t)tok0 + row;
     const __nv_bfloat16* q = p.q + (tok * p.H + h) * D;
     const int hk = h / p.G;
     const int lo = max(min(row, n) - p.window + 1, 0), hi = min(row + 1, n), sk = min(p.n_sinks, lo);
     const float nl = win_neg_lse(lse);
-    for (int c = c0; c < c1; ++c) {
+    for (int c = 0; c < D / 8; ++c) {
         float o[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = 0.f;
@@ -142,7 +137,7 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x / 32;
     const int lane = threadIdx.x % 32;
-    if (warp == C::kSoftWarps && lane == 0) {
+    if (warp == 4 && lane == 0) {
         tma_prefetch_map(&tm_q);
         tma_prefetch_map(&tm_k);
         tma_prefetch_map(&tm_v);
@@ -189,8 +184,7 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
     uint64_t* v_full = bars + 13;
     uint64_t* v_empty = bars + 16;
     uint64_t* o_done = bars + 19;      // the last P V: O is final
-    uint64_t* meet = bars + 20;        // [4] the warps that share 32 rows
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 24);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 20);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const bool leader = lane == 0;
     WaitCtl ctl{abort_flag, p.status, p.wait_limit_ns, (int)UNIPIN_ERR_DEVICE_TIMEOUT};
@@ -201,15 +195,14 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
     };
     auto load_k = [&](int i) { load_tile(tm_k, sK + i % C::kKSlots * C::kKvTile, k_full + i % C::kKSlots, i); };
     auto load_v = [&](int i) { load_tile(tm_v, sV + i % C::kVSlots * C::kKvTile, v_full + i % C::kVSlots, i); };
-    if (warp == C::kSoftWarps && leader) {
+    if (warp == 4 && leader) {
         mbar_init(bar_q, 1);
         mbar_init(bar_drain, 1);
         mbar_init(pv_done, 1);
         mbar_init(o_done, 1);
-        for (int x = 0; x < 4; ++x) mbar_init(meet + x, C::kHalves);
         for (int x = 0; x < 2; ++x) {
             mbar_init(s_ready + x, 1);
-            mbar_init(p_ready + x, C::kSoftWarps);
+            mbar_init(p_ready + x, 4);
         }
         for (int x = 0; x < 3; ++x) {
             mbar_init(k_full + x, 1);
@@ -230,7 +223,7 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
             }
         }
     }
-    if (warp == C::kSoftWarps + 1) {
+    if (warp == 5) {
         tmem_alloc(tmem_slot, C::kTmemCols);
         tmem_relinquish();
     }
@@ -239,7 +232,7 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
 
-    if (warp == C::kSoftWarps) {
+    if (warp == 4) {
         // ------------------------------------------------------------ producer
         // in the order in which the slots come free: V of a tile behind the P V of the tile kVSlots before,
         // K behind the (earlier) S of the tile kKSlots before
@@ -268,7 +261,7 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
             for (int i = max(nv - C::kVSlots, 0); i < nv; ++i)
                 mbar_wait_drain(v_full + i % C::kVSlots, (i / C::kVSlots) & 1, p.wait_limit_ns);
         }
-    } else if (warp == C::kSoftWarps + 1) {
+    } else if (warp == 5) {
         // --------------------------------------------------------- MMA issuer
         constexpr uint32_t idesc_s = idesc_bf16_f32(kWinRes, kWinStr, false);
         constexpr uint32_t idesc_o = idesc_bf16_f32(kWinRes, D, true);      // A from TMEM, B MN-major
@@ -312,7 +305,7 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
                 const uint64_t slot = (uint64_t)((i % C::kVSlots * C::kKvTile) >> 4);
 #pragma unroll
                 for (int kk = 0; kk < kWinStr / 16; ++kk)
-                    umma_bf16_ts(tmem + C::kColO, tmem + x * kWinStr + (C::kHalves == 2 ? kk / 2 * 32 + kk % 2 * 8 : kk * 8),
+                    umma_bf16_ts(tmem + C::kColO, tmem + x * kWinStr + kk * 8,
                                  d_v + slot + (uint64_t)((kk * 16 * C::kRowBytes) >> 4), idesc_o,
                                  (i > 0 || kk > 0) ? 1u : 0u);
                 umma_commit(v_empty + i % C::kVSlots);
@@ -333,18 +326,11 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
         }
     } else {
         // ------------------------------------------------- softmax + epilogue
-        constexpr int kCols = kWinStr / C::kHalves;  // keys of a tile, and
-        constexpr int kDims = D / C::kHalves;        // columns of O, that are this thread's
-        const int hf = warp / 4;
-        const int t = (warp % 4) * 32 + lane;
+        const int t = threadIdx.x;
         const int row = r0 + t;                      // within the segment
         const bool live = row < s.len;
-        const uint32_t lanes = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16);
-        const uint32_t tO = lanes + C::kColO + hf * kDims;
-        uint16_t* s_max = reinterpret_cast<uint16_t*>(smem + C::kOffMax);
-        volatile uint8_t* s_flag = reinterpret_cast<volatile uint8_t*>(bars + 25);   // [2][4][kHalves]
-        uint32_t n_meet = 0;
-        auto meet_rows = [&]() -> bool { return warp_group_sync(meet + warp % 4, n_meet, ctl, lane); };
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+        const uint32_t tO = lanes + C::kColO;
         const size_t at = ((size_t)s.tok0 + row) * p.H + h;
         const size_t at_kv = ((size_t)s.tok0 + row) * p.Hkv + h / p.G;
         const bool self = live && row >= s.n;        // a candidate: its own key
@@ -364,18 +350,16 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
             ok = __all_sync(0xffffffffu, mbar_wait(s_ready + x, (i / C::kStages) & 1, ctl));
             if (!ok) break;
             tc_fence_after_sync();
-            uint32_t sc[kCols];
-            if constexpr (kCols == 64) tmem_ld64(tS, sc);
-            else tmem_ld32(tS + hf * kCols, sc);
+            uint32_t sc[kWinStr];
+            tmem_ld64(tS, sc);
             // a warp's 32 rows by 32 keys at a time: under a short window a good part of a tile's have no
             // pair, and cost nothing
-            constexpr int kParts = kCols / 32;
-            uint32_t see[kParts];
-            bool some[kParts];
-            float m_tile = -INFINITY;
+            uint32_t see[2];
+            bool some[2];
+            float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-            for (int half = 0; half < kParts; ++half) {
-                const int c0 = row0 + hf * kCols + 32 * half;
+            for (int half = 0; half < 2; ++half) {
+                const int c0 = row0 + 32 * half;
                 see[half] = win_see32(lo - c0, hi - c0, p.n_sinks - c0);
                 some[half] = __any_sync(0xffffffffu, see[half] != 0u);
                 if (!some[half]) continue;
@@ -391,42 +375,20 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
                     m0 = max3f<true>(m0, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
                     m1 = max3f<true>(m1, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
                 }
-                m_tile = fmax_nan(m_tile, fmax_nan(m0, m1));
+                mx[half] = fmax_nan(m0, m1);
             }
-            m_tile *= sl2;
+            const float m_tile = fmax_nan(mx[0], mx[1]) * sl2;
             odd = odd || !(m_tile < INFINITY);
             // move the reference max only when some row of the warp would see P > 2^8
-            bool grow = __any_sync(0xffffffffu, m_tile > m + kWfRescaleLog2);
-            if constexpr (C::kHalves == 2) {
-                // .. or of the warp with the rows' other keys: the two keep one reference
-                if (lane == 0) s_flag[((i & 1) * 4 + warp % 4) * 2 + hf] = grow;
-                if (!(ok = meet_rows())) break;
-                grow = s_flag[((i & 1) * 4 + warp % 4) * 2] | s_flag[((i & 1) * 4 + warp % 4) * 2 + 1];
-            }
-            if (grow) {
-                float top = m_tile;
-                if constexpr (C::kHalves == 2) {
-                    // the maximum over both, in two halves of its bits (shared memory for one is left)
-                    const uint32_t mine = __float_as_uint(m_tile);
-                    uint32_t other = 0u;
-#pragma unroll
-                    for (int part = 0; part < 2; ++part) {
-                        s_max[hf * kWinRes + t] = (uint16_t)(mine >> (16 * part));
-                        if (!(ok = meet_rows())) break;
-                        other |= (uint32_t)s_max[(1 - hf) * kWinRes + t] << (16 * part);
-                        if (!(ok = meet_rows())) break;   // both have read
-                    }
-                    if (!ok) break;
-                    top = fmax_nan(m_tile, __uint_as_float(other));
-                }
-                const float m_new = fmaxf(m, top);
+            if (__any_sync(0xffffffffu, m_tile > m + kWfRescaleLog2)) {
+                const float m_new = fmaxf(m, m_tile);
                 const float corr = m == -INFINITY ? 0.f : ex2_approx(m - m_new);
                 if (i > 0) {
                     ok = __all_sync(0xffffffffu, mbar_wait(pv_done, (i - 1) & 1, ctl));
                     if (!ok) break;
                     tc_fence_after_sync();
 #pragma unroll
-                    for (int c = 0; c < kDims; c += 8) {
+                    for (int c = 0; c < D; c += 8) {
                         uint32_t o[8];
                         tmem_ld8(tO + c, o);
 #pragma unroll
@@ -442,7 +404,7 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
             // prefill, the issue slots and not the MUFU were the limit here
             const uint64_t sc2 = f2_pack(sl2, sl2), nm2 = f2_pack(-m_use, -m_use);
 #pragma unroll
-            for (int half = 0; half < kParts; ++half) {
+            for (int half = 0; half < 2; ++half) {
                 uint32_t pk[16];
                 if (some[half]) {
                     uint64_t acc[2] = {0ull, 0ull};
@@ -463,16 +425,15 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
 #pragma unroll
                     for (int c = 0; c < 16; ++c) pk[c] = 0u;
                 }
-                // P over S: over columns that this warp has read, 16 per 32 keys
-                if (half + 1 < kParts) tmem_st16_nowait(tS + hf * kCols + half * 16, pk);
-                else tmem_st16(tS + hf * kCols + half * 16, pk);
+                if (half == 0) tmem_st16_nowait(tS, pk);
+                else tmem_st16(tS + 16, pk);
             }
             ok = __all_sync(0xffffffffu, mbar_wait(v_full + i % C::kVSlots, (i / C::kVSlots) & 1, ctl));
             if (!ok) break;
             // rows of V that are no past key of the segment become zeros
             const int end = s.n - row0;
             if (end < kWinStr) {
-                if (hf == 0 && t < kWinStr && t >= end) {
+                if (t < kWinStr && t >= end) {
                     uint8_t* dst = sV + (i % C::kVSlots) * C::kKvTile + t * C::kRowBytes;
 #pragma unroll
                     for (int c = 0; c < C::kBoxes; ++c)
@@ -486,22 +447,15 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
             __syncwarp();
             if (lane == 0) mbar_arrive(p_ready + x);
         }
-        // the own value is fetched before O is waited for
-        uint4 own[kDims / 8];
+        // the own value (half of it at D = 128, for the registers) is fetched before O is waited for
+        constexpr int kAhead = D / 8 < 8 ? D / 8 : 8;
+        uint4 own[kAhead];
 #pragma unroll
-        for (int c = 0; c < kDims / 8; ++c)
-            own[c] = self ? __ldg(reinterpret_cast<const uint4*>(p.v + at_kv * D + hf * kDims) + c)
-                          : make_uint4(0u, 0u, 0u, 0u);
+        for (int c = 0; c < kAhead; ++c)
+            own[c] = self ? __ldg(reinterpret_cast<const uint4*>(p.v + at_kv * D) + c) : make_uint4(0u, 0u, 0u, 0u);
         if (ok && total > 0) {
             ok = __all_sync(0xffffffffu, mbar_wait(o_done, 0, ctl));
             tc_fence_after_sync();
-        }
-        if constexpr (C::kHalves == 2) {
-            // the row's whole sum; K's ring is free (every product has run)
-            float* s_sum = reinterpret_cast<float*>(sK);
-            s_sum[hf * kWinRes + t] = odd ? __int_as_float(0x7fffffff) : l;
-            ok = ok && meet_rows();
-            l = s_sum[t] + s_sum[kWinRes + t];
         }
         if (ok) {
             const float m_fin = fmaxf(m, ss);
@@ -511,11 +465,16 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
             const float denom = l * a + w;
             const float inv = denom == 0.f ? 0.f : 1.f / denom;
             const float lse = m_fin + log2f(denom);
-            if (live && hf == 0 && p.lse) p.lse[at] = lse;
+            if (live && p.lse) p.lse[at] = lse;
             float chk = 0.f;     // NaN once an element is not finite
 #pragma unroll
-            for (int c = 0; c < kDims / 32; ++c) {
+            for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
+                if (c * 4 == kAhead) {
+#pragma unroll
+                    for (int i = 0; i < kAhead; ++i)
+                        if (self) own[i] = __ldg(reinterpret_cast<const uint4*>(p.v + at_kv * D) + kAhead + i);
+                }
                 if (total > 0) {
                     tmem_ld32(tO + c * 32, o);       // warp-collective: every lane loads
                 } else {
@@ -529,7 +488,7 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
 #pragma unroll
                     for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(o[g * 8 + e]) * a;
                     if (self) {
-                        win_unpack8(own[c * 4 + g], vf);
+                        win_unpack8(own[(c * 4 + g) % kAhead], vf);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) f[e] = fmaf(w, vf[e], f[e]);
                     }
@@ -538,16 +497,16 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
                         f[e] *= inv;
                         chk = fmaf(f[e], 0.f, chk);
                     }
-                    win_store8(p.out, p.out_fp32, at * D + hf * kDims + c * 32 + g * 8, f);
+                    win_store8(p.out, p.out_fp32, at * D + c * 32 + g * 8, f);
                 }
             }
-            if (chk != chk) win_row_again<D>(p, s.tok0, s.n, row, h, lse, hf * kDims / 8, (hf + 1) * kDims / 8);
+            if (chk != chk) win_row_again<D>(p, s.tok0, s.n, row, h, lse);
         }
     }
 
     tc_fence_before_sync();
     __syncthreads();
-    if (warp == C::kSoftWarps + 1) {
+    if (warp == 5) {
         __syncwarp();
         tc_fence_after_sync();
         tmem_dealloc(tmem, C::kTmemCols);
