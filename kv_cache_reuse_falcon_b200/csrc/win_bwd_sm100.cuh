@@ -81,6 +81,11 @@ struct WbCfg {
     static constexpr int kColAcc0 = 128 * kStages;
     static constexpr int kColAcc1 = kColAcc0 + D;
     static constexpr int kTmemCols = D == 128 ? 512 : 256;
+    // P and dS (dQ: dS in two parts) in columns of their own where some are left: a dQ block has one sum
+    // only, and at D = 32 there is room in either kind.  The next S and dP of a stage then wait for its
+    // scores to be read, not for the products that read P and dS.
+    static __device__ constexpr bool apart(bool kv) { return !kv || D == 32; }
+    static __device__ constexpr int col_apart(int x) { return D == 32 ? 192 : kColAcc0 + 64 * x; }
     static_assert(kColAcc1 + D <= kTmemCols, "TMEM budget");
     static_assert(kSmemBytes * kBlocksPerSm <= 226 * 1024, "shared memory budget");
 };
@@ -279,11 +284,12 @@ __device__ __forceinline__ uint32_t wb_sign_pair(uint32_t a, uint32_t b)
 }
 
 // One softmax pass over half a streamed tile: P and dS of this thread's resident row over 32 of the 64
-// streamed rows, from S and dP in TMEM (32 columns at tS and at tS + 64) and back as bfloat16 pairs over
-// the first 16 of those columns.  `see`: the columns that are allowed pairs.  kKV: -lse and -Dvec per
+// streamed rows, from S and dP in TMEM (32 columns at tS and at tS + 64) and back as bfloat16 pairs, P to
+// tP and dS to tD (dQ: the lower part of dS and the upper).  read(): the scores have been read; free(): the
+// columns written may be (false: a timeout).  `see`: the columns that are allowed pairs.  kKV: -lse and -Dvec per
 // column from shared memory, otherwise this row's own.
-template <bool kKV>
-__device__ __forceinline__ void wb_softmax(uint32_t tS, float sl2, const float* nlse, const float* ndvec, float nl,
+template <bool kKV, typename Read, typename Free>
+__device__ __forceinline__ bool wb_softmax(uint32_t tS, uint32_t tP, uint32_t tD, Read read, Free free, float sl2, const float* nlse, const float* ndvec, float nl,
                                            float nd, uint32_t see)
 {
     const uint64_t sc = f2_pack(sl2, sl2);
@@ -293,11 +299,14 @@ __device__ __forceinline__ void wb_softmax(uint32_t tS, float sl2, const float* 
     if (!__any_sync(0xffffffffu, see != 0u)) {       // no pair of these 32 x 32
 #pragma unroll
         for (int i = 0; i < 16; ++i) pk[i] = 0u;
-        tmem_st16_nowait(tS, pk);
-        tmem_st16(tS + kWinStr, pk);
-        return;
+        read();
+        if (!free()) return false;
+        tmem_st16_nowait(tP, pk);
+        tmem_st16(tD, pk);
+        return true;
     }
     tmem_ld32x2(tS, sr, tS + kWinStr, dr);
+    read();
 #pragma unroll
     for (int e = 0; e < 32; e += 4) {
         uint64_t a[2], b[2];
@@ -334,8 +343,10 @@ __device__ __forceinline__ void wb_softmax(uint32_t tS, float sl2, const float* 
             }
         }
     }
-    tmem_st16_nowait(tS, pk);
-    tmem_st16(tS + kWinStr, dk);
+    if (!free()) return false;
+    tmem_st16_nowait(tP, pk);
+    tmem_st16(tD, dk);
+    return true;
 }
 
 template <int D, bool kKV>
@@ -370,13 +381,16 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
     uint64_t* s_ready = bars + 3;      // [2]
     uint64_t* p_ready = bars + 5;      // [2]
     uint64_t* grp = bars + 7;          // [2]
-    uint64_t* full = bars + 9;         // [kSlots]
+    uint64_t* s_free = bars + 9;       // [2] a stage's scores have been read (apart)
+    uint64_t* p_free = bars + 11;      // [2] .. its P and dS (apart)
+    uint64_t* full = bars + 13;        // [kSlots]
     uint64_t* empty = full + C::kSlots;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(empty + C::kSlots);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     volatile int* last_piece = reinterpret_cast<volatile int*>(tmem_slot + 2);   // [2]
     WaitCtl ctl{abort_flag, p.status, p.wait_limit_ns, (int)UNIPIN_ERR_DEVICE_TIMEOUT};
     const bool leader = lane == 0;
+    constexpr bool kApart = C::apart(kKV);
     // streamed tile i = tile `idx` of query head `g` of the group, into its ring slot
     auto load_tile = [&](int i, int g, int idx) {
         const int st = i % C::kSlots;
@@ -400,6 +414,8 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
                 mbar_init(s_ready + x, 1);
                 mbar_init(p_ready + x, 8);
                 mbar_init(grp + x, 8);
+                mbar_init(s_free + x, 8);
+                mbar_init(p_free + x, 1);
             }
             for (int x = 0; x < C::kSlots; ++x) {
                 mbar_init(full + x, 1);
@@ -490,8 +506,14 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
         for (int i = 0; ok && i < total; ++i) {
             const int x = i % C::kStages, st = i % C::kSlots;
             // kSlots > kStages: the later tile's load does not need this tile's slot
-            ok = landed(i + C::kStages) &&
-                 __all_sync(0xffffffffu, mbar_wait(p_ready + x, (i / C::kStages) & 1, ctl));
+            if (!(ok = landed(i + C::kStages))) break;
+            if (kApart && i + C::kStages < total) {
+                ok = __all_sync(0xffffffffu, mbar_wait(s_free + x, (i / C::kStages) & 1, ctl));
+                if (!ok) break;
+                tc_fence_after_sync();
+                scores(i + C::kStages);
+            }
+            ok = __all_sync(0xffffffffu, mbar_wait(p_ready + x, (i / C::kStages) & 1, ctl));
             if (!ok) break;
             tc_fence_after_sync();
             if (elect_one()) {
@@ -499,17 +521,19 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
 #pragma unroll
                 for (int kk = 0; kk < kWinStr / 16; ++kk) {
                     // 16 streamed rows: 8 columns of pairs, those of rows 32.. at column 32
-                    const uint32_t tS = tmem + x * 128 + (kk / 2) * 32 + (kk % 2) * 8;
+                    const uint32_t tP = tmem + (kApart ? C::col_apart(x) + kk * 8 : x * 128 + (kk / 2) * 32 + (kk % 2) * 8);
+                    const uint32_t tD = tP + (kApart ? 32 : kWinStr);
                     const uint64_t off = slot + (uint64_t)((kk * 16 * C::kRowBytes) >> 4);
                     const uint32_t acc = (i > 0 || kk > 0) ? 1u : 0u;
-                    if (kKV) umma_bf16_ts(tmem + C::kColAcc0, tS, d_g1 + off, idesc_g, acc);
-                    umma_bf16_ts(tmem + C::kColAcc1, tS + kWinStr, d_g0 + off, idesc_g, acc);
-                    if (!kKV) umma_bf16_ts(tmem + C::kColAcc1, tS, d_g0 + off, idesc_g, 1u);   // the lower part
+                    if (kKV) umma_bf16_ts(tmem + C::kColAcc0, tP, d_g1 + off, idesc_g, acc);
+                    umma_bf16_ts(tmem + C::kColAcc1, tD, d_g0 + off, idesc_g, acc);
+                    if (!kKV) umma_bf16_ts(tmem + C::kColAcc1, tP, d_g0 + off, idesc_g, 1u);   // the lower part
                 }
                 umma_commit(empty + st);
+                if (kApart) umma_commit(p_free + x);
                 if (i + 1 == total) umma_commit(acc_done);
             }
-            if (i + C::kStages < total) {
+            if (!kApart && i + C::kStages < total) {
                 // only products into one accumulator are sure to run in order: S and dP over P and dS wait
                 // for the products that read those
                 ok = __all_sync(0xffffffffu, mbar_wait(empty + st, (i / C::kSlots) & 1, ctl));
@@ -578,7 +602,23 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
             ok = __all_sync(0xffffffffu, mbar_wait(s_ready + x, k & 1, ctl));
             if (!ok) break;
             tc_fence_after_sync();
-            wb_softmax<kKV>(lanes + x * 128 + half * 32, p.sl2, st + half * 32, st + kWinStr + half * 32, nl, nd, see);
+            const uint32_t tS = lanes + x * 128 + half * 32;
+            const uint32_t tP = kApart ? lanes + C::col_apart(x) + half * 16 : tS;
+            auto read = [&]() {
+                if (!kApart) return;
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s_free + x);
+            };
+            auto free = [&]() -> bool {
+                if (!kApart || k == 0) return true;
+                if (!__all_sync(0xffffffffu, mbar_wait(p_free + x, (k - 1) & 1, ctl))) return false;
+                tc_fence_after_sync();
+                return true;
+            };
+            ok = wb_softmax<kKV>(tS, tP, tP + (kApart ? 32 : kWinStr), read, free, p.sl2, st + half * 32,
+                                 st + kWinStr + half * 32, nl, nd, see);
+            if (!ok) break;
             // streamed rows that are no row (KV: behind the segment) or no past key (dQ) become zeros
             const int end = (kKV ? s.len : s.n) - row0;
             if (end < kWinStr) {
