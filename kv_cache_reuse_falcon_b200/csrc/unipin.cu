@@ -335,9 +335,20 @@ int launch_win_bwd(const CUtensorMap (&m)[8], const WbParams& p, unsigned prep_b
 {
     win_bwd_prep_kernel<D><<<dim3(prep_blocks, (unsigned)p.B, 1), kWbPrepThreads, 0, s>>>(p);
     if (cudaGetLastError() != cudaSuccess) return UNIPIN_ERR_CUDA;
-    win_bwd_kernel<D><<<blocks, WbCfg<D>::kThreads, WbCfg<D>::kSmemBytes, s>>>(m[0], m[1], m[2], m[3], m[4], m[5],
-                                                                               m[6], m[7], p);
-    return cudaGetLastError() == cudaSuccess ? UNIPIN_OK : UNIPIN_ERR_CUDA;
+    // may begin while the prep kernel drains (it waits for its results itself)
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks, 1, 1);
+    cfg.blockDim = dim3(WbCfg<D>::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = WbCfg<D>::kSmemBytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, win_bwd_kernel<D>, m[0], m[1], m[2], m[3], m[4], m[5], m[6], m[7], p) == cudaSuccess
+               ? UNIPIN_OK
+               : UNIPIN_ERR_CUDA;
 }
 
 int decode_nsplit(int R, int H, int D, int max_k, int n_cap, int sms)

@@ -128,6 +128,9 @@ __global__ void __launch_bounds__(kWbPrepThreads, 4) win_bwd_prep_kernel(const W
 {
     constexpr int L = D / 8;
     constexpr int kGroups = kWbPrepThreads / L;
+    // the main kernel may start: its loads and first products need nothing from here, and what does waits
+    // for this kernel's end
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     for (long long i = ((long long)blockIdx.y * gridDim.x + blockIdx.x) * kWbPrepThreads + threadIdx.x; i < p.n_counters;
          i += (long long)gridDim.x * gridDim.y * kWbPrepThreads)
         p.counters[i] = 0u;
@@ -367,7 +370,10 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
     WbItem it;
     WinSegment s;
     const bool work = wb_item<kKV>(p, block, it, s);
-    if (!work || failed == (int)UNIPIN_ERR_DEVICE_TIMEOUT) return;
+    if (!work || failed == (int)UNIPIN_ERR_DEVICE_TIMEOUT) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");   // no block ends before the prep kernel
+        return;
+    }
     const int cnt = it.sweep.cnt;
     const int total = it.total;
 
@@ -553,6 +559,7 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
         const int t = (warp % 4) * 32 + lane;        // resident row
         const uint32_t lanes = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16);
         const int row = it.r0 + t;                   // within the segment
+        asm volatile("griddepcontrol.wait;" ::: "memory");   // Dvec, dself and the counters
         const bool live = row < (kKV ? s.n : s.len);
         float nl = 0.f, nd = 0.f;
         // the resident row's allowed streamed rows: r < hi with r >= lo or r < sk
