@@ -205,20 +205,6 @@ int launch_decode_mode(int mode, bool wide, const PgParams& p, cudaStream_t s)
     }
 }
 
-// j / d = umulhi(j, mul) >> shift for 0 <= j < 2^31 and d >= 2: with s = ceil(log2 d) and
-// mul = floor(2^(31 + s) / d) + 1 <= 2^32 - 1 the product exceeds 2^(31 + s) j / d by at most
-// j < 2^31 <= 2^(31 + s) / d, too little to reach the next quotient.
-void set_divisor(PgParams* p, int d)
-{
-    p->ps_mul = 0;
-    p->ps_shift = 0;
-    if (d < 2) return;
-    int s = 0;
-    while ((1ll << s) < d) ++s;
-    p->ps_mul = (uint32_t)((1ull << (31 + s)) / (uint64_t)d + 1);
-    p->ps_shift = s - 1;
-}
-
 }  // namespace
 
 extern "C" {
@@ -258,6 +244,8 @@ int unipin_paged_pool_write(const unipin_kvpool* pool, int layer, const void* k,
     p.ps = pool->n_cap;
     p.max_pages = max_pages;
     p.max_new = max_new;
+    p.page_of = pg_divisor(pool->n_cap);
+    p.token_of = pg_divisor(pool->H * (pool->D / 8));
     p.total_tokens = total_tokens;
     p.status = dev_status;
     const dim3 grid((unsigned)blocks, (unsigned)B, 1);
@@ -331,7 +319,7 @@ int unipin_paged_decode_attn(const void* q, const void* k_self, const void* v_se
     p.G = G;
     p.S = pool->S;
     p.ps = pool->n_cap;
-    set_divisor(&p, pool->n_cap);
+    p.page_of = pg_divisor(pool->n_cap);
     p.max_pages = max_pages;
     p.max_len = max_len;
     p.window = window;
@@ -408,6 +396,7 @@ int unipin_paged_evict(const unipin_kvpool* pool, int layer, float* key_weights,
     p.n_sinks = n_sinks;
     p.n_recent = n_recent;
     p.row_bytes = (int)(pool->D * elt_bytes(pool));
+    p.page_of = pg_divisor(pool->n_cap);
     p.status = dev_status;
     p.keys_cap = max_len < kSelKeysCap ? max_len : kSelKeysCap;
     cudaStream_t s = static_cast<cudaStream_t>(stream);

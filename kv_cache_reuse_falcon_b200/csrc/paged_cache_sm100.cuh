@@ -8,6 +8,7 @@
 #include <cuda_bf16.h>
 
 #include "e4m3.cuh"
+#include "paged_common.cuh"
 #include "sm100_ptx.cuh"
 #include "unipin.h"
 
@@ -26,6 +27,7 @@ struct PgWriteParams {
     const int* first;      // [B] cache row of the first one
     float* key_weights;    // the layer's [S, H, ps] or null: the written rows' weights become 0
     int H, D, S, ps, max_pages, max_new, total_tokens;
+    PgDiv page_of, token_of;   // division by the rows of a page, and by a token's vectors
     float inv_k, inv_v;    // E4M3
     int* status;
 };
@@ -52,30 +54,34 @@ __global__ void __launch_bounds__(kPgWriteThreads) paged_write_kernel(const PgWr
         if (threadIdx.x == 0 && blockIdx.x == 0) report(p.status, (int)UNIPIN_ERR_OUT_OF_RANGE);
         return;
     }
-    const int vpr = p.D / 8;                  // vectors of a head's row
+    const int vpr = p.D / 8;                  // vectors of a head's row (a power of two)
+    const int vpr_shift = 31 - __clz(vpr);
     const int vpt = p.H * vpr;                // vectors of a token
-    const long long total = (long long)n * vpt;
-    const long long base = (long long)blockIdx.x * (kPgWriteThreads * kPgWriteVecs) + threadIdx.x;
-    const uint4* k = p.k + (long long)start * vpt;
-    const uint4* v = p.v + (long long)start * vpt;
+    // the block's first token, and where in it the block begins; behind it 32 bits are enough
+    const long long base = (long long)blockIdx.x * (kPgWriteThreads * kPgWriteVecs);
+    const int j0 = (int)(base / vpt);
+    const int rest0 = (int)(base - (long long)j0 * vpt) + threadIdx.x;
+    const uint4* k = p.k + (long long)start * vpt + base + threadIdx.x;
+    const uint4* v = p.v + (long long)start * vpt + base + threadIdx.x;
     uint4 kk[kPgWriteVecs], vv[kPgWriteVecs];
+    int j[kPgWriteVecs], rest[kPgWriteVecs];
 #pragma unroll
     for (int i = 0; i < kPgWriteVecs; ++i) {
-        const long long x = base + i * kPgWriteThreads;
-        if (x < total) {
-            kk[i] = __ldg(k + x);
-            vv[i] = __ldg(v + x);
+        const int y = rest0 + i * kPgWriteThreads;
+        j[i] = p.token_of(y);
+        rest[i] = y - j[i] * vpt;
+        j[i] += j0;
+        if (j[i] < n) {
+            kk[i] = __ldg(k + i * kPgWriteThreads);
+            vv[i] = __ldg(v + i * kPgWriteThreads);
         }
     }
 #pragma unroll
     for (int i = 0; i < kPgWriteVecs; ++i) {
-        const long long x = base + i * kPgWriteThreads;
-        if (x >= total) break;
-        const int j = (int)(x / vpt);
-        const int rest = (int)(x - (long long)j * vpt);
-        const int h = rest / vpr, c = rest - h * vpr;
-        const int row = first + j;
-        const int pg = row / p.ps;
+        if (j[i] >= n) break;
+        const int h = rest[i] >> vpr_shift, c = rest[i] & (vpr - 1);
+        const int row = first + j[i];
+        const int pg = p.page_of(row);
         const int page = __ldg(p.table + (size_t)b * p.max_pages + pg);
         if (page < 0 || page >= p.S) {
             report(p.status, (int)UNIPIN_ERR_OUT_OF_RANGE);
@@ -121,6 +127,7 @@ struct PgEvictParams {
     int* new_lens;         // [R]
     int H, S, ps, max_pages, max_len, budget, n_sinks, n_recent;
     int row_bytes;
+    PgDiv page_of;         // division by ps
     int keys_cap;          // keys that fit the shared-memory copy
     int* status;
 };
@@ -174,7 +181,7 @@ __global__ void __launch_bounds__(kPgSelThreads) paged_evict_select_kernel(const
         return;
     }
     auto slot = [&](int j) -> float* {
-        const int pg = j / p.ps;
+        const int pg = p.page_of(j);
         return p.key_weights + ((size_t)__ldg(table + pg) * p.H + h) * p.ps + (j - pg * p.ps);
     };
     const int m0 = p.n_sinks, mid = n - p.n_sinks - p.n_recent;   // n > budget >= n_sinks + n_recent
@@ -291,7 +298,7 @@ __global__ void __launch_bounds__(kPgMoveThreads) paged_evict_move_kernel(const 
     const int c = threadIdx.x % kVec, row = threadIdx.x / kVec;
     const size_t col = ((size_t)slice * kVec + c) * 16;
     auto addr = [&](int j) -> uint4* {
-        const int pg = j / p.ps;
+        const int pg = p.page_of(j);
         const size_t at = ((size_t)__ldg(table + pg) * p.H + h) * p.ps + (j - pg * p.ps);
         return reinterpret_cast<uint4*>(pool + at * p.row_bytes + col);
     };

@@ -59,6 +59,7 @@
 #include <cuda_fp16.h>
 
 #include "e4m3.cuh"
+#include "paged_common.cuh"
 #include "sm100_ptx.cuh"
 #include "unipin.h"
 
@@ -111,8 +112,7 @@ struct PgParams {
     float* row_lse;                // [R * H] log2 of a finished row's weight sum; +inf: rejected (key_weights)
     float* scores;                 // [R * H, vmax] log2-unit scores of the visible rows (key_weights)
     int R, H, Hkv, G, S, ps, max_pages, max_len;
-    uint32_t ps_mul;               // j / ps = umulhi(j, ps_mul) >> ps_shift; 0: ps = 1
-    int ps_shift;
+    PgDiv page_of;                 // division by ps
     int unit_shift;                // log2 of a unit's rows
     int window, n_sinks;
     int heads;                     // query heads of a unit: min(G, 16)
@@ -151,11 +151,6 @@ __device__ __forceinline__ PgRows pg_rows(const PgParams& p, int r)
 __device__ __forceinline__ int pg_units(const PgParams& p, int vis)
 {
     return max((vis + (1 << p.unit_shift) - 1) >> p.unit_shift, 1);
-}
-
-__device__ __forceinline__ int pg_page(const PgParams& p, int j)
-{
-    return p.ps_mul ? (int)(__umulhi((uint32_t)j, p.ps_mul) >> p.ps_shift) : j;
 }
 
 // A place in the sequence of units: request r, key/value head hk, head group cg, unit t of u.
@@ -446,7 +441,7 @@ __global__ void __launch_bounds__(kPgThreads, PgCfg<D, kMode>::kBlocksPerSm) pag
         row_bad = false;
         if (row_live) {
             const int j = ld.rows.row(v);
-            const int pg = pg_page(p, j);
+            const int pg = p.page_of(j);
             const int page = __ldg(p.table + (size_t)ld.r * p.max_pages + pg);
             row_bad = page < 0 || page >= p.S;
             if (row_bad) row_live = false;
@@ -952,7 +947,7 @@ __global__ void __launch_bounds__(32 * kPgJoinWarps) paged_join_kernel(const PgP
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int j = rows.row(min(v + i, rows.vis - 1));
-        const int pg = pg_page(p, j);
+        const int pg = p.page_of(j);
         dst[i] = p.key_weights + ((size_t)__ldg(table + pg) * p.Hkv + hkv) * p.ps + (j - pg * p.ps);
     }
     // atomic: requests may share pages (a common prefix)
