@@ -405,9 +405,9 @@ int unipin_paged_evict(const unipin_kvpool* pool, int layer, float* key_weights,
     if (max_len <= budget) return UNIPIN_OK;
     if (p.row_bytes >= 64)
         return launch_dependent(paged_evict_move_kernel<4>,
-                                dim3((unsigned)(2 * p.row_bytes / 64), (unsigned)pool->H, (unsigned)R), kPgMoveThreads,
+                                dim3((unsigned)(2 * p.row_bytes / 64 + 1), (unsigned)pool->H, (unsigned)R), kPgMoveThreads,
                                 0, s, p);
-    return launch_dependent(paged_evict_move_kernel<2>, dim3(2, (unsigned)pool->H, (unsigned)R), kPgMoveThreads, 0, s,
+    return launch_dependent(paged_evict_move_kernel<2>, dim3(3, (unsigned)pool->H, (unsigned)R), kPgMoveThreads, 0, s,
                             p);
 }
 

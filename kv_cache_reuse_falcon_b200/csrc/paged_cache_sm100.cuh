@@ -108,13 +108,13 @@ __global__ void __launch_bounds__(kPgWriteThreads) paged_write_kernel(const PgWr
 //
 // paged_evict_select_kernel: one block per (request, head).  The weights of the middle rows become
 // order-preserving 32-bit keys; the need-th largest is found by radix selection, eight bits a pass
-// (a histogram of the keys that still match), from a copy in shared memory where it fits.  A pass
-// over the rows in order then writes the kept rows' indices (ballots and a block-wide prefix give
-// each its place; ties are counted in row order), and moves the weights: a row moves only towards
-// the front, and a step's loads all precede its stores, so it can be done in place.
-// paged_evict_move_kernel: the same move for a slice of the bytes of every K or V row.  Rows move in
-// order within a slice and slices do not touch each other, so the move is in place with one barrier
-// per step, and slices, heads and requests give the blocks that fill the memory.
+// (a histogram of the keys that still match; the lanes of a warp with one digit add once: the first
+// digits of attention weights are nearly all equal), from a copy in shared memory where it fits.  Then
+// each warp counts what stays of its consecutive share of the rows, one scan over the warps gives each
+// its place (and its share of the ties, in row order), and it writes the rows' numbers there.
+// paged_evict_move_kernel: moves a slice of the bytes of every K or V row, or the weights.  Rows move
+// towards the front and in order within a slice, and slices do not touch each other, so the move is in
+// place with one barrier per step, and slices, heads and requests give the blocks that fill the memory.
 // Bound: memory (the weights once, the kept rows read and written once).
 
 struct PgEvictParams {
@@ -191,13 +191,18 @@ __global__ void __launch_bounds__(kPgSelThreads) paged_evict_select_kernel(const
     if (cached)
         for (int i = tid; i < mid; i += kPgSelThreads) s_keys[i] = pg_order_key(*slot(m0 + i));
     uint32_t prefix = 0, mask = 0;
-    if (need > 0) {
+    const bool any = need > 0;
+    if (any) {
         for (int shift = 24; shift >= 0; shift -= 8) {
             for (int i = tid; i < 256; i += kPgSelThreads) hist[i] = 0;
             __syncthreads();
-            for (int i = tid; i < mid; i += kPgSelThreads) {
-                const uint32_t x = key(i);
-                if ((x & mask) == prefix) atomicAdd(&hist[(x >> shift) & 255u], 1u);
+            for (int i0 = 0; i0 < mid; i0 += kPgSelThreads) {
+                const int i = i0 + tid;
+                const uint32_t x = i < mid ? key(i) : 0u;
+                const bool in = i < mid && (x & mask) == prefix;
+                const uint32_t digit = in ? (x >> shift) & 255u : 256u;
+                const uint32_t same = __match_any_sync(0xffffffffu, digit);
+                if (in && lane == __ffs(same) - 1) atomicAdd(&hist[digit], (uint32_t)__popc(same));
             }
             __syncthreads();
             if (warp == 0) {
@@ -229,94 +234,111 @@ __global__ void __launch_bounds__(kPgSelThreads) paged_evict_select_kernel(const
             need = s_need;
             mask |= 255u << shift;
         }
+    } else {
+        __syncthreads();
     }
     // every key above `prefix` stays, and the first `need` rows whose key equals it
-    const bool any = p.budget - p.n_sinks - p.n_recent > 0;
-    uint32_t ties = 0;       // ties seen before this step
-    int at = 0;              // rows kept before this step
+    const int share = ((n + kPgSelThreads - 1) / kPgSelThreads) * 32;     // rows of a warp, whole groups of 32
+    const int j0 = min(warp * share, n), j1 = min(j0 + share, n);
+    auto look = [&](int j, bool& keep, bool& tie) {
+        keep = tie = false;
+        if (j >= j1) return;
+        if (j < m0 || j >= n - p.n_recent) {
+            keep = true;
+        } else if (any) {
+            const uint32_t x = key(j - m0);
+            keep = x > prefix;
+            tie = x == prefix;
+        }
+    };
+    int n_keep = 0, n_tie = 0;
+    for (int j = j0; j < j1; j += 32) {
+        bool keep, tie;
+        look(j + lane, keep, tie);
+        n_keep += __popc(__ballot_sync(0xffffffffu, keep));
+        n_tie += __popc(__ballot_sync(0xffffffffu, tie));
+    }
+    if (lane == 0) {
+        w_keep[warp] = n_keep;
+        w_tie[warp] = n_tie;
+    }
     __syncthreads();
-    for (int j0 = 0; j0 < n; j0 += kPgSelThreads) {
-        const int j = j0 + tid;
-        bool keep = false, tie = false;
-        float w = 0.f;
-        if (j < n) {
-            w = *slot(j);
-            if (j < m0 || j >= n - p.n_recent) {
-                keep = true;
-            } else if (any) {
-                const uint32_t x = pg_order_key(w);
-                keep = x > prefix;
-                tie = x == prefix;
-            }
+    int ties = 0, at = 0;    // ties and kept rows before this warp's
+    {
+        const int tw = w_tie[lane], kw = w_keep[lane];
+        int incl = tw;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += up;
         }
+        const int stay = kw + max(min((int)need - (incl - tw), tw), 0);   // rows of warp `lane` that stay
+        int kept_incl = stay;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, kept_incl, off);
+            if (lane >= off) kept_incl += up;
+        }
+        ties = __shfl_sync(0xffffffffu, incl - tw, warp);
+        at = __shfl_sync(0xffffffffu, kept_incl - stay, warp);
+    }
+    for (int j = j0; j < j1; j += 32) {
+        bool keep, tie;
+        look(j + lane, keep, tie);
+        const uint32_t below = (1u << lane) - 1u;
         const uint32_t tb = __ballot_sync(0xffffffffu, tie);
-        if (lane == 0) w_tie[warp] = __popc(tb);
-        __syncthreads();
-        int tbase = (int)ties, tall = 0;
-        for (int x = 0; x < 32; ++x) {
-            const int c = w_tie[x];
-            if (x < warp) tbase += c;
-            tall += c;
-        }
-        if (tie && (uint32_t)(tbase + __popc(tb & ((1u << lane) - 1u))) < need) keep = true;
+        if (tie && ties + __popc(tb & below) < (int)need) keep = true;
+        ties += __popc(tb);
         const uint32_t kb = __ballot_sync(0xffffffffu, keep);
-        if (lane == 0) w_keep[warp] = __popc(kb);
-        __syncthreads();       // also: every load of this step precedes its stores
-        int kbase = at, kall = 0;
-        for (int x = 0; x < 32; ++x) {
-            const int c = w_keep[x];
-            if (x < warp) kbase += c;
-            kall += c;
-        }
-        if (keep) {
-            const int i = kbase + __popc(kb & ((1u << lane) - 1u));
-            kept[i] = j;
-            if (i != j) *slot(i) = w;
-        }
-        ties += (uint32_t)tall;
-        at += kall;
-        // the next step's ballot counts overwrite w_tie only after every thread has read them
-        // (the barrier above), and w_keep after the next step's first barrier
+        if (keep) kept[at + __popc(kb & below)] = j + lane;
+        at += __popc(kb);
     }
 }
 
-// kVec: 16-byte vectors of a row slice.  Grid (2 x slices, H, R): K's slices, then V's.
+// kVec: 16-byte vectors of a row slice.  Grid (2 x slices + 1, H, R): K's slices, then V's, then the weights.
 template <int kVec>
 __global__ void __launch_bounds__(kPgMoveThreads) paged_evict_move_kernel(const PgEvictParams p)
 {
-    constexpr int kRowsStep = kPgMoveThreads / kVec;
     constexpr int kUnroll = 4;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int r = blockIdx.z, h = blockIdx.y;
     const int n = p.lens[r];
     if (p.new_lens[r] < 0 || n <= p.budget) return;
-    const int slices = gridDim.x / 2;
-    uint8_t* pool = blockIdx.x < (unsigned)slices ? p.pool_k : p.pool_v;
-    const int slice = blockIdx.x % slices;
     const int* table = p.table + (size_t)r * p.max_pages;
     const int* kept = p.kept + ((size_t)r * p.H + h) * p.budget;
-    const int c = threadIdx.x % kVec, row = threadIdx.x / kVec;
-    const size_t col = ((size_t)slice * kVec + c) * 16;
-    auto addr = [&](int j) -> uint4* {
+    auto row_at = [&](int j) -> size_t {
         const int pg = p.page_of(j);
-        const size_t at = ((size_t)__ldg(table + pg) * p.H + h) * p.ps + (j - pg * p.ps);
-        return reinterpret_cast<uint4*>(pool + at * p.row_bytes + col);
+        return ((size_t)__ldg(table + pg) * p.H + h) * p.ps + (j - pg * p.ps);
     };
-    for (int i0 = 0; i0 < p.budget; i0 += kRowsStep * kUnroll) {
-        uint4 x[kUnroll];
-        bool move[kUnroll];
+    // row kept[i] to row i for all i, `rows` of them per step and load, in order
+    auto move = [&](int rows, int row, auto load, auto store) {
+        for (int i0 = 0; i0 < p.budget; i0 += rows * kUnroll) {
+            decltype(load(size_t(0))) x[kUnroll];
+            bool moves[kUnroll];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int i = i0 + u * kRowsStep + row;
-            const int j = i < p.budget ? kept[i] : i;
-            move[u] = j != i;
-            if (move[u]) x[u] = *addr(j);
+            for (int u = 0; u < kUnroll; ++u) {
+                const int i = i0 + u * rows + row;
+                const int j = i < p.budget ? kept[i] : i;
+                moves[u] = j != i;
+                if (moves[u]) x[u] = load(row_at(j));
+            }
+            __syncthreads();       // every load of the step precedes its stores
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+                if (moves[u]) store(row_at(i0 + u * rows + row), x[u]);
         }
-        __syncthreads();       // every load of the step precedes its stores
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-            if (move[u]) *addr(i0 + u * kRowsStep + row) = x[u];
+    };
+    const int slices = gridDim.x / 2;
+    if ((int)blockIdx.x == 2 * slices) {
+        move(kPgMoveThreads, threadIdx.x, [&](size_t at) { return p.key_weights[at]; },
+             [&](size_t at, float w) { p.key_weights[at] = w; });
+        return;
     }
+    uint8_t* pool = (int)blockIdx.x < slices ? p.pool_k : p.pool_v;
+    const size_t col = ((size_t)(blockIdx.x % slices) * kVec + threadIdx.x % kVec) * 16;
+    move(kPgMoveThreads / kVec, threadIdx.x / kVec,
+         [&](size_t at) { return *reinterpret_cast<const uint4*>(pool + at * p.row_bytes + col); },
+         [&](size_t at, uint4 x) { *reinterpret_cast<uint4*>(pool + at * p.row_bytes + col) = x; });
 }
 
 }  // namespace unipin
