@@ -202,7 +202,8 @@ int unipin_windowed_prefill_attn(const void* q, const void* k, const void* v, vo
  *                  (row statistics and partial sums); not shared by overlapping calls
  * B <= 65535.  Other arguments and errors as unipin_masked_prefill_bwd.  A segment
  * whose history length is out of range gets zero gradients; rows behind the last
- * segment are left as they are.
+ * segment are left as they are.  A NaN or infinity in a segment may reach any
+ * gradient of that segment and none of another's.
  */
 int unipin_windowed_prefill_bwd(const void* q, const void* k, const void* v, const void* out, const void* dout,
                                 const float* lse, void* dq, void* dk, void* dv, int grad_fp32, const int* cu_seqlens,
@@ -335,7 +336,8 @@ size_t unipin_rank_decode_noalloc_scratch_bytes(void);
  *                  collected, in the pool's layout (one number per row and head)
  * A page id out of range behind a row that a call needs, or a length out of range,
  * is UNIPIN_ERR_OUT_OF_RANGE in *dev_status.  Rows of one layer are numbered with
- * 32 bits: S * H * n_cap must be below 2^32 (UNIPIN_ERR_UNSUPPORTED).  R, B <= 65535.
+ * 32 bits: S * H * n_cap must be below 2^32 (UNIPIN_ERR_UNSUPPORTED).  R, B <= 65535,
+ * max_len <= 2^30.
  */
 
 /*

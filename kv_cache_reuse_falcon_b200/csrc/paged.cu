@@ -225,7 +225,7 @@ int unipin_paged_pool_write(const unipin_kvpool* pool, int layer, const void* k,
     if (!aligned16(k) || !aligned16(v)) return UNIPIN_ERR_MISALIGNED;
     const long long per_block = (long long)kPgWriteThreads * kPgWriteVecs;
     const long long blocks = ((long long)max_new * pool->H * (pool->D / 8) + per_block - 1) / per_block;
-    if (blocks >= (1ll << 31)) return UNIPIN_ERR_INVALID_ARG;
+    if (blocks >= (1ll << 31) || (long long)pool->H * (pool->D / 8) >= (1ll << 30)) return UNIPIN_ERR_INVALID_ARG;
     rc = ensure_paged();
     if (rc != UNIPIN_OK) return rc;
     PgWriteParams p = {};
@@ -297,6 +297,7 @@ int unipin_paged_decode_attn(const void* q, const void* k_self, const void* v_se
     // rows and units are numbered with 31 bits
     const long long units = (long long)R * pool->H * groups * ((pl.vmax + 63) / 64 + 1);
     if (R > 65535 || max_len > (1 << 30) || units >= (1ll << 31)) return UNIPIN_ERR_INVALID_ARG;
+    if (weights && G > 8192) return UNIPIN_ERR_UNSUPPORTED;   // (the join keeps a group's statistics in shared memory)
     rc = ensure_paged();
     if (rc != UNIPIN_OK) return rc;
     DecodeSpace w = decode_space(pl, R, H, pool->H, D, weights);
@@ -376,7 +377,7 @@ int unipin_paged_evict(const unipin_kvpool* pool, int layer, float* key_weights,
         new_lens == lens)
         return UNIPIN_ERR_INVALID_ARG;
     if ((long long)max_len > (long long)max_pages * pool->n_cap) return UNIPIN_ERR_OUT_OF_RANGE;
-    if (R > 65535 || pool->H > 65535) return UNIPIN_ERR_INVALID_ARG;
+    if (R > 65535 || pool->H > 65535 || max_len > (1 << 30)) return UNIPIN_ERR_INVALID_ARG;
     rc = ensure_paged();
     if (rc != UNIPIN_OK) return rc;
     PgEvictParams p = {};

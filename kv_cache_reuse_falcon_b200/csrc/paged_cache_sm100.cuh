@@ -38,7 +38,8 @@ constexpr int kPgWriteVecs = 4;   // vectors of K and of V per thread
 // Memory bound: each row of K and V read once and written once.  A thread takes 16-byte vectors of
 // the packed token rows (consecutive threads: consecutive vectors of a token, all heads), so the
 // reads are contiguous; a head's D elements of a row are contiguous in the pool.  Four vectors of
-// each tensor are loaded before the first is stored.
+// each tensor are loaded before the first is stored.  Divisions are multiplications (PgDiv): with the
+// 64-bit ones of a first version the kernel was bound by them, not by memory.
 // Grid (blocks of rows, B).
 template <bool kE4M3>
 __global__ void __launch_bounds__(kPgWriteThreads) paged_write_kernel(const PgWriteParams p)
@@ -50,7 +51,7 @@ __global__ void __launch_bounds__(kPgWriteThreads) paged_write_kernel(const PgWr
     const int first = p.first[b];
     if (n < 0 || n > len || n > p.max_new || first < 0 || start < 0 ||
         (long long)start + n > (long long)p.total_tokens ||
-        (long long)first + n > (long long)p.max_pages * p.ps) {
+        (long long)first + n > min((long long)p.max_pages * p.ps, 0x7fffffffll)) {
         if (threadIdx.x == 0 && blockIdx.x == 0) report(p.status, (int)UNIPIN_ERR_OUT_OF_RANGE);
         return;
     }

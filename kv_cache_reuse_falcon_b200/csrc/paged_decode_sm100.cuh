@@ -315,7 +315,7 @@ __device__ __forceinline__ float pg_finish_row(const PgParams& p, int r, int h, 
     float res[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        float x = a == 0.f ? 0.f : o[e] * a;
+        float x = o[e] * a;                       // (a = 0: a NaN or infinite value still shows)
         if (b != 0.f)
             x = fmaf(b, __bfloat162float(p.v_self[((size_t)r * p.Hkv + h / p.G) * D + lane * E + e]), x);
         res[e] = x * inv;

@@ -292,8 +292,8 @@ __device__ __forceinline__ uint32_t wb_sign_pair(uint32_t a, uint32_t b)
 // columns written may be (false: a timeout).  `see`: the columns that are allowed pairs.  kKV: -lse and -Dvec per
 // column from shared memory, otherwise this row's own.
 template <bool kKV, typename Read, typename Free>
-__device__ __forceinline__ bool wb_softmax(uint32_t tS, uint32_t tP, uint32_t tD, Read read, Free free, float sl2, const float* nlse, const float* ndvec, float nl,
-                                           float nd, uint32_t see)
+__device__ __forceinline__ bool wb_softmax(uint32_t tS, uint32_t tP, uint32_t tD, Read read, Free free, float sl2,
+                                           const float* nlse, const float* ndvec, float nl, float nd, uint32_t see)
 {
     const uint64_t sc = f2_pack(sl2, sl2);
     const uint64_t nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd);

@@ -67,24 +67,13 @@ __device__ __forceinline__ WinSweep win_row_sweep(int r0, const WinSegment& s, i
     return w;
 }
 
-// Bits c = 0 .. 63 with c < n.
-__device__ __forceinline__ uint64_t win_below(int n)
-{
-    return n <= 0 ? 0ull : (n >= 64 ? ~0ull : (1ull << n) - 1ull);
-}
-
-// Bits c with c < hi and (c >= lo or c < sk).
-__device__ __forceinline__ uint64_t win_see(int lo, int hi, int sk)
-{
-    return win_below(hi) & (~win_below(lo) | win_below(sk));
-}
-
-// The same of 32 columns.
+// Bits c = 0 .. 31 with c < n.
 __device__ __forceinline__ uint32_t win_below32(int n)
 {
     return n >= 32 ? ~0u : (1u << max(n, 0)) - 1u;
 }
 
+// Bits c with c < hi and (c >= lo or c < sk).
 __device__ __forceinline__ uint32_t win_see32(int lo, int hi, int sk)
 {
     return win_below32(hi) & (~win_below32(lo) | win_below32(sk));

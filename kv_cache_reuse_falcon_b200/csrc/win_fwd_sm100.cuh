@@ -99,8 +99,8 @@ __device__ __forceinline__ float wf_score(const __nv_bfloat16* q, const __nv_bfl
     return (a + b) * sl2;
 }
 
-// A row whose result is not finite, from its visible keys alone: O = sum_j 2^(s_j - lse) v_j, in pieces
-// of eight elements (one thread; rare, so not fast).
+// A row whose result is not finite although its statistics are numbers, from its visible keys alone:
+// O = sum_j 2^(s_j - lse) v_j, in pieces of eight elements (one thread; rare, so not fast).
 template <int D>
 __device__ __noinline__ void win_row_again(const WfParams& p, int tok0, int n, int row, int h, float lse)
 {
@@ -500,7 +500,7 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
                     win_store8(p.out, p.out_fp32, at * D + c * 32 + g * 8, f);
                 }
             }
-            if (chk != chk) win_row_again<D>(p, s.tok0, s.n, row, h, lse);
+            if (chk != chk && lse == lse) win_row_again<D>(p, s.tok0, s.n, row, h, lse);
         }
     }
 

@@ -161,3 +161,14 @@ def test_binding_refuses_tensors_that_do_not_fit(ub):
     for f in (ub.paged_decode_attn, ub.paged_evict):
         with pytest.raises(ValueError):
             f(pool, pool, None, 0, past[:, None], past, 16, 8)
+
+
+def test_sizes_beyond_the_kernels_numbers_are_refused(ub):
+    p = _pool(ub, H=16384, S=1, n_cap=1024)
+    assert _decode(ub, p, H=16384, R=65535, max_len=100, window=100, pages=1) == INVALID   # units of 31 bits
+    one = _pool(ub, H=1, S=64, n_cap=64)
+    assert _decode(ub, one, H=8193, weights=A, ws=A, ws_bytes=1 << 40) == UNSUPPORTED   # heads that share weights
+    wide = _pool(ub, H=1 << 28, S=1, n_cap=1)
+    assert _write(ub, wide, max_new=1, pages=1) == INVALID                           # vectors of a token
+    assert _evict(ub, _pool(ub, n_cap=1 << 20, S=8), pages=2000, max_len=(1 << 30) + 1) == INVALID
+    assert _decode(ub, _pool(ub, n_cap=1 << 20, S=8), pages=2000, max_len=(1 << 30) + 1) == INVALID
