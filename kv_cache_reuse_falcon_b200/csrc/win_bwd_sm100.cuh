@@ -11,7 +11,9 @@
 // Row i sees the past keys j <= i, j < n_b with min(i, n_b) - j < window or
 // j < n_sinks, and a candidate its own key.
 //
-// win_bwd_prep_kernel: Dvec of every row, and for a candidate its own key (the
+// win_bwd_prep_kernel: Dvec of every row (dO . O, O as the forward rounded it; where a row sees eight keys or
+// fewer, sum_j P_ij dO_i . v_j: there dS is small against dO . O and the rounding of O would be the largest
+// error of dQ and dK, 3.5e-3 of a gradient under a window of two in place of 1.7e-3), and for a candidate its own key (the
 // only row that sees it): dK and dV of a candidate come from here alone, and the
 // weight of that key in dQ (dself) is left for the dQ blocks.
 // win_bwd_kernel: blocks of two kinds, the first n_kv of the grid the KV blocks.
@@ -39,11 +41,11 @@
 // D = 128 two stages of S and dP and one block per SM: while one group of softmax
 // warps works on a tile the other's products run.  At D <= 64 one stage and two
 // blocks per SM, which also hides a block's first loads and its epilogue.
-// P and dS are rounded to bfloat16 (relative 2^-8 each) as tensor-core operands of
-// dV and dK; scores, P, dS and all sums are float32.  dQ takes dS as the sum of two
-// bfloat16 (relative 2^-15): its row's Dvec comes from an output that carries two
-// roundings already, and with a third dQ would be the least exact of the results
-// (relative error 2.5e-3 in place of 2.0e-3, where the output's own rounding is 1.7e-3).
+// P is rounded to bfloat16 (relative 2^-8) as a tensor-core operand of dV; dS goes to the products as the sum of
+// two bfloat16 (relative 2^-15), which costs one product per tile in either kind of block: dS carries the
+// error of Dvec already (of an output that was rounded twice), and with a third rounding dQ and dK would be
+// the least exact of the results (relative error 2.5e-3 in place of 1.8e-3, where the gradients' own rounding
+// to bfloat16 is 1.7e-3).  Scores, P, dS and all sums are float32.
 // Segments are kept apart: streamed rows behind the segment's (or behind its
 // history) are zeroed in shared memory before they meet a zero weight, so what
 // another segment holds cannot reach a gradient through 0 * NaN.
@@ -76,15 +78,14 @@ struct WbCfg {
     static constexpr int kOffStat = kOffRing + kSlots * kSlotBytes;   // per group: 2 buffers of -lse[64], -dvec[64]
     static constexpr int kOffBar = kOffStat + kStages * 2 * 2 * kWinStr * 4;
     static constexpr int kSmemBytes = kOffBar + 256;
-    // TMEM columns: stage x has S at 128 x and dP at 128 x + 64; then P and dS of streamed rows 0..31 in
-    // the first 16 columns of each, of rows 32..63 in the 16 from column 32 on
+    // TMEM columns: stage x has S at 128 x and dP at 128 x + 64; KV: then P of streamed rows 0..31 in the
+    // first 16 columns of S, of rows 32..63 in the 16 from column 32 on, the upper part of dS likewise in dP
+    // and the lower part in the 16 columns behind each
     static constexpr int kColAcc0 = 128 * kStages;
     static constexpr int kColAcc1 = kColAcc0 + D;
     static constexpr int kTmemCols = D == 128 ? 512 : 256;
-    // P and dS (dQ: dS in two parts) in columns of their own where some are left: a dQ block has one sum
-    // only, and at D = 32 there is room in either kind.  The next S and dP of a stage then wait for its
-    // scores to be read, not for the products that read P and dS.
-    static __device__ constexpr bool apart(bool kv) { return !kv || D == 32; }
+    // dQ: the two parts of dS in columns of their own (a dQ block has one sum only): the next S and dP of a
+    // stage then wait for its scores to be read, not for the products that read dS.
     static __device__ constexpr int col_apart(int x) { return D == 32 ? 192 : kColAcc0 + 64 * x; }
     static_assert(kColAcc1 + D <= kTmemCols, "TMEM budget");
     static_assert(kSmemBytes * kBlocksPerSm <= 226 * 1024, "shared memory budget");
@@ -120,6 +121,7 @@ struct WbParams {
 
 constexpr int kWbPrepThreads = 256;
 constexpr int kWbPrepRows = 16;     // rows of a block
+constexpr int kWbFewKeys = 8;       // most keys of a row whose Dvec is summed over them (see above)
 constexpr int kWbPrepUnroll = 4;    // query rows of a thread at a time: loads in flight
 
 // Grid (blocks of rows, B); D / 8 lanes per query row, 16 bytes of it each.
@@ -184,7 +186,36 @@ __global__ void __launch_bounds__(kWbPrepThreads, 4) win_bwd_prep_kernel(const W
             }
         }
     }
+    // rows that see few keys: sum_j P_ij dO_i . v_j itself (each by the lanes that stored its dO . O)
+    if (p.window <= kWbFewKeys || min(r0, s.n) < kWbFewKeys) {
+        const int rows = (r1 - r0) * p.H;
+        for (int x0 = grp; x0 - grp < rows; x0 += kGroups) {
+            const int x = min(x0, rows - 1), row = r0 + x / p.H, h = x % p.H;
+            // keys below sk and from lo to hi - 1, and a candidate's own
+            const int lo = max(min(row, s.n) - p.window + 1, 0), hi = min(row + 1, s.n);
+            const int sk = min(min(p.n_sinks, lo), hi);
+            const int n = sk + max(hi - lo, 0) + (row >= s.n ? 1 : 0);
+            const bool few = x0 < rows && n <= kWbFewKeys;
+            if (!__any_sync(0xffffffffu, few)) continue;
+            const size_t qr = ((size_t)s.tok0 + row) * p.H + h;
+            const uint4 q4 = __ldg(reinterpret_cast<const uint4*>(p.q + qr * D + c * 8));
+            const uint4 g4 = __ldg(reinterpret_cast<const uint4*>(p.dout + qr * D + c * 8));
+            const float nl = win_neg_lse(p.lse[qr]);
+            float d = 0.f;
+#pragma unroll 1
+            for (int y = 0; y < kWbFewKeys; ++y) {
+                int j = y < sk ? y : lo + y - sk;
+                if (j >= hi) j = row;
+                const size_t at = (((size_t)s.tok0 + j) * p.Hkv + h / p.G) * D + c * 8;
+                const float qk = dot_lanes(dot8(q4, __ldg(reinterpret_cast<const uint4*>(p.k + at))));
+                const float gv = dot_lanes(dot8(g4, __ldg(reinterpret_cast<const uint4*>(p.v + at))));
+                if (y < n) d = fmaf(ex2_approx(fmaf(qk, p.sl2, nl)), gv, d);
+            }
+            if (few && c == 0) p.dvec[qr] = d;
+        }
+    }
     // candidates: their own key
+    __syncthreads();                                     // Dvec of the block's rows
     const int c0 = max(r0, s.n);
     const int pairs = max(r1 - c0, 0) * p.Hkv;           // (at most 16 rows)
     for (int x = grp; x - grp < pairs; x += kGroups) {
@@ -199,12 +230,11 @@ __global__ void __launch_bounds__(kWbPrepThreads, 4) win_bwd_prep_kernel(const W
         for (int g = 0; g < p.G; ++g) {
             const size_t qr = tok * p.H + hk * p.G + g;
             const uint4 q4 = __ldg(reinterpret_cast<const uint4*>(p.q + qr * D + c * 8));
-            const uint4 o4 = __ldg(reinterpret_cast<const uint4*>(p.o + qr * D + c * 8));
             const uint4 g4 = __ldg(reinterpret_cast<const uint4*>(p.dout + qr * D + c * 8));
             const float lse = p.lse[qr];
-            const float dvec = dot_lanes(dot8(o4, g4)), qk = dot_lanes(dot8(q4, k4)), gv = dot_lanes(dot8(g4, v4));
+            const float qk = dot_lanes(dot8(q4, k4)), gv = dot_lanes(dot8(g4, v4));
             const float w = ex2_approx(fmaf(qk, p.sl2, win_neg_lse(lse)));
-            const float ds = w * (gv - dvec);
+            const float ds = w * (gv - p.dvec[qr]);
             if (live && c == 0) p.dself[qr] = ds;
             float qf[8], gf[8];
             win_unpack8(q4, qf);
@@ -287,25 +317,27 @@ __device__ __forceinline__ uint32_t wb_sign_pair(uint32_t a, uint32_t b)
 }
 
 // One softmax pass over half a streamed tile: P and dS of this thread's resident row over 32 of the 64
-// streamed rows, from S and dP in TMEM (32 columns at tS and at tS + 64) and back as bfloat16 pairs, P to
-// tP and dS to tD (dQ: the lower part of dS and the upper).  read(): the scores have been read; free(): the
-// columns written may be (false: a timeout).  `see`: the columns that are allowed pairs.  kKV: -lse and -Dvec per
-// column from shared memory, otherwise this row's own.
+// streamed rows, from S and dP in TMEM (32 columns at tS and at tS + 64) and back as bfloat16 pairs: P (KV)
+// to tP, dS in two parts to tD (the upper 8 bits) and tL.  read(): the scores have been read; free(): the
+// columns written may be (false: a timeout).  `see`: the columns that are allowed pairs.  kKV: -lse and
+// -Dvec per column from shared memory, otherwise this row's own.
 template <bool kKV, typename Read, typename Free>
-__device__ __forceinline__ bool wb_softmax(uint32_t tS, uint32_t tP, uint32_t tD, Read read, Free free, float sl2,
-                                           const float* nlse, const float* ndvec, float nl, float nd, uint32_t see)
+__device__ __forceinline__ bool wb_softmax(uint32_t tS, uint32_t tP, uint32_t tD, uint32_t tL, Read read, Free free,
+                                           float sl2, const float* nlse, const float* ndvec, float nl, float nd,
+                                           uint32_t see)
 {
     const uint64_t sc = f2_pack(sl2, sl2);
     const uint64_t nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd);
     const bool full = __all_sync(0xffffffffu, see == ~0u);
-    uint32_t sr[32], dr[32], pk[16], dk[16];             // (dQ: dS in two parts, the lower one in pk)
+    uint32_t sr[32], dr[32], pk[16], dk[16], lk[16];
     if (!__any_sync(0xffffffffu, see != 0u)) {       // no pair of these 32 x 32
 #pragma unroll
-        for (int i = 0; i < 16; ++i) pk[i] = 0u;
+        for (int i = 0; i < 16; ++i) dk[i] = 0u;
         read();
         if (!free()) return false;
-        tmem_st16_nowait(tP, pk);
-        tmem_st16(tD, pk);
+        if (kKV) tmem_st16_nowait(tP, dk);
+        tmem_st16_nowait(tL, dk);
+        tmem_st16(tD, dk);
         return true;
     }
     tmem_ld32x2(tS, sr, tS + kWinStr, dr);
@@ -326,28 +358,35 @@ __device__ __forceinline__ bool wb_softmax(uint32_t tS, uint32_t tP, uint32_t tD
             float x0, x1, d0, d1;
             f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), sc, a[f]), x0, x1);
             f2_unpack(f2_add(f2_pack(__uint_as_float(dr[i]), __uint_as_float(dr[i + 1])), b[f]), d0, d1);
-            float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+            const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
             d0 *= p0;
             d1 *= p1;
-            if (kKV) {
-                pk[i / 2] = pack_bf16x2(p0, p1);
-                dk[i / 2] = pack_bf16x2(d0, d1);
-            } else {
-                // the upper 8 bits of dS, and the rest rounded to as many
-                const uint32_t b0 = __float_as_uint(d0), b1 = __float_as_uint(d1);
-                dk[i / 2] = __byte_perm(b0, b1, 0x7632);
-                pk[i / 2] = pack_bf16x2(d0 - __uint_as_float(b0 & 0xffff0000u), d1 - __uint_as_float(b1 & 0xffff0000u));
-            }
+            // the upper 8 bits of dS, and the rest rounded to as many
+            const uint32_t b0 = __float_as_uint(d0), b1 = __float_as_uint(d1);
+            dk[i / 2] = __byte_perm(b0, b1, 0x7632);
+            lk[i / 2] = pack_bf16x2(d0 - __uint_as_float(b0 & 0xffff0000u), d1 - __uint_as_float(b1 & 0xffff0000u));
+            if (kKV) pk[i / 2] = pack_bf16x2(p0, p1);
             if (!full) {
                 // bits i, i + 1 of `see` as the signs of two bytes, spread over the pair's halves
                 const uint32_t pair = wb_sign_pair(see << (31 - i), see << (30 - i));
-                pk[i / 2] &= pair;
                 dk[i / 2] &= pair;
+                lk[i / 2] &= pair;
+                if (kKV) pk[i / 2] &= pair;
             }
         }
+        if (kKV && e % 16 == 12) {                   // (as soon as they are there, for the registers)
+            const int c = e / 16 * 8;
+            tmem_st8_nowait(tP + c, pk + c);
+            tmem_st8_nowait(tL + c, lk + c);
+            tmem_st8_nowait(tD + c, dk + c);
+        }
+    }
+    if (kKV) {
+        tmem_st_wait();
+        return true;
     }
     if (!free()) return false;
-    tmem_st16_nowait(tP, pk);
+    tmem_st16_nowait(tL, lk);
     tmem_st16(tD, dk);
     return true;
 }
@@ -387,8 +426,8 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
     uint64_t* s_ready = bars + 3;      // [2]
     uint64_t* p_ready = bars + 5;      // [2]
     uint64_t* grp = bars + 7;          // [2]
-    uint64_t* s_free = bars + 9;       // [2] a stage's scores have been read (apart)
-    uint64_t* p_free = bars + 11;      // [2] .. its P and dS (apart)
+    uint64_t* s_free = bars + 9;       // [2] dQ: a stage's scores have been read
+    uint64_t* p_free = bars + 11;      // [2] .. its dS
     uint64_t* full = bars + 13;        // [kSlots]
     uint64_t* empty = full + C::kSlots;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(empty + C::kSlots);
@@ -396,7 +435,7 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
     volatile int* last_piece = reinterpret_cast<volatile int*>(tmem_slot + 2);   // [2]
     WaitCtl ctl{abort_flag, p.status, p.wait_limit_ns, (int)UNIPIN_ERR_DEVICE_TIMEOUT};
     const bool leader = lane == 0;
-    constexpr bool kApart = C::apart(kKV);
+    constexpr bool kApart = !kKV;
     // streamed tile i = tile `idx` of query head `g` of the group, into its ring slot
     auto load_tile = [&](int i, int g, int idx) {
         const int st = i % C::kSlots;
@@ -527,13 +566,14 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
 #pragma unroll
                 for (int kk = 0; kk < kWinStr / 16; ++kk) {
                     // 16 streamed rows: 8 columns of pairs, those of rows 32.. at column 32
-                    const uint32_t tP = tmem + (kApart ? C::col_apart(x) + kk * 8 : x * 128 + (kk / 2) * 32 + (kk % 2) * 8);
-                    const uint32_t tD = tP + (kApart ? 32 : kWinStr);
+                    const uint32_t tP = tmem + x * 128 + (kk / 2) * 32 + (kk % 2) * 8;
+                    const uint32_t tD = kApart ? tmem + C::col_apart(x) + kk * 8 : tP + kWinStr;
+                    const uint32_t tL = tD + (kApart ? 32 : 16);
                     const uint64_t off = slot + (uint64_t)((kk * 16 * C::kRowBytes) >> 4);
                     const uint32_t acc = (i > 0 || kk > 0) ? 1u : 0u;
                     if (kKV) umma_bf16_ts(tmem + C::kColAcc0, tP, d_g1 + off, idesc_g, acc);
                     umma_bf16_ts(tmem + C::kColAcc1, tD, d_g0 + off, idesc_g, acc);
-                    if (!kKV) umma_bf16_ts(tmem + C::kColAcc1, tP, d_g0 + off, idesc_g, 1u);   // the lower part
+                    umma_bf16_ts(tmem + C::kColAcc1, tL, d_g0 + off, idesc_g, 1u);
                 }
                 umma_commit(empty + st);
                 if (kApart) umma_commit(p_free + x);
@@ -610,7 +650,7 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
             if (!ok) break;
             tc_fence_after_sync();
             const uint32_t tS = lanes + x * 128 + half * 32;
-            const uint32_t tP = kApart ? lanes + C::col_apart(x) + half * 16 : tS;
+            const uint32_t tD = kApart ? lanes + C::col_apart(x) + half * 16 : tS + kWinStr;
             auto read = [&]() {
                 if (!kApart) return;
                 tc_fence_before_sync();
@@ -623,7 +663,7 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
                 tc_fence_after_sync();
                 return true;
             };
-            ok = wb_softmax<kKV>(tS, tP, tP + (kApart ? 32 : kWinStr), read, free, p.sl2, st + half * 32,
+            ok = wb_softmax<kKV>(tS, tS, tD, tD + (kApart ? 32 : 16), read, free, p.sl2, st + half * 32,
                                  st + kWinStr + half * 32, nl, nd, see);
             if (!ok) break;
             // streamed rows that are no row (KV: behind the segment) or no past key (dQ) become zeros
