@@ -313,16 +313,24 @@ __global__ void __launch_bounds__(kPgMoveThreads) paged_evict_move_kernel(const 
     };
     // row kept[i] to row i for all i, `rows` of them per step and load, in order
     auto move = [&](int rows, int row, auto load, auto store) {
+        int next[kUnroll];         // kept[] a step ahead: its latency is not added to the rows'
+        auto ahead = [&](int i0) {
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const int i = i0 + u * rows + row;
+                next[u] = i < p.budget ? kept[i] : i;
+            }
+        };
+        ahead(0);
         for (int i0 = 0; i0 < p.budget; i0 += rows * kUnroll) {
             decltype(load(size_t(0))) x[kUnroll];
             bool moves[kUnroll];
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
-                const int i = i0 + u * rows + row;
-                const int j = i < p.budget ? kept[i] : i;
-                moves[u] = j != i;
-                if (moves[u]) x[u] = load(row_at(j));
+                moves[u] = next[u] != i0 + u * rows + row;
+                if (moves[u]) x[u] = load(row_at(next[u]));
             }
+            ahead(i0 + rows * kUnroll);
             __syncthreads();       // every load of the step precedes its stores
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u)
