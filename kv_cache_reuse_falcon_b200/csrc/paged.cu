@@ -142,9 +142,10 @@ DecodeShape decode_shape(const unipin_kvpool* pool)
     return {PgCfg<32, kPgBf16>::kBlocksPerSm, PgCfg<32, kPgBf16>::kUnit};
 }
 
-// One wave of blocks.  Rows stay whole (no partials, no second launch) where they are short: up to 512
-// visible rows a block's sweep takes less time than the join's launch, and without
-// parallelism to gain the join would only add to it.
+// One wave of blocks.  Rows stay whole (no partials, no second launch) where they are short: up to two units,
+// and up to 512 visible rows where the rows fill half of the device's blocks alone.  Whole and split, D = 64,
+// H = 8: one request of 256 rows 6.9 and 7.4 us, of 500 8.7 and 7.7 us, of 1000 12.0 and 8.2 us; 32 requests
+// of 256 7.9 and 9.7 us, of 500 10.0 and 13.6 us.
 DecodePlan decode_plan(const unipin_kvpool* pool, int R, int H, int max_len, int window, int n_sinks, bool weights,
                        int sms)
 {
@@ -156,8 +157,8 @@ DecodePlan decode_plan(const unipin_kvpool* pool, int R, int H, int max_len, int
     const long long pairs = (long long)R * pool->H * ((G + 15) / 16);
     const DecodeShape shape = decode_shape(pool);
     const long long units = vmax > 0 ? (vmax + shape.unit - 1) / shape.unit : 1;
-    pl.whole = !weights && vmax <= 512;
     const long long slots = (long long)sms * shape.blocks_per_sm;
+    pl.whole = !weights && (units <= 2 || (vmax <= 512 && 2 * pairs >= slots));
     const long long most = pl.whole ? pairs : pairs * units;
     pl.shares = (int)(most < slots ? most : slots);
     return pl;

@@ -15,13 +15,13 @@
 // Bound: memory.  Each visible K and V row is read once for the G query heads
 // that share it: 2 D elements for 4 D G flops.  So the kernel is built around
 // loads in flight, not around the tensor cores:
-//   - the work is cut into units of 128 visible rows of one (request, key/value
-//     head, up to 16 query heads of the group); the units of all requests, in
+//   - the work is cut into units of 128 visible rows (64 at 256-byte rows) of one
+//     (request, key/value head, up to 16 query heads of the group); the units of all requests, in
 //     order, go to one wave of blocks in equal contiguous shares, whatever the
 //     requests' lengths.  (One block per chunk of a request left a third of the
 //     time to the blocks' starts and ends.)  A block that holds all of a row's
 //     units finishes the row; the others' pieces are joined by a second kernel;
-//   - a warp takes 32 rows of each of its block's units on its own, through a ring
+//   - a warp takes 32 (16) rows of each of its block's units on its own, through a ring
 //     of stages of its own: no block-wide barrier within a row, and the copies run
 //     on across the ends of rows and requests.  Neighbouring lanes copy (cp.async)
 //     neighbouring 16-byte chunks of a row, so each sector crosses from L2 once;
@@ -41,6 +41,12 @@
 // under a tenth of the tensor cores' rate at the full memory rate, and a TMEM
 // accumulator would put a chain of barriers (load, S, softmax, P, P.V) into
 // every tile.
+// Measured (B200, with the join): 32 requests of 1024 .. 2048 rows, H = 8, D = 64, bf16 21.8 us (102 MB:
+// 4.7 TB/s, 71% of the rate of a copy); 256 of 32 .. 4096 under a window of 1024, D = 128, E4M3 97.6 us
+// (477 MB: 4.9 TB/s, 75%); 8 of 777 .. 32768, H = 8 over 2, D = 128, with key_weights 38 us (150 MB); one of
+// 500 rows 8.8 us.  What is left is instruction issue (at 12 warps per SM a wait for an issue slot, a product
+// or a row stands behind most stalls) and the first and last units of a block; the smallest calls are one
+// chain: lengths, page, rows, S, P, O, join of the warps.
 // Scores, row maxima, row sums and O are float32.  P is rounded to the type of
 // V's fragment (bfloat16; float16 over E4M3 codes), as in the prefill: one
 // rounding of relative size <= 2^-8 (2^-11) per weight, independent of the others.
@@ -84,7 +90,8 @@ struct PgCfg {
     static constexpr int kRowsPerCopy = 32 / kChunks;       // rows that one copy of a warp covers
     static constexpr int kStageBytes = 2 * kKeys * kRowBytes;   // K and V of a tile
     // Bytes in flight per SM for the memory latency: about 100 KB (one stage of two or two of three of 12
-    // or 16 warps).
+    // or 16 warps).  Three blocks per SM against two, with a wider join: 24.3 -> 21.7 us (R = 32, D = 64, bf16),
+    // 41 -> 38 us (R = 8 with weights, D = 128), 109 -> 98 us (R = 256, window, E4M3).
     static constexpr int kStages = kRowBytes >= 128 ? 2 : (kRowBytes == 64 ? 3 : 4);
     static constexpr int kBlocksPerSm = kRowBytes >= 128 ? 3 : 4;
     static constexpr int kRingBytes = kPgWarps * kStages * kStageBytes;

@@ -295,8 +295,9 @@ struct WbPlan {
 };
 
 // The sweep of a key tile is cut where one would outlast the others: into pieces of at least half the steps
-// that an SM takes on average (a step: 64 rows of one query head), and of 16 steps, which take longer than
-// a piece's sums cost.  All rows see a tile with sinks; others those within the window, and candidates,
+// that an SM takes on average (a step: 64 rows of one query head), and of four steps: where the device is
+// not full, pieces of 16, 8 and 4 steps took 47, 42 and 42 us (1 segment of 186 + 125 rows, H = 8 over 1,
+// D = 128, window 80, with the forward) and 50, 39 and 34 us (25 + 108, H = 16 over 1, D = 64).  All rows see a tile with sinks; others those within the window, and candidates,
 // of which the host does not know the number.
 WbPlan win_bwd_plan(int B, int H, int H_kv, int D, int max_seqlen, int total_tokens, int window, int n_sinks)
 {
@@ -311,7 +312,7 @@ WbPlan win_bwd_plan(int B, int H, int H_kv, int D, int max_seqlen, int total_tok
     const long long all = (long long)B * H_kv * (pl.sink_tiles * far_steps + (pl.tiles - pl.sink_tiles) * near_steps) + dq_steps;
     const long long sms = kNumSmsHint;              // (not the device's own: the workspace must not depend on it)
     long long most = all / (2 * sms);
-    if (most < 16) most = 16;
+    if (most < 4) most = 4;
     pl.sink_pieces = pl.sink_tiles > 0 ? (int)((far_steps + most - 1) / most) : 1;
     pl.win_pieces = (int)((near_steps + most - 1) / most);
     pl.n_kv = (long long)B * H_kv *
@@ -1034,7 +1035,10 @@ int unipin_windowed_prefill_bwd(const void* q, const void* k, const void* v, con
                             (const void*)workspace})
         if (!aligned16(ptr)) return UNIPIN_ERR_MISALIGNED;
     if ((reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return UNIPIN_ERR_MISALIGNED;
-    const long long prep = ((long long)max_seqlen + kWbPrepRows - 1) / kWbPrepRows;
+    // a block's rows run one after another: fewer of them where the device would not be full
+    int prep_rows = kWbPrepRows;
+    while (prep_rows > 2 && ((long long)max_seqlen + prep_rows - 1) / prep_rows * B < 4 * kNumSmsHint) prep_rows /= 2;
+    const long long prep = ((long long)max_seqlen + prep_rows - 1) / prep_rows;
     // blocks are numbered with 31 bits
     if (B > 65535 || pl.n_kv + pl.n_dq >= (1ll << 31)) return UNIPIN_ERR_INVALID_ARG;
     int rc = ensure_device();
@@ -1057,6 +1061,7 @@ int unipin_windowed_prefill_bwd(const void* q, const void* k, const void* v, con
     p.n_counters = pl.n_counters;
     p.part = reinterpret_cast<float*>(ws + pl.part);
     p.tiles = pl.tiles;
+    p.prep_rows = prep_rows;
     p.sink_tiles = pl.sink_tiles;
     p.sink_pieces = pl.sink_pieces;
     p.win_pieces = pl.win_pieces;

@@ -46,6 +46,12 @@
 // error of Dvec already (of an output that was rounded twice), and with a third rounding dQ and dK would be
 // the least exact of the results (relative error 2.5e-3 in place of 1.8e-3, where the gradients' own rounding
 // to bfloat16 is 1.7e-3).  Scores, P, dS and all sums are float32.
+// Bound: the chain of a tile (S and dP, softmax, the products that read P and dS) at one or two blocks per
+// SM; the first loads and the epilogue of a block are 5 of its 11 .. 15 us.  Measured (B200), with the forward:
+// 64 segments of 256 + 128 rows, H = 8, D = 64, window 128, 185 us (forward 45, prep kernel about 15 of 24
+// exposed, this one 124; 304 MB); 8 segments of 700 .. 1500, H = 8 over 2, D = 128, window 300, 171 us.  A
+// persistent block that took its items from a ring of its own took 145 us for this kernel; sweeps with
+// sinks in one piece 190 and 180 us for the two.
 // Segments are kept apart: streamed rows behind the segment's (or behind its
 // history) are zeroed in shared memory before they meet a zero weight, so what
 // another segment holds cannot reach a gradient through 0 * NaN.
@@ -103,13 +109,14 @@ struct WbParams {
     void* dv;
     float* dvec;                // [T, H] workspace
     float* dself;               // [T, H] workspace: dS of a candidate's own key
-    float* part;                // workspace: pieces' sums [slot][dV, dK][128][D]
+    float* part;                // workspace: pieces' sums [slot][dV, dK: 2 D / 4][128 rows][4]
     unsigned* counters;         // workspace: ended pieces of (segment, kv head, key tile, dV or dK)
     long long n_counters;
     const int* cu;
     const int* past;
     int B, H, Hkv, G, total_rows, max_rows;
     int tiles, sink_tiles;      // key tiles of max_rows, and how many of them may hold a sink
+    int prep_rows;              // rows of a prep kernel's block
     int sink_pieces, win_pieces;   // most pieces of a KV block's sweep with and without sinks
     int window, n_sinks;
     int grad_fp32;
@@ -120,13 +127,14 @@ struct WbParams {
 };
 
 constexpr int kWbPrepThreads = 256;
-constexpr int kWbPrepRows = 16;     // rows of a block
+constexpr int kWbPrepRows = 16;     // most rows of a block
 constexpr int kWbFewKeys = 8;       // most keys of a row whose Dvec is summed over them (see above)
+constexpr int kWbPrepHeads = 2;     // query heads of a candidate at a time
 constexpr int kWbPrepUnroll = 4;    // query rows of a thread at a time: loads in flight
 
 // Grid (blocks of rows, B); D / 8 lanes per query row, 16 bytes of it each.
 template <int D>
-__global__ void __launch_bounds__(kWbPrepThreads, 4) win_bwd_prep_kernel(const WbParams p)
+__global__ void __launch_bounds__(kWbPrepThreads, 3) win_bwd_prep_kernel(const WbParams p)
 {
     constexpr int L = D / 8;
     constexpr int kGroups = kWbPrepThreads / L;
@@ -139,7 +147,7 @@ __global__ void __launch_bounds__(kWbPrepThreads, 4) win_bwd_prep_kernel(const W
     const int b = blockIdx.y;
     const WinSegment s = win_segment(p.cu, p.past, b, p.max_rows, p.total_rows);
     if (!s.ok && blockIdx.x == 0 && threadIdx.x == 0) report(p.status, (int)UNIPIN_ERR_OUT_OF_RANGE);
-    const int r0 = blockIdx.x * kWbPrepRows, r1 = min(r0 + kWbPrepRows, s.len);
+    const int r0 = blockIdx.x * p.prep_rows, r1 = min(r0 + p.prep_rows, s.len);
     if (!s.rows_ok || r0 >= r1) return;
     const int c = threadIdx.x % L, grp = threadIdx.x / L;
     if (!s.ok) {                                         // an out-of-range history length: zero gradients
@@ -202,14 +210,22 @@ __global__ void __launch_bounds__(kWbPrepThreads, 4) win_bwd_prep_kernel(const W
             const uint4 g4 = __ldg(reinterpret_cast<const uint4*>(p.dout + qr * D + c * 8));
             const float nl = win_neg_lse(p.lse[qr]);
             float d = 0.f;
-#pragma unroll 1
-            for (int y = 0; y < kWbFewKeys; ++y) {
-                int j = y < sk ? y : lo + y - sk;
-                if (j >= hi) j = row;
-                const size_t at = (((size_t)s.tok0 + j) * p.Hkv + h / p.G) * D + c * 8;
-                const float qk = dot_lanes(dot8(q4, __ldg(reinterpret_cast<const uint4*>(p.k + at))));
-                const float gv = dot_lanes(dot8(g4, __ldg(reinterpret_cast<const uint4*>(p.v + at))));
-                if (y < n) d = fmaf(ex2_approx(fmaf(qk, p.sl2, nl)), gv, d);
+            const int most = __reduce_max_sync(0xffffffffu, few ? n : 0);
+            for (int y0 = 0; y0 < most; y0 += 4) {
+                uint4 k4[4], v4[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    int j = y0 + y < sk ? y0 + y : lo + y0 + y - sk;
+                    if (j >= hi) j = row;
+                    const size_t at = (((size_t)s.tok0 + j) * p.Hkv + h / p.G) * D + c * 8;
+                    k4[y] = __ldg(reinterpret_cast<const uint4*>(p.k + at));
+                    v4[y] = __ldg(reinterpret_cast<const uint4*>(p.v + at));
+                }
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const float qk = dot_lanes(dot8(q4, k4[y])), gv = dot_lanes(dot8(g4, v4[y]));
+                    if (y0 + y < n) d = fmaf(ex2_approx(fmaf(qk, p.sl2, nl)), gv, d);
+                }
             }
             if (few && c == 0) p.dvec[qr] = d;
         }
@@ -227,22 +243,33 @@ __global__ void __launch_bounds__(kWbPrepThreads, 4) win_bwd_prep_kernel(const W
         float dk[8], dv[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) dk[e] = dv[e] = 0.f;
-        for (int g = 0; g < p.G; ++g) {
-            const size_t qr = tok * p.H + hk * p.G + g;
-            const uint4 q4 = __ldg(reinterpret_cast<const uint4*>(p.q + qr * D + c * 8));
-            const uint4 g4 = __ldg(reinterpret_cast<const uint4*>(p.dout + qr * D + c * 8));
-            const float lse = p.lse[qr];
-            const float qk = dot_lanes(dot8(q4, k4)), gv = dot_lanes(dot8(g4, v4));
-            const float w = ex2_approx(fmaf(qk, p.sl2, win_neg_lse(lse)));
-            const float ds = w * (gv - p.dvec[qr]);
-            if (live && c == 0) p.dself[qr] = ds;
-            float qf[8], gf[8];
-            win_unpack8(q4, qf);
-            win_unpack8(g4, gf);
+#pragma unroll 1
+        for (int g0 = 0; g0 < p.G; g0 += kWbPrepHeads) {
+            uint4 q4[kWbPrepHeads], g4[kWbPrepHeads];
+            float nl[kWbPrepHeads], dvec[kWbPrepHeads];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                dk[e] = fmaf(p.scale * ds, qf[e], dk[e]);
-                dv[e] = fmaf(w, gf[e], dv[e]);
+            for (int g = 0; g < kWbPrepHeads; ++g) {
+                const size_t qr = tok * p.H + hk * p.G + min(g0 + g, p.G - 1);
+                q4[g] = __ldg(reinterpret_cast<const uint4*>(p.q + qr * D + c * 8));
+                g4[g] = __ldg(reinterpret_cast<const uint4*>(p.dout + qr * D + c * 8));
+                nl[g] = win_neg_lse(p.lse[qr]);
+                dvec[g] = p.dvec[qr];
+            }
+#pragma unroll
+            for (int g = 0; g < kWbPrepHeads; ++g) {
+                if (g0 + g >= p.G) break;
+                const float qk = dot_lanes(dot8(q4[g], k4)), gv = dot_lanes(dot8(g4[g], v4));
+                const float w = ex2_approx(fmaf(qk, p.sl2, nl[g]));
+                const float ds = w * (gv - dvec[g]);
+                if (live && c == 0) p.dself[tok * p.H + hk * p.G + g0 + g] = ds;
+                float qf[8], gf[8];
+                win_unpack8(q4[g], qf);
+                win_unpack8(g4[g], gf);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    dk[e] = fmaf(p.scale * ds, qf[e], dk[e]);
+                    dv[e] = fmaf(w, gf[e], dv[e]);
+                }
             }
         }
         if (live) {
@@ -702,7 +729,8 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
                 float* part = nullptr;
                 if (it.pieces > 1) {
                     // this piece's sums; the piece that ends last adds them all up, in order
-                    part = p.part + (it.slot * kWinRes + t) * (2 * D) + c_first;
+                    // (four columns of all rows side by side: a warp's accesses are contiguous)
+                    part = p.part + it.slot * (2 * kWinRes * D) + ((size_t)c_first / 4 * kWinRes + t) * 4;
                     float* mine = part + (size_t)it.piece * (2 * kWinRes * D);
 #pragma unroll
                     for (int c = 0; c < kPart; c += 32) {
@@ -710,7 +738,8 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
                         tmem_ld32(lanes + C::kColAcc0 + c_first + c, a);
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<uint4*>(mine + c + e) = make_uint4(a[e], a[e + 1], a[e + 2], a[e + 3]);
+                            *reinterpret_cast<uint4*>(mine + (c + e) * kWinRes) =
+                                make_uint4(a[e], a[e + 1], a[e + 2], a[e + 3]);
                     }
                     __threadfence();
                     ok = warp_group_sync(grp + x, ngrp, ctl, lane);
@@ -729,11 +758,12 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
                     if (it.pieces > 1) {
 #pragma unroll
                         for (int e = 0; e < 32; ++e) a[e] = 0u;
+#pragma unroll 2
                         for (int y = 0; y < it.pieces; ++y) {
-                            const float* from = part + (size_t)y * (2 * kWinRes * D) + c;
+                            const float* from = part + (size_t)y * (2 * kWinRes * D) + c * kWinRes;
 #pragma unroll
                             for (int e = 0; e < 32; e += 4) {
-                                const float4 v = __ldcg(reinterpret_cast<const float4*>(from + e));
+                                const float4 v = __ldcg(reinterpret_cast<const float4*>(from + e * kWinRes));
                                 a[e] = __float_as_uint(__uint_as_float(a[e]) + v.x);
                                 a[e + 1] = __float_as_uint(__uint_as_float(a[e + 1]) + v.y);
                                 a[e + 2] = __float_as_uint(__uint_as_float(a[e + 2]) + v.z);
