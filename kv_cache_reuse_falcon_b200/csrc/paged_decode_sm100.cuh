@@ -44,7 +44,7 @@
 // Measured (B200, with the join): 32 requests of 1024 .. 2048 rows, H = 8, D = 64, bf16 21.8 us (102 MB:
 // 4.7 TB/s, 71% of the rate of a copy); 256 of 32 .. 4096 under a window of 1024, D = 128, E4M3 97.6 us
 // (477 MB: 4.9 TB/s, 75%); 8 of 777 .. 32768, H = 8 over 2, D = 128, with key_weights 38 us (150 MB); one of
-// 500 rows 8.8 us.  What is left is instruction issue (at 12 warps per SM a wait for an issue slot, a product
+// 500 rows 8.3 us.  What is left is instruction issue (at 12 warps per SM a wait for an issue slot, a product
 // or a row stands behind most stalls) and the first and last units of a block; the smallest calls are one
 // chain: lengths, page, rows, S, P, O, join of the warps.
 // Scores, row maxima, row sums and O are float32.  P is rounded to the type of

@@ -19,7 +19,9 @@
 // so the next tile's S is computed while the softmax works; at D <= 64 one, and
 // the other blocks' products run meanwhile.
 // Warps: 0-3 softmax and epilogue, 4 TMA producer, 5 MMA issuer (owns TMEM).
-// Bound: the chain of a tile (S, its softmax, P V) against the two or three blocks that hide it.  Measured
+// Bound, at D = 128: the products themselves.  An M = 128, N = 64 product from shared memory takes about 50
+// cycles where its rate is 32 (its A is read again for few columns), P V's N = 128 about 65: 650 of the 700
+// cycles that an SM takes per tile.  (Wider key tiles would need TMEM that the second block has.)  Measured
 // (B200): 16 segments of 500 .. 2048 past rows and 50 .. 256 candidates, H = 8, D = 128, window 512, 99 us
 // (40.4 GFLOP of allowed pairs: 408 TFLOP/s, 25% of the rate of a large product; 191 MB); 2 segments of 300,
 // D = 64, 10.3 us.  The masked prefill's engine with a window took 162 us for the first; two threads per row
