@@ -21,6 +21,9 @@ std::mutex g_paged_mutex;
 bool g_paged_ready[kMaxDevices] = {};
 
 constexpr int kSelKeysCap = 48 * 1024;   // keys of the selection's shared-memory copy (192 KB)
+// Rows up to which the selection takes the smaller block (256 threads against 1024: 133 requests of 7 rows,
+// H = 8, 13.9 and 33.9 us; 184 of 165, H = 2, 7.7 and 10.8; one of 1000, H = 8, 12.0 and 10.6).
+constexpr int kSelShort = 512;
 
 template <int D, int kMode, int kNG>
 int set_decode_attr()
@@ -61,7 +64,8 @@ int ensure_paged()
     int rc = set_decode_attrs<32>();
     if (rc == UNIPIN_OK) rc = set_decode_attrs<64>();
     if (rc == UNIPIN_OK) rc = set_decode_attrs<128>();
-    if (rc == UNIPIN_OK && cudaFuncSetAttribute(paged_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (rc == UNIPIN_OK && cudaFuncSetAttribute(paged_evict_select_kernel<kPgSelThreads>,
+                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                 kSelKeysCap * 4) != cudaSuccess)
         rc = UNIPIN_ERR_CUDA;
     if (rc != UNIPIN_OK) return rc;
@@ -402,7 +406,12 @@ int unipin_paged_evict(const unipin_kvpool* pool, int layer, float* key_weights,
     p.status = dev_status;
     p.keys_cap = max_len < kSelKeysCap ? max_len : kSelKeysCap;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    paged_evict_select_kernel<<<dim3((unsigned)pool->H, (unsigned)R, 1), kPgSelThreads, (size_t)p.keys_cap * 4, s>>>(p);
+    const dim3 sgrid((unsigned)pool->H, (unsigned)R, 1);
+    const size_t ssmem = (size_t)p.keys_cap * 4;
+    if (max_len <= kSelShort)
+        paged_evict_select_kernel<kPgSelThreadsShort><<<sgrid, kPgSelThreadsShort, ssmem, s>>>(p);
+    else
+        paged_evict_select_kernel<kPgSelThreads><<<sgrid, kPgSelThreads, ssmem, s>>>(p);
     if (cudaGetLastError() != cudaSuccess) return UNIPIN_ERR_CUDA;
     if (max_len <= budget) return UNIPIN_OK;
     if (p.row_bytes >= 64)

@@ -139,7 +139,8 @@ struct PgEvictParams {
     int* status;
 };
 
-constexpr int kPgSelThreads = 1024;
+constexpr int kPgSelThreads = 1024;      // of a selection block, and where no request is long
+constexpr int kPgSelThreadsShort = 256;
 constexpr int kPgMoveThreads = 256;
 
 // Larger float, larger key; -0 counts as 0 and NaN as less than every number.
@@ -156,12 +157,13 @@ __device__ __forceinline__ bool pg_evict_len_ok(const PgEvictParams& p, int n)
     return n >= 0 && n <= p.max_len && (long long)n <= (long long)p.max_pages * p.ps;
 }
 
-__global__ void __launch_bounds__(kPgSelThreads) paged_evict_select_kernel(const PgEvictParams p)
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads) paged_evict_select_kernel(const PgEvictParams p)
 {
     extern __shared__ uint32_t s_keys[];
     __shared__ uint32_t hist[256];
     __shared__ uint32_t s_prefix, s_need;
-    __shared__ int w_keep[32], w_tie[32];
+    __shared__ int w_keep[kThreads / 32], w_tie[kThreads / 32];
     const int r = blockIdx.y, h = blockIdx.x;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int n = p.lens[r];
@@ -169,13 +171,13 @@ __global__ void __launch_bounds__(kPgSelThreads) paged_evict_select_kernel(const
     int* kept = p.kept + ((size_t)r * p.H + h) * p.budget;
     bool bad = !pg_evict_len_ok(p, n);
     if (!bad)
-        for (int i = tid; i < (n + p.ps - 1) / p.ps; i += kPgSelThreads) {
+        for (int i = tid; i < (n + p.ps - 1) / p.ps; i += kThreads) {
             const int page = table[i];
             bad |= page < 0 || page >= p.S;
         }
     if (__syncthreads_or(bad)) {
         // nothing moves; the caller sees no kept row and a length of -1
-        for (int i = tid; i < p.budget; i += kPgSelThreads) kept[i] = -1;
+        for (int i = tid; i < p.budget; i += kThreads) kept[i] = -1;
         if (tid == 0) {
             report(p.status, (int)UNIPIN_ERR_OUT_OF_RANGE);
             if (h == 0) p.new_lens[r] = -1;
@@ -184,7 +186,7 @@ __global__ void __launch_bounds__(kPgSelThreads) paged_evict_select_kernel(const
     }
     if (tid == 0 && h == 0) p.new_lens[r] = min(n, p.budget);
     if (n <= p.budget) {
-        for (int i = tid; i < p.budget; i += kPgSelThreads) kept[i] = i < n ? i : -1;
+        for (int i = tid; i < p.budget; i += kThreads) kept[i] = i < n ? i : -1;
         return;
     }
     auto slot = [&](int j) -> float* {
@@ -196,14 +198,14 @@ __global__ void __launch_bounds__(kPgSelThreads) paged_evict_select_kernel(const
     const bool cached = mid <= p.keys_cap;
     auto key = [&](int i) -> uint32_t { return cached ? s_keys[i] : pg_order_key(*slot(m0 + i)); };
     if (cached)
-        for (int i = tid; i < mid; i += kPgSelThreads) s_keys[i] = pg_order_key(*slot(m0 + i));
+        for (int i = tid; i < mid; i += kThreads) s_keys[i] = pg_order_key(*slot(m0 + i));
     uint32_t prefix = 0, mask = 0;
     const bool any = need > 0;
     if (any) {
         for (int shift = 24; shift >= 0; shift -= 8) {
-            for (int i = tid; i < 256; i += kPgSelThreads) hist[i] = 0;
+            for (int i = tid; i < 256; i += kThreads) hist[i] = 0;
             __syncthreads();
-            for (int i0 = 0; i0 < mid; i0 += kPgSelThreads) {
+            for (int i0 = 0; i0 < mid; i0 += kThreads) {
                 const int i = i0 + tid;
                 const uint32_t x = i < mid ? key(i) : 0u;
                 const bool in = i < mid && (x & mask) == prefix;
@@ -245,7 +247,7 @@ __global__ void __launch_bounds__(kPgSelThreads) paged_evict_select_kernel(const
         __syncthreads();
     }
     // every key above `prefix` stays, and the first `need` rows whose key equals it
-    const int share = ((n + kPgSelThreads - 1) / kPgSelThreads) * 32;     // rows of a warp, whole groups of 32
+    const int share = ((n + kThreads - 1) / kThreads) * 32;     // rows of a warp, whole groups of 32
     const int j0 = min(warp * share, n), j1 = min(j0 + share, n);
     auto look = [&](int j, bool& keep, bool& tie) {
         keep = tie = false;
@@ -272,7 +274,8 @@ __global__ void __launch_bounds__(kPgSelThreads) paged_evict_select_kernel(const
     __syncthreads();
     int ties = 0, at = 0;    // ties and kept rows before this warp's
     {
-        const int tw = w_tie[lane], kw = w_keep[lane];
+        const bool is = lane < kThreads / 32;
+        const int tw = is ? w_tie[lane] : 0, kw = is ? w_keep[lane] : 0;
         int incl = tw;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
