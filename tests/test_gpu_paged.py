@@ -335,6 +335,15 @@ def test_evict_matches_plain(ub, D, Hkv, page, scales, budget, sinks, recent):
     _evict_case(ub, case, budget, sinks, recent)
 
 
+@pytest.mark.parametrize("budget,sinks,recent", [(1, 0, 0), (1, 1, 0), (64, 4, 16), (64, 64, 0), (64, 0, 64), (300, 0, 0)])
+def test_evict_in_the_larger_block(ub, budget, sinks, recent):
+    """The same lengths where max_len asks for the larger selection block, and lengths on both sides of it."""
+    case = PagedCase(36, [0, 1, 64, 65, 129, 400, 1024], 2, 32, 48, width=30)
+    _evict_case(ub, case, budget, sinks, recent, max_len=1400)
+    for n in (512, 513):
+        _evict_case(ub, PagedCase(37, [n, 7], 1, 32, 16), budget, sinks, recent)
+
+
 def test_evict_ties_zeros_and_odd_weights(ub):
     """Equal weights go to the lowest row; -0 is 0, negatives and infinities are ordered, NaN leaves first."""
     case = PagedCase(40, [500, 500, 500, 500], 1, 32, 16)
