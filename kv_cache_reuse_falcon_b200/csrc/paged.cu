@@ -292,7 +292,7 @@ int unipin_paged_decode_attn(const void* q, const void* k_self, const void* v_se
     if (rc != UNIPIN_OK) return rc;
     if ((k_self == nullptr) != (v_self == nullptr)) return UNIPIN_ERR_INVALID_ARG;
     if (R == 0) return UNIPIN_OK;
-    if (!q || !out || !page_table || !lens || (max_pages < 1 && max_len > 0)) return UNIPIN_ERR_INVALID_ARG;
+    if (!q || !out || !lens || ((!page_table || max_pages < 1) && max_len > 0)) return UNIPIN_ERR_INVALID_ARG;
     if ((long long)max_len > (long long)max_pages * pool->n_cap) return UNIPIN_ERR_OUT_OF_RANGE;
     if (!aligned16(q) || !aligned16(k_self) || !aligned16(v_self) || !aligned16(out)) return UNIPIN_ERR_MISALIGNED;
     if (workspace && !aligned16(workspace)) return UNIPIN_ERR_MISALIGNED;
@@ -378,7 +378,7 @@ int unipin_paged_evict(const unipin_kvpool* pool, int layer, float* key_weights,
     int rc = check_paged_pool(pool, pool->H, layer);
     if (rc != UNIPIN_OK) return rc;
     if (R == 0) return UNIPIN_OK;
-    if (!key_weights || !page_table || !lens || !kept || !new_lens || (max_pages < 1 && max_len > 0) ||
+    if (!key_weights || !lens || !kept || !new_lens || ((!page_table || max_pages < 1) && max_len > 0) ||
         new_lens == lens)
         return UNIPIN_ERR_INVALID_ARG;
     if ((long long)max_len > (long long)max_pages * pool->n_cap) return UNIPIN_ERR_OUT_OF_RANGE;

@@ -125,3 +125,37 @@ def test_a_dominant_own_key_does_not_hide_a_nan_value(ub):
     pv[0, 0, 0, 2, 7] = float("nan")
     out = ub.paged_decode_attn(*args, k_self=own, v_self=own)
     assert torch.isnan(out[0, 0, 7]) and (out[0, 0, :7] == 16).all()
+
+
+def test_calls_on_an_empty_cache(ub):
+    """No page yet (a page table of no columns): the own value, zeros without one, and nothing to evict."""
+    g = torch.Generator().manual_seed(23)
+    pk = torch.full((1, 4, 2, 16, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+    pv, w = pk.clone(), torch.zeros((1, 4, 2, 16), device="cuda")
+    table, lens = torch.empty((3, 0), dtype=torch.int32, device="cuda"), _i32([0, 0, 0])
+    q, own = _rnd(g, 3, 4, 64).cuda(), _rnd(g, 3, 2, 64).cuda()
+    for weights in (None, w):
+        out = ub.paged_decode_attn(q, table, lens, pk, pv, 0, 0, k_self=own, v_self=own, key_weights=weights)
+        assert torch.equal(out, own.float().repeat_interleave(2, 1))
+        assert (ub.paged_decode_attn(q, table, lens, pk, pv, 0, 0, key_weights=weights) == 0).all()
+    kept, fewer = ub.paged_evict(pk, pv, w, 0, table, lens, 0, 5)
+    assert (kept == -1).all() and fewer.tolist() == [0, 0, 0] and (w == 0).all()
+
+
+def test_decode_of_requests_that_share_pages(ub):
+    """A common prefix in the same pages: both requests read it, and its weights are the sum of theirs."""
+    g = torch.Generator().manual_seed(24)
+    Hkv, ps, D, H = 2, 16, 64, 4
+    pk, pv = _rnd(g, 1, 8, Hkv, ps, D), _rnd(g, 1, 8, Hkv, ps, D)
+    table, lens, q = [[5, 2, 7], [5, 2, 0]], [40, 33], _rnd(g, 2, H, D)
+    w = torch.zeros((1, 8, Hkv, ps), device="cuda")
+    out = ub.paged_decode_attn(q.cuda(), _i32(table), _i32(lens), pk.cuda(), pv.cuda(), 0, 48, key_weights=w)
+    want = torch.zeros((8, Hkv, ps), dtype=torch.float64)
+    for r in range(2):
+        k = torch.cat([pk[0, p] for p in table[r]], 1)[:, :lens[r]].transpose(0, 1)
+        v = torch.cat([pv[0, p] for p in table[r]], 1)[:, :lens[r]].transpose(0, 1)
+        ref, mag, wt = _plain(q[r], k, v)
+        assert ((out[r].cpu().double() - ref).abs() <= mag * (ROUND + SCORE) + 1e-6).all()
+        for j in range(lens[r]):
+            want[table[r][j // ps], :, j % ps] += wt[j]
+    assert ((w[0].cpu().double() - want).abs() <= want * (SCORE + 2.0 ** -22) + 1e-7).all()
