@@ -9,9 +9,11 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <initializer_list>
+#include <optional>
 #include <stdexcept>
 #include <string>
 
@@ -163,7 +165,9 @@ Window window_of(PyObject* window, PyObject* n_sinks)
 
 float scale_of(PyObject* scale, int64_t D) { return given(scale) ? (float)real(scale) : (float)(1.0 / std::sqrt((double)D)); }
 
-// The tensors lie on one CUDA device, which is current while this lives; the stream of the call.
+// The tensors lie on one CUDA device.  While this lives that device is current on the thread, and on it the stream
+// of the call: what the call allocates then belongs to that stream.  (Memory from the caller's current stream may
+// still have work queued there, which the call's stream does not wait for.)
 class Place {
 public:
     Place(std::initializer_list<const at::Tensor*> tensors, PyObject* stream) : device_((*tensors.begin())->device())
@@ -185,21 +189,25 @@ public:
             raw_ = reinterpret_cast<cudaStream_t>(PyLong_AsUnsignedLongLong(raw));
             Py_DECREF(raw);
             if (PyErr_Occurred()) throw PythonError();
-            other_ = raw_ != current.stream();
+            if (raw_ != current.stream()) {
+                caller_ = current;
+                stream_guard_.reset_stream(c10::cuda::getStreamFromExternal(raw_, device_.index()));
+            }
         }
     }
     void* stream() const { return raw_; }
-    // Memory allocated for this call must not go to others before its stream is done with it.
-    void made(const at::Tensor& t) const
+    // An output: the caller goes on with it on the stream that was current.
+    void handed_out(const at::Tensor& t) const
     {
-        if (other_ && t.defined()) t.record_stream(c10::cuda::getStreamFromExternal(raw_, device_.index()).unwrap());
+        if (caller_) t.record_stream(caller_->unwrap());
     }
 
 private:
     c10::Device device_;
     c10::cuda::OptionalCUDAGuard guard_;
+    c10::cuda::OptionalCUDAStreamGuard stream_guard_;
     cudaStream_t raw_ = nullptr;
-    bool other_ = false;
+    std::optional<c10::cuda::CUDAStream> caller_;   // where the call's stream is another
 };
 
 template <typename T = void>
@@ -207,12 +215,35 @@ T* address(const at::Tensor* t) { return t ? static_cast<T*>(t->data_ptr()) : nu
 
 const at::Tensor* optional(PyObject* o, const char* name) { return given(o) ? &tensor(o, name) : nullptr; }
 
-at::Tensor make(Sizes shape, at::ScalarType type, const at::Tensor& like)
-{
-    return at::empty(at::IntArrayRef(shape), like.options().dtype(type));
-}
+// An output argument of up to three dimensions: the tensor given, or one that is made under the call's stream.
+class Output {
+public:
+    Output(PyObject* o, const char* name, Sizes shape, at::ScalarType type) : type_(type), dims_(shape.size())
+    {
+        std::copy(shape.begin(), shape.end(), shape_);
+        if (!given(o)) return;
+        t_ = tensor(o, name);
+        fits(t_, name, type, shape);
+    }
+    const at::Tensor* lent() const { return t_.defined() ? &t_ : nullptr; }
+    const at::Tensor& in(const Place& at_, const at::Tensor& like)
+    {
+        if (!t_.defined()) {
+            t_ = at::empty(at::IntArrayRef(shape_, dims_), like.options().dtype(type_));
+            at_.handed_out(t_);
+        }
+        return t_;
+    }
 
-// The workspace argument: "auto" (a fresh buffer of `bytes`), None, or a contiguous tensor.
+private:
+    at::Tensor t_;
+    at::ScalarType type_;
+    size_t dims_;
+    int64_t shape_[3];
+};
+
+// The workspace argument: "auto" (a fresh buffer of `bytes`, of the current stream: the call's), None, or a contiguous
+// tensor.
 struct Space {
     at::Tensor made;
     const at::Tensor* tensor = nullptr;
@@ -226,7 +257,7 @@ struct Space {
             bytes = need();
             if (bytes == 0) return;
             bytes = (bytes + 15) / 16 * 16;
-            made = make({(int64_t)bytes}, at::kByte, like);
+            made = at::empty({(int64_t)bytes}, like.options().dtype(at::kByte));
             tensor = &made;
         } else if (given(o)) {
             tensor = &::tensor(o, "workspace");
@@ -236,19 +267,6 @@ struct Space {
         }
     }
 };
-
-// An output argument: the tensor given, or a fresh one.
-at::Tensor output(PyObject* o, const char* name, Sizes shape, at::ScalarType type, const at::Tensor& like, bool& fresh)
-{
-    fresh = !given(o);
-    if (fresh) {
-        if (!like.is_cuda()) throw ValueError("the tensors must lie on one CUDA device: " + like.device().str());
-        return make(shape, type, like);
-    }
-    const at::Tensor& t = tensor(o, name);
-    fits(t, name, type, shape);
-    return t;
-}
 
 PyObject* answer(int rc) { return PyLong_FromLong(rc); }
 
@@ -328,9 +346,9 @@ PyObject* decode(PyObject* const* a)
     const int layer = as_int(a[5]), max_len = as_int(a[6]);
     const bool fp32 = truth(a[13]);
     const float scale = scale_of(a[14], D);
-    bool fresh;
-    const at::Tensor out = output(a[12], "out", {R, H, D}, fp32 ? at::kFloat : at::kBFloat16, q, fresh);
-    const Place at_({&q, ks, vs, &table, &lens, &pk, &pv, w, &out, status}, a[17]);
+    Output made(a[12], "out", {R, H, D}, fp32 ? at::kFloat : at::kBFloat16);
+    const Place at_({&q, ks, vs, &table, &lens, &pk, &pv, w, made.lent(), status}, a[17]);
+    const at::Tensor& out = made.in(at_, q);
     const Space ws(a[15], q, [&] {
         return unipin_paged_decode_workspace_size(&pool, small(R, "q"), small(H, "q"), max_len, win.window, win.n_sinks,
                                                   w != nullptr);
@@ -341,8 +359,6 @@ PyObject* decode(PyObject* const* a)
         small(table.size(1), "page_table"), address<int>(&lens), small(R, "q"), small(H, "q"), small(D, "q"), max_len,
         win.window, win.n_sinks, scale, &pool, layer, address<float>(w), address(ws.tensor), ws.bytes, address<int>(status),
         at_.stream());
-    at_.made(ws.made);
-    if (fresh) at_.made(out);
     return answer(rc, out);
 }
 
@@ -360,16 +376,13 @@ PyObject* evict(PyObject* const* a)
     const at::Tensor& table = page_table(a[4], R);
     const at::Tensor* status = optional(a[12], "dev_status");
     const int layer = as_int(a[3]), max_len = as_int(a[6]), budget = as_int(a[7]);
-    bool fresh[2];
-    const at::Tensor kept = output(a[10], "kept", {R, pool.H, budget > 0 ? budget : 0}, at::kInt, lens, fresh[0]);
-    const at::Tensor fewer = output(a[11], "new_lens", {R}, at::kInt, lens, fresh[1]);
-    const Place at_({&pk, &pv, &w, &table, &lens, &kept, &fewer, status}, a[13]);
+    Output rows(a[10], "kept", {R, pool.H, budget > 0 ? budget : 0}, at::kInt), left(a[11], "new_lens", {R}, at::kInt);
+    const Place at_({&pk, &pv, &w, &table, &lens, rows.lent(), left.lent(), status}, a[13]);
+    const at::Tensor &kept = rows.in(at_, lens), &fewer = left.in(at_, lens);
     const int rc = unipin_paged_evict(&pool, layer, address<float>(&w), address<int>(&table),
                                       small(table.size(1), "page_table"), address<int>(&lens), small(R, "lens"), max_len,
                                       budget, as_int(a[8]), as_int(a[9]), address<int>(&kept), address<int>(&fewer),
                                       address<int>(status), at_.stream());
-    if (fresh[0]) at_.made(kept);
-    if (fresh[1]) at_.made(fewer);
     return answer(rc, kept, fewer);
 }
 
@@ -396,14 +409,13 @@ PyObject* prefill(PyObject* const* a)
     const bool fp32 = truth(a[9]);
     const at::Tensor *lse = optional(a[13], "lse"), *status = optional(a[11], "dev_status");
     if (lse) fits(*lse, "lse", at::kFloat, {x.T, x.H});
-    bool fresh;
-    const at::Tensor out = output(a[8], "out", {x.T, x.H, x.D}, fp32 ? at::kFloat : at::kBFloat16, x.q, fresh);
-    const Place at_({&x.q, &x.k, &x.v, &cu, &past, &out, lse, status}, a[12]);
+    Output made(a[8], "out", {x.T, x.H, x.D}, fp32 ? at::kFloat : at::kBFloat16);
+    const Place at_({&x.q, &x.k, &x.v, &cu, &past, made.lent(), lse, status}, a[12]);
+    const at::Tensor& out = made.in(at_, x.q);
     const int rc = unipin_windowed_prefill_attn(
         x.q.data_ptr(), x.k.data_ptr(), x.v.data_ptr(), out.data_ptr(), fp32, address<float>(lse), address<int>(&cu),
         address<int>(&past), small(B, "past_lens"), small(x.H, "q"), small(x.Hkv, "k"), small(x.D, "q"), as_int(a[5]),
         small(x.T, "q"), win.window, win.n_sinks, scale_of(a[10], x.D), address<int>(status), at_.stream());
-    if (fresh) at_.made(out);
     return answer(rc, out);
 }
 
@@ -424,11 +436,11 @@ PyObject* prefill_bwd(PyObject* const* a)
     const at::ScalarType kind = fp32 ? at::kFloat : at::kBFloat16;
     const int max_seqlen = as_int(a[8]);
     const at::Tensor* status = optional(a[17], "dev_status");
-    bool fresh[3];
-    const at::Tensor dq = output(a[13], "dq", {x.T, x.H, x.D}, kind, x.q, fresh[0]);
-    const at::Tensor dk = output(a[14], "dk", {x.T, x.Hkv, x.D}, kind, x.q, fresh[1]);
-    const at::Tensor dv = output(a[15], "dv", {x.T, x.Hkv, x.D}, kind, x.q, fresh[2]);
-    const Place at_({&x.q, &x.k, &x.v, &o, &g, &lse, &cu, &past, &dq, &dk, &dv, status}, a[18]);
+    Output made_q(a[13], "dq", {x.T, x.H, x.D}, kind), made_k(a[14], "dk", {x.T, x.Hkv, x.D}, kind),
+        made_v(a[15], "dv", {x.T, x.Hkv, x.D}, kind);
+    const Place at_({&x.q, &x.k, &x.v, &o, &g, &lse, &cu, &past, made_q.lent(), made_k.lent(), made_v.lent(), status},
+                    a[18]);
+    const at::Tensor &dq = made_q.in(at_, x.q), &dk = made_k.in(at_, x.q), &dv = made_v.in(at_, x.q);
     const Space ws(a[16], x.q, [&] {
         return unipin_windowed_prefill_bwd_workspace_size(small(B, "past_lens"), small(x.H, "q"), small(x.Hkv, "k"),
                                                           small(x.D, "q"), max_seqlen, small(x.T, "q"), win.window,
@@ -440,10 +452,6 @@ PyObject* prefill_bwd(PyObject* const* a)
         dk.data_ptr(), dv.data_ptr(), fp32, address<int>(&cu), address<int>(&past), small(B, "past_lens"), small(x.H, "q"),
         small(x.Hkv, "k"), small(x.D, "q"), max_seqlen, small(x.T, "q"), win.window, win.n_sinks, scale_of(a[11], x.D),
         address(ws.tensor), ws.bytes, address<int>(status), at_.stream());
-    at_.made(ws.made);
-    if (fresh[0]) at_.made(dq);
-    if (fresh[1]) at_.made(dk);
-    if (fresh[2]) at_.made(dv);
     return answer(rc, dq, dk, dv);
 }
 

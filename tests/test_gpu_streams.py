@@ -1,0 +1,96 @@
+"""Calls on a stream that is not the current one: what a call allocates belongs to the call's stream, so that
+nothing still queued on the current stream can touch it, and outputs are not handed out again while the
+current stream uses them.  The allocator's own record says under which stream each allocation was made: no
+timing is needed."""
+
+import contextlib
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ub():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from kv_cache_reuse_falcon_b200 import binding
+    return binding
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def _rnd(*shape):
+    return torch.randn(*shape, device="cuda").to(torch.bfloat16)
+
+
+@contextlib.contextmanager
+def allocations(into):
+    """The stream of every allocation made inside."""
+    torch.cuda.memory._record_memory_history(max_entries=1000, stacks="python")
+    try:
+        yield
+        for e in torch.cuda.memory._snapshot()["device_traces"][torch.cuda.current_device()]:
+            if e["action"] == "alloc":
+                into.append(e["stream"])
+    finally:
+        torch.cuda.memory._record_memory_history(enabled=None)
+
+
+def paged_calls(ub):
+    """name -> (call of a stream, allocations of the call)"""
+    q, x = _rnd(3, 8, 64), [_rnd(200, h, 64) for h in (4, 2, 2)]
+    pk, pv = _rnd(1, 64, 2, 16, 64), _rnd(1, 64, 2, 16, 64)
+    w = torch.rand(1, 64, 2, 16, device="cuda")
+    table, lens = _i32(torch.arange(60).reshape(3, 20).tolist()), _i32([300, 7, 150])
+    cu, past = _i32([0, 120, 200]), _i32([100, 60])
+    lse = torch.empty(200, 4, device="cuda")
+    o = ub.windowed_prefill_attn(*x, cu, past, 120, 30, 1, out_fp32=False, lse=lse)
+    return {
+        "decode": (lambda s: [ub.paged_decode_attn(q, table, lens, pk, pv, 0, 300, key_weights=w, stream=s)], 2),
+        "evict": (lambda s: ub.paged_evict(pk, pv, w, 0, table, lens, 300, 150, stream=s), 2),
+        "prefill": (lambda s: [ub.windowed_prefill_attn(*x, cu, past, 120, 30, 1, stream=s)], 1),
+        "prefill_bwd": (lambda s: ub.windowed_prefill_bwd(*x, o, x[0], lse, cu, past, 120, 30, 1, stream=s), 4),
+    }
+
+
+def _check_allocations(call, count):
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    for s, want in ((stream, stream.cuda_stream), (None, torch.cuda.current_stream().cuda_stream),
+                    (torch.cuda.current_stream(), torch.cuda.current_stream().cuda_stream)):
+        seen = []
+        with allocations(seen):
+            out = call(s)
+        assert seen == [want] * count
+        torch.cuda.synchronize()
+        del out
+    assert torch.cuda.current_stream() == torch.cuda.default_stream()      # as the caller left it
+
+
+def _check_hand_out(call):
+    """An output that the current stream still uses does not go to the call's stream again."""
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    out = list(call(stream))
+    torch.cuda.current_stream().wait_stream(stream)
+    mine = {(t.untyped_storage().data_ptr(), t.untyped_storage().nbytes()) for t in out}
+    torch.cuda._sleep(400_000_000)          # about 0.2 s in which the current stream is not done with it
+    used = [t.clone() for t in out]
+    shapes = [(t.shape, t.dtype) for t in out]
+    del out
+    with torch.cuda.stream(stream):
+        again = [torch.empty(s, dtype=d, device="cuda") for s, d in shapes]
+    assert not mine & {(t.untyped_storage().data_ptr(), t.untyped_storage().nbytes()) for t in again}
+    torch.cuda.synchronize()
+    del used, again
+
+
+@pytest.mark.parametrize("name", ["decode", "evict", "prefill", "prefill_bwd"])
+def test_paged_and_windowed_calls_allocate_under_their_stream(ub, name):
+    call, count = paged_calls(ub)[name]
+    _check_allocations(call, count)
+    _check_hand_out(call)
