@@ -212,14 +212,28 @@ def _pool(pool_k: torch.Tensor, pool_v: torch.Tensor, pool_scales=None) -> KVPoo
     return KVPool(pool_k.data_ptr(), pool_v.data_ptr(), *shape, POOL_E4M3, ks, vs)
 
 
-def _workspace(workspace, nbytes: int, device):
+def _empty(shape, dtype, device, stream, output: bool = True):
+    """Memory for a call on `stream`, allocated under it: memory of another stream may still have work queued
+    there.  An output is recorded for the current stream, on which the caller goes on with it."""
+    if stream is None or stream.cuda_stream == torch.cuda.current_stream(device).cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if output:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _workspace(workspace, nbytes: int, device, stream):
     """'auto': a fresh device buffer of nbytes; None: no workspace; else the given tensor."""
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError("workspace must be 'auto', None or a CUDA tensor")
         if nbytes <= 0:
             return None, 0
-        workspace = torch.empty((nbytes + 15) // 16 * 4, dtype=torch.float32, device=device)
+        workspace = _empty((nbytes + 15) // 16 * 4, torch.float32, device, stream, output=False)
     if workspace is None:
         return None, 0
     if not workspace.is_cuda or not workspace.is_contiguous():
@@ -245,7 +259,7 @@ def masked_prefill_attn(q, k, v, cu_seqlens, past_lens, max_seqlen: int, out=Non
     _index(cu_seqlens, "cu_seqlens", B + 1)
     _index(past_lens, "past_lens", B)
     if out is None:
-        out = torch.empty((T, H, D), dtype=torch.float32 if out_fp32 else torch.bfloat16, device=q.device)
+        out = _empty((T, H, D), torch.float32 if out_fp32 else torch.bfloat16, q.device, stream)
     elif out.dtype != (torch.float32 if out_fp32 else torch.bfloat16) or out.shape != q.shape or not out.is_contiguous():
         raise ValueError("out has the wrong dtype or shape")
     pool = None
@@ -255,7 +269,7 @@ def masked_prefill_attn(q, k, v, cu_seqlens, past_lens, max_seqlen: int, out=Non
     if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, H) or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 tensor [T, H]")
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    ws, ws_bytes = _workspace(workspace, masked_prefill_workspace_size(), q.device)
+    ws, ws_bytes = _workspace(workspace, masked_prefill_workspace_size(), q.device, stream)
     rc = LIB.unipin_masked_prefill_attn(_ptr(q), _ptr(k), _ptr(v), _ptr(out), int(bool(out_fp32)), _ptr(lse),
                                         _ptr(cu_seqlens), _ptr(past_lens), B, H, H_kv, D, int(max_seqlen), T, scale,
                                         ctypes.byref(pool) if pool is not None else None,
@@ -287,11 +301,11 @@ def masked_prefill_bwd(q, k, v, out, dout, lse, cu_seqlens, past_lens, max_seqle
     grads = []
     for g, heads in ((dq, H), (dk, H_kv), (dv, H_kv)):
         if g is None:
-            g = torch.empty((T, heads, D), dtype=torch.float32, device=q.device)
+            g = _empty((T, heads, D), torch.float32, q.device, stream)
         elif g.dtype != torch.float32 or tuple(g.shape) != (T, heads, D) or not g.is_contiguous():
             raise ValueError("gradient outputs must be contiguous float32: dq [T, H, D], dk and dv [T, H_kv, D]")
         grads.append(g)
-    ws, ws_bytes = _workspace(workspace, masked_prefill_bwd_workspace_size(T, H), q.device)
+    ws, ws_bytes = _workspace(workspace, masked_prefill_bwd_workspace_size(T, H), q.device, stream)
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     rc = LIB.unipin_masked_prefill_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(dout), _ptr(lse),
                                        _ptr(grads[0]), _ptr(grads[1]), _ptr(grads[2]), _ptr(cu_seqlens),
@@ -351,11 +365,11 @@ def rank_decode_attn(q_c, k_c, v_c, cu_seqlens_c, slot_ids, past_lens, pool_k, p
     _index(slot_ids, "slot_ids", R)
     _index(past_lens, "past_lens", R)
     if out is None:
-        out = torch.empty((T, H, D), dtype=torch.float32 if out_fp32 else torch.bfloat16, device=q_c.device)
+        out = _empty((T, H, D), torch.float32 if out_fp32 else torch.bfloat16, q_c.device, stream)
     elif out.dtype != (torch.float32 if out_fp32 else torch.bfloat16) or out.shape != q_c.shape or not out.is_contiguous():
         raise ValueError("out has the wrong dtype or shape")
     ws, ws_bytes = _workspace(workspace, int(LIB.unipin_rank_decode_pool_workspace_size(
-        ctypes.byref(pool), R, H, int(max_k), T)) if isinstance(workspace, str) else 0, q_c.device)
+        ctypes.byref(pool), R, H, int(max_k), T)) if isinstance(workspace, str) else 0, q_c.device, stream)
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     rc = LIB.unipin_rank_decode_attn(_ptr(q_c), _ptr(k_c), _ptr(v_c), _ptr(out), int(bool(out_fp32)),
                                      _ptr(cu_seqlens_c), _ptr(slot_ids), _ptr(past_lens), R, H, D, int(max_k), T,
@@ -409,7 +423,7 @@ def selftest_exp2(x: torch.Tensor, stream=None) -> torch.Tensor:
     """The softmax's FMA-pipe exp2 on a CUDA float32 tensor."""
     if x.dtype != torch.float32 or not x.is_cuda or not x.is_contiguous():
         raise ValueError("x must be a contiguous CUDA float32 tensor")
-    y = torch.empty_like(x)
+    y = _empty(x.shape, x.dtype, x.device, stream)
     _check(LIB.unipin_selftest_exp2(_ptr(x), _ptr(y), x.numel(), _stream(stream)), "unipin_selftest_exp2")
     return y
 

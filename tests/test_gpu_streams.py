@@ -94,3 +94,47 @@ def test_paged_and_windowed_calls_allocate_under_their_stream(ub, name):
     call, count = paged_calls(ub)[name]
     _check_allocations(call, count)
     _check_hand_out(call)
+
+
+def slot_calls(ub):
+    x = [_rnd(200, h, 64) for h in (4, 2, 2)]
+    cu, past, slots = _i32([0, 120, 200]), _i32([100, 60]), _i32([1, 0])
+    pk, pv = _rnd(1, 2, 2, 128, 64), _rnd(1, 2, 2, 128, 64)
+    pk8, pv8 = (torch.zeros(1, 2, 2, 128, 64, dtype=torch.uint8, device="cuda") for _ in range(2))
+    lse = torch.empty(200, 4, device="cuda")
+    o = ub.masked_prefill_attn(*x, cu, past, 120, out_fp32=False, lse=lse)
+    cu_c = _i32([0, 120, 200])
+    y = torch.rand(1000, device="cuda")
+    return {
+        "prefill": (lambda s: [ub.masked_prefill_attn(*x, cu, past, 120, stream=s)], 2),
+        "prefill_bwd": (lambda s: ub.masked_prefill_bwd(*x, o, x[0], lse, cu, past, 120, stream=s), 4),
+        "decode": (lambda s: [ub.rank_decode_attn(*x, cu_c, slots, past, pk, pv, 0, 120, stream=s)], 2),
+        "decode_e4m3": (lambda s: [ub.rank_decode_attn(*x, cu_c, slots, past, pk8, pv8, 0, 120, stream=s,
+                                                       pool_scales=(0.5, 0.5))], 2),
+        "exp2": (lambda s: [ub.selftest_exp2(y, stream=s)], 1),
+    }
+
+
+@pytest.mark.parametrize("name", ["prefill", "prefill_bwd", "decode", "decode_e4m3", "exp2"])
+def test_slot_pool_calls_allocate_under_their_stream(ub, name):
+    call, count = slot_calls(ub)[name]
+    _check_allocations(call, count)
+    _check_hand_out(call)
+
+
+def test_a_foreign_stream_object_is_taken_by_its_handle(ub):
+    """Anything with a `cuda_stream`, as the calls' own look-up of the handle allows."""
+    class Handle:
+        def __init__(self, stream):
+            self.cuda_stream = stream.cuda_stream
+
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    for calls in (paged_calls(ub), slot_calls(ub)):
+        call, count = calls["prefill"]
+        torch.cuda.synchronize()
+        want, seen = call(None), []
+        with allocations(seen):
+            got = call(Handle(stream))
+        torch.cuda.synchronize()
+        assert seen == [stream.cuda_stream] * count and torch.equal(got[0], want[0])
