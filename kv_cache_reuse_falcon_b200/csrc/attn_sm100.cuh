@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // A timeout recorded earlier means a block of this or a previous launch
     // gave up; later blocks skip their work instead of waiting again.
-    if (p.status && *reinterpret_cast<volatile int*>(p.status) == (int)UNIPIN_ERR_DEVICE_TIMEOUT) return;
+    if (block_timed_out(status_seen(p.status), (int)UNIPIN_ERR_DEVICE_TIMEOUT)) return;
     if ((smem_u32(smem) & 1023u) != 0) {   // the layout needs 1024-byte aligned tiles
         if (threadIdx.x == 0) report(p.status, (int)UNIPIN_ERR_CUDA);
         return;

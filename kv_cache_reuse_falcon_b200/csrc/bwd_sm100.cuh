@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kBwThreads, 1)
     if (!bw_segment_ok(p, b, tok0, len, npast)) return;   // bwd_prep_kernel zeroed and reported it
     const int j0 = kt * kBwRows;
     if (j0 >= npast) return;
-    if (p.status && *reinterpret_cast<volatile int*>(p.status) == (int)UNIPIN_ERR_DEVICE_TIMEOUT) return;
+    if (block_timed_out(status_seen(p.status), (int)UNIPIN_ERR_DEVICE_TIMEOUT)) return;
     if ((smem_u32(smem) & 1023u) != 0) {
         if (threadIdx.x == 0) report(p.status, (int)UNIPIN_ERR_CUDA);
         return;

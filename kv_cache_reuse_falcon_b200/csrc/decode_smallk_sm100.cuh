@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(kSkThreads, SkCfg<D, N, kE4M3>::kCtasPerSm)
 
     const int warp = threadIdx.x / 32;
     const int lane = threadIdx.x % 32;
-    if (p.status && *reinterpret_cast<volatile int*>(p.status) == (int)UNIPIN_ERR_DEVICE_TIMEOUT) return;
+    if (block_timed_out(status_seen(p.status), (int)UNIPIN_ERR_DEVICE_TIMEOUT)) return;
     if ((smem_u32(smem) & 1023u) != 0) {
         if (threadIdx.x == 0) report(p.status, (int)UNIPIN_ERR_CUDA);
         return;

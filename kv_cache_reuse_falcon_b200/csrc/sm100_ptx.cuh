@@ -185,6 +185,21 @@ struct WaitCtl {
     int timeout_code;         // value stored into *status on expiry
 };
 
+// Whether a wait of an earlier block or launch ran out of time: later blocks then skip their work instead of
+// waiting again.  One thread reads the call's status word (may be null), and all threads of the block take its
+// answer: another block may record its timeout at any moment, and a block of which some warps left and others
+// went on would run on barriers and tensor memory that nobody set up.  (Two steps, so that the load's latency
+// can overlap others.)
+__device__ __forceinline__ int status_seen(const int* status)
+{
+    return status && threadIdx.x == 0 ? *reinterpret_cast<const volatile int*>(status) : 0;
+}
+
+__device__ __forceinline__ bool block_timed_out(int seen, int timeout_code)
+{
+    return __syncthreads_or(seen == timeout_code);
+}
+
 // Wait for phase `parity` of `bar` to complete.  Returns false if the wait
 // ran out of time (then sets the abort flag and the status word) or if
 // another wait of this CTA already aborted.

@@ -433,12 +433,11 @@ __device__ __forceinline__ void wb_body(const CUtensorMap& tm_r0, const CUtensor
         tma_prefetch_map(&tm_s0);
         tma_prefetch_map(&tm_s1);
     }
-    // a timeout recorded earlier: later blocks skip their work instead of waiting again
-    const int failed = p.status ? *reinterpret_cast<volatile int*>(p.status) : 0;
+    const int seen = status_seen(p.status);
     WbItem it;
     WinSegment s;
     const bool work = wb_item<kKV>(p, block, it, s);
-    if (!work || failed == (int)UNIPIN_ERR_DEVICE_TIMEOUT) {
+    if (!work || block_timed_out(seen, (int)UNIPIN_ERR_DEVICE_TIMEOUT)) {
         asm volatile("griddepcontrol.wait;" ::: "memory");   // no block ends before the prep kernel
         return;
     }

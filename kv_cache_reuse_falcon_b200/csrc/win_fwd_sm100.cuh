@@ -149,8 +149,7 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
         tma_prefetch_map(&tm_k);
         tma_prefetch_map(&tm_v);
     }
-    // a timeout recorded earlier: later blocks skip their work instead of waiting again
-    const int failed = p.status ? *reinterpret_cast<volatile int*>(p.status) : 0;
+    const int seen = status_seen(p.status);
     if ((smem_u32(smem) & 1023u) != 0) {   // the layout needs 1024-byte aligned tiles
         if (threadIdx.x == 0) report(p.status, (int)UNIPIN_ERR_CUDA);
         return;
@@ -164,7 +163,7 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
     const int r0 = t0 * kWinRes;
     const WinSegment s = win_segment(p.cu, p.past, b, p.max_rows, p.total_rows);
     if (!s.ok && t0 == 0 && h == 0 && threadIdx.x == 0) report(p.status, (int)UNIPIN_ERR_OUT_OF_RANGE);
-    if (!s.rows_ok || r0 >= s.len || failed == (int)UNIPIN_ERR_DEVICE_TIMEOUT) return;
+    if (!s.rows_ok || r0 >= s.len || block_timed_out(seen, (int)UNIPIN_ERR_DEVICE_TIMEOUT)) return;
     if (!s.ok) {
         // a history length out of range: zeros
         const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
