@@ -48,8 +48,9 @@
 // or a row stands behind most stalls) and the first and last units of a block; the smallest calls are one
 // chain: lengths, page, rows, S, P, O, join of the warps.
 // Scores, row maxima, row sums and O are float32.  P is rounded to the type of
-// V's fragment (bfloat16; float16 over E4M3 codes), as in the prefill: one
-// rounding of relative size <= 2^-8 (2^-11) per weight, independent of the others.
+// V's fragment (bfloat16; float16 over E4M3 codes with power-of-two scales), as
+// in the prefill: one rounding of relative size <= 2^-8 (2^-11, see PgWeights) per
+// weight, independent of the others.
 //
 // E4M3 pools: attention reads code c as bf16(value(c) * scale).  Where both
 // scales are powers of two that is value(c) * scale exactly, so the codes go to
@@ -74,9 +75,19 @@ namespace unipin {
 constexpr int kPgWarps = 4;
 constexpr int kPgThreads = 32 * kPgWarps;
 constexpr float kPgLog2e = 1.4426950408889634f;
-constexpr float kPgRescaleLog2 = 8.0f;           // O is rescaled only when a row max grows by > 2^8
 
 enum PgMode { kPgBf16 = 0, kPgE4M3Pow2 = 1, kPgE4M3Any = 2 };
+
+// O is rescaled only when a row's maximum grows by more than 2^kRescale, and weights are held as 2^kLift times
+// themselves.  In float16 a weight below 2^-14 loses bits and one below 2^-25 is gone, while the row's sum
+// still counts it: so the weights use float16's whole range, the largest of a row in [2^14, 2^15].  Then weights
+// down to 2^-28 of the largest are rounded by 2^-11 of themselves and smaller ones by 2^-39 of the largest,
+// 2^-9 in all for the longest row that a call takes (2^30).
+template <int kMode>
+struct PgWeights {
+    static constexpr float kRescale = kMode == kPgE4M3Pow2 ? 1.0f : 8.0f;
+    static constexpr float kLift = kMode == kPgE4M3Pow2 ? 14.0f : 0.0f;
+};
 
 template <int D, int kMode>
 struct PgCfg {
@@ -414,6 +425,7 @@ template <int D, int kMode, int kNG>
 __global__ void __launch_bounds__(kPgThreads, PgCfg<D, kMode>::kBlocksPerSm) paged_decode_kernel(const PgParams p)
 {
     using C = PgCfg<D, kMode>;
+    using W = PgWeights<kMode>;
     constexpr bool kHalf = kMode == kPgE4M3Pow2;
     constexpr int MT = D / 16;                      // k-steps of S^T, m-tiles of O^T
     extern __shared__ __align__(1024) uint8_t smem[];   // (fragment addresses are formed by xor)
@@ -671,7 +683,7 @@ __global__ void __launch_bounds__(kPgThreads, PgCfg<D, kMode>::kBlocksPerSm) pag
                     top[n][e] = fmaxf(s[n][0][e], s[n][0][e + 2]);
 #pragma unroll
                     for (int k = 1; k < KT; ++k) top[n][e] = max3f(top[n][e], s[n][k][e], s[n][k][e + 2]);
-                    grow |= top[n][e] > m[n][e] + kPgRescaleLog2;
+                    grow |= top[n][e] > m[n][e] + W::kRescale;
                 }
             }
             if (__any_sync(0xffffffffu, grow)) {
@@ -698,7 +710,8 @@ __global__ void __launch_bounds__(kPgThreads, PgCfg<D, kMode>::kBlocksPerSm) pag
             uint32_t pb[kNG][KT][2];
 #pragma unroll
             for (int n = 0; n < kNG; ++n) {
-                const float u0 = m[n][0] == -INFINITY ? 0.f : m[n][0], u1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+                const float u0 = m[n][0] == -INFINITY ? 0.f : m[n][0] - W::kLift;
+                const float u1 = m[n][1] == -INFINITY ? 0.f : m[n][1] - W::kLift;
 #pragma unroll
                 for (int k = 0; k < KT; ++k) {
                     const float e0 = ex2_approx(s[n][k][0] - u0), e1 = ex2_approx(s[n][k][1] - u1);
@@ -758,7 +771,7 @@ __global__ void __launch_bounds__(kPgThreads, PgCfg<D, kMode>::kBlocksPerSm) pag
                 sum += __shfl_xor_sync(0xffffffffu, sum, 8);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 16);
                 if (g == 0) {
-                    sMl[(warp * 16 + n * 8 + 2 * t + e) * 2] = m[n][e];
+                    sMl[(warp * 16 + n * 8 + 2 * t + e) * 2] = m[n][e] - W::kLift;   // what l and O are relative to
                     sMl[(warp * 16 + n * 8 + 2 * t + e) * 2 + 1] = sum;
                 }
             }
