@@ -170,8 +170,8 @@ __global__ void __launch_bounds__(kThreads) paged_evict_select_kernel(const PgEv
     const int* table = p.table + (size_t)r * p.max_pages;
     int* kept = p.kept + ((size_t)r * p.H + h) * p.budget;
     bool bad = !pg_evict_len_ok(p, n);
-    if (!bad)
-        for (int i = tid; i < (n + p.ps - 1) / p.ps; i += kThreads) {
+    if (!bad && n > 0)
+        for (int i = tid, last = p.page_of(n - 1); i <= last; i += kThreads) {   // (n + ps may pass 31 bits)
             const int page = table[i];
             bad |= page < 0 || page >= p.S;
         }
