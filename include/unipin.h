@@ -411,6 +411,7 @@ size_t unipin_paged_decode_workspace_size(const unipin_kvpool* pool, int R, int 
  *   new_lens       device int32 [R], not lens itself: min(n_r, budget).  lens stays as it is,
  *                  so that every layer can be evicted before the lengths are swapped.
  *   max_len        host int >= every lens[r]
+ *   budget         1 .. 2^30 (max_len: nothing is evicted)
  * A request whose length or a page id is out of range keeps its rows and gets
  * kept = -1 and new_lens = -1.
  */

@@ -376,7 +376,9 @@ PyObject* evict(PyObject* const* a)
     const at::Tensor& table = page_table(a[4], R);
     const at::Tensor* status = optional(a[12], "dev_status");
     const int layer = as_int(a[3]), max_len = as_int(a[6]), budget = as_int(a[7]);
-    Output rows(a[10], "kept", {R, pool.H, budget > 0 ? budget : 0}, at::kInt), left(a[11], "new_lens", {R}, at::kInt);
+    // (a budget that the call refuses gets no memory)
+    const int64_t places = budget > 0 && budget <= (1 << 30) ? budget : 0;
+    Output rows(a[10], "kept", {R, pool.H, places}, at::kInt), left(a[11], "new_lens", {R}, at::kInt);
     const Place at_({&pk, &pv, &w, &table, &lens, rows.lent(), left.lent(), status}, a[13]);
     const at::Tensor &kept = rows.in(at_, lens), &fewer = left.in(at_, lens);
     const int rc = unipin_paged_evict(&pool, layer, address<float>(&w), address<int>(&table),

@@ -382,7 +382,7 @@ int unipin_paged_evict(const unipin_kvpool* pool, int layer, float* key_weights,
         new_lens == lens)
         return UNIPIN_ERR_INVALID_ARG;
     if ((long long)max_len > (long long)max_pages * pool->n_cap) return UNIPIN_ERR_OUT_OF_RANGE;
-    if (R > 65535 || pool->H > 65535 || max_len > (1 << 30)) return UNIPIN_ERR_INVALID_ARG;
+    if (R > 65535 || pool->H > 65535 || max_len > (1 << 30) || budget > (1 << 30)) return UNIPIN_ERR_INVALID_ARG;
     rc = ensure_paged();
     if (rc != UNIPIN_OK) return rc;
     PgEvictParams p = {};
