@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kPgWriteThreads) paged_write_kernel(const PgWr
     const int b = blockIdx.y;
     const int n = p.new_lens[b];
     const int start = p.cu[b];
-    const int len = p.cu[b + 1] - start;
+    const long long len = (long long)p.cu[b + 1] - start;
     const int first = p.first[b];
     if (n < 0 || n > len || n > p.max_new || first < 0 || start < 0 ||
         (long long)start + n > (long long)p.total_tokens ||

@@ -36,3 +36,14 @@ def test_evict_checks_the_pages_of_the_longest_request(ub):
     kept, fewer = ub.paged_evict(pk, pv, w, 0, _i32([[0]]), _i32([64]), 1 << 30, 40, dev_status=status)
     torch.cuda.synchronize()
     assert int(status.item()) == 0 and fewer.tolist() == [40] and kept[0, 0].tolist() == list(range(24, 64))
+
+
+def test_write_refuses_a_segment_that_ends_far_before_its_start(ub):
+    """The difference of the two ends passes 31 bits and must not come out as a long segment."""
+    g = torch.Generator().manual_seed(2)
+    k = torch.randn(16, 1, 32, generator=g).to(torch.bfloat16).cuda()
+    pk = torch.zeros((1, 2, 1, 8, 32), dtype=torch.bfloat16, device="cuda")
+    pv, status = torch.zeros_like(pk), torch.zeros(1, dtype=torch.int32, device="cuda")
+    ub.paged_pool_write(pk, pv, 0, k, k, _i32([4, -2 ** 31]), _i32([2]), _i32([[0]]), _i32([0]), 2, dev_status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == -4 and (pk == 0).all() and (pv == 0).all()
