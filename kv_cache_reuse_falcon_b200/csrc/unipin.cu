@@ -324,9 +324,10 @@ WbPlan win_bwd_plan(int B, int H, int H_kv, int D, int max_seqlen, int total_tok
     pl.dvec = room((size_t)total_tokens * H * 4);
     pl.dself = room((size_t)total_tokens * H * 4);
     pl.counters = room((size_t)pl.n_counters * 4);
-    const size_t slots = !cut ? 0
-                              : (size_t)B * H_kv * ((size_t)pl.sink_tiles * pl.sink_pieces +
-                                                    (size_t)(pl.tiles - pl.sink_tiles) * pl.win_pieces);
+    // sums of the tiles that are cut, and of no others
+    const size_t slots = (size_t)B * H_kv *
+                         ((pl.sink_pieces > 1 ? (size_t)pl.sink_tiles * pl.sink_pieces : 0) +
+                          (pl.win_pieces > 1 ? (size_t)(pl.tiles - pl.sink_tiles) * pl.win_pieces : 0));
     pl.part = room(slots * 2 * kWinRes * D * 4);
     return pl;
 }

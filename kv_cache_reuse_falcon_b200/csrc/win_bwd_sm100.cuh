@@ -288,7 +288,7 @@ struct WbItem {
     WinSweep sweep;      // the streamed tiles (KV: of each of the G query heads in turn)
     int first, total;    // the block's part of them: its first, and how many
     int piece, pieces;   // KV: which of how many pieces of the tile's sweep
-    size_t slot, tile;   // KV: number of the tile's first piece, and of the tile
+    size_t slot, tile;   // KV: number of the tile's first piece (of the tiles that are cut), and of the tile
 };
 
 template <bool kKV>
@@ -315,7 +315,7 @@ __device__ __forceinline__ bool wb_item(const WbParams& p, unsigned block, WbIte
             t -= sinks;
             it.piece = t % most;
             t /= most;
-            it.slot = (size_t)bh_count * sinks + ((size_t)bh * (p.tiles - p.sink_tiles) + t) * most;
+            it.slot = (size_t)bh_count * (p.sink_pieces > 1 ? sinks : 0) + ((size_t)bh * (p.tiles - p.sink_tiles) + t) * most;
             t += p.sink_tiles;
         }
         it.tile = (size_t)bh * p.tiles + t;
