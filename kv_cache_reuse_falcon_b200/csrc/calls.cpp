@@ -281,9 +281,14 @@ PyObject* answer(int rc, const Ts&... ts)
     return r;
 }
 
-template <PyObject* (*F)(PyObject* const*)>
-PyObject* guarded(PyObject*, PyObject* const* a, Py_ssize_t)
+// A method: kArgs arguments by position.
+template <PyObject* (*F)(PyObject* const*), int kArgs>
+PyObject* guarded(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
+    if (n != kArgs) {
+        PyErr_Format(PyExc_TypeError, "%d arguments by position, got %zd", kArgs, n);
+        return nullptr;
+    }
     try {
         return F(a);
     } catch (const ValueError& e) {
@@ -459,11 +464,11 @@ PyObject* prefill_bwd(PyObject* const* a)
 
 // The binding passes every argument by position.
 PyMethodDef methods[] = {
-    {"pool_write", (PyCFunction)(void (*)())&guarded<pool_write>, METH_FASTCALL, nullptr},
-    {"decode", (PyCFunction)(void (*)())&guarded<decode>, METH_FASTCALL, nullptr},
-    {"evict", (PyCFunction)(void (*)())&guarded<evict>, METH_FASTCALL, nullptr},
-    {"prefill", (PyCFunction)(void (*)())&guarded<prefill>, METH_FASTCALL, nullptr},
-    {"prefill_bwd", (PyCFunction)(void (*)())&guarded<prefill_bwd>, METH_FASTCALL, nullptr},
+    {"pool_write", (PyCFunction)(void (*)())&guarded<pool_write, 14>, METH_FASTCALL, nullptr},
+    {"decode", (PyCFunction)(void (*)())&guarded<decode, 19>, METH_FASTCALL, nullptr},
+    {"evict", (PyCFunction)(void (*)())&guarded<evict, 14>, METH_FASTCALL, nullptr},
+    {"prefill", (PyCFunction)(void (*)())&guarded<prefill, 14>, METH_FASTCALL, nullptr},
+    {"prefill_bwd", (PyCFunction)(void (*)())&guarded<prefill_bwd, 19>, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 
