@@ -2,13 +2,15 @@
 
 Argument marshalling only: torch tensors supply device pointers and the
 current CUDA stream; every step of the computation runs in the CUDA kernels of
-``libunipin.so``.  If it or ``_calls.so`` is missing or fails to load, importing
-this module raises: there is no fallback.
+``libunipin.so``.  If it is missing or fails to load, importing this module
+raises; if the compiled calls' module is, the first paged or windowed call does:
+there is no fallback.
 """
 
 from __future__ import annotations
 
 import ctypes
+import importlib
 import math
 import os
 from typing import Optional
@@ -151,7 +153,23 @@ def _load(path: str = _LIB_PATH):
 
 LIB = _load()
 
-from kv_cache_reuse_falcon_b200 import _calls  # noqa: E402  (links against the library loaded above)
+
+class _CallsOnDemand:
+    """Stands for the compiled calls (csrc/calls.cpp, built against the installed torch) until one is used: the
+    other calls need the library alone."""
+
+    def __getattr__(self, name):
+        global _calls
+        from kv_cache_reuse_falcon_b200 import build
+        module = build.calls_module()
+        try:
+            _calls = importlib.import_module("kv_cache_reuse_falcon_b200." + module)
+        except ImportError as e:
+            raise ImportError("%s: %s (build it with kv_cache_reuse_falcon_b200.build.build())" % (module, e)) from e
+        return getattr(_calls, name)
+
+
+_calls = _CallsOnDemand()
 
 
 def _ptr(t: Optional[torch.Tensor]):

@@ -1,10 +1,11 @@
-"""Build the sm_100a shared library ``libunipin.so`` (nvcc) and the Python calls into it, ``_calls.so`` (g++,
+"""Build the sm_100a shared library ``libunipin.so`` (nvcc) and the Python calls into it (calls_module(), g++,
 against the installed torch), in-tree."""
 
 from __future__ import annotations
 
 import glob
 import os
+import re
 import subprocess
 import sys
 
@@ -13,7 +14,6 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libunipin.so")
-CALLS = os.path.join(PKG, "_calls.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -33,6 +33,18 @@ def _deps():
         + [os.path.join(INCLUDE, "unipin.h")]
 
 
+def calls_module() -> str:
+    """Name of the compiled module of the paged and windowed calls.  It is built against one torch, whose version
+    is part of the name (and Python's ABI of the file's): under another one it is a module yet to be built."""
+    import torch
+    return "_calls_torch_" + re.sub(r"\W", "_", torch.__version__)
+
+
+def calls_path() -> str:
+    import sysconfig
+    return os.path.join(PKG, calls_module() + sysconfig.get_config_var("EXT_SUFFIX"))
+
+
 def _calls_deps():
     return [os.path.join(CSRC, "calls.cpp"), os.path.join(INCLUDE, "unipin.h")]
 
@@ -45,7 +57,7 @@ def _newer(target, deps) -> bool:
 
 
 def up_to_date() -> bool:
-    return _newer(LIB, _deps()) and _newer(CALLS, _calls_deps())
+    return _newer(LIB, _deps()) and _newer(calls_path(), _calls_deps())
 
 
 def _build_calls(verbose: bool):
@@ -54,9 +66,10 @@ def _build_calls(verbose: bool):
     import torch
     root = os.path.join(os.path.dirname(torch.__file__))
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
-    tmp = CALLS + ".tmp.%d" % os.getpid()
+    target = calls_path()
+    tmp = target + ".tmp.%d" % os.getpid()
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
-           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI)]
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI), "-DCALLS_MODULE=" + calls_module()]
     for d in (os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
               sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE):
         cmd += ["-I", d]
@@ -65,12 +78,12 @@ def _build_calls(verbose: bool):
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.run(cmd, check=True)
-    os.replace(tmp, CALLS)
+    os.replace(tmp, target)
 
 
 def build(force: bool = False, verbose: bool = False, extra=None) -> str:
     """Compile every .cu under csrc/ into libunipin.so (static cudart, no libcuda link) and calls.cpp into
-    _calls.so."""
+    the module calls_module()."""
     if not force and up_to_date():
         return LIB
     if force or not _newer(LIB, _deps()):
@@ -81,7 +94,7 @@ def build(force: bool = False, verbose: bool = False, extra=None) -> str:
             print(" ".join(cmd), file=sys.stderr)
         subprocess.run(cmd, check=True)
         os.replace(tmp, LIB)
-    if force or not _newer(CALLS, _calls_deps()):
+    if force or not _newer(calls_path(), _calls_deps()):
         _build_calls(verbose)
     return LIB
 

@@ -472,8 +472,14 @@ PyMethodDef methods[] = {
     {nullptr, nullptr, 0, nullptr},
 };
 
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+#define CALLS_TEXT_(x) #x
+#define CALLS_TEXT(x) CALLS_TEXT_(x)
+#define CALLS_JOIN_(a, b) a##b
+#define CALLS_JOIN(a, b) CALLS_JOIN_(a, b)
+
+PyModuleDef module = {PyModuleDef_HEAD_INIT, CALLS_TEXT(CALLS_MODULE), nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__calls() { return PyModule_Create(&module); }
+// CALLS_MODULE: the module's name, which the build forms from torch's version
+PyMODINIT_FUNC CALLS_JOIN(PyInit_, CALLS_MODULE)() { return PyModule_Create(&module); }
