@@ -386,7 +386,8 @@ int unipin_paged_pool_write(const unipin_kvpool* pool, int layer, const void* k,
  * A bfloat16 pool, or an E4M3 pool with any scales (its codes are read in place;
  * powers of two are faster).  Scores, softmax statistics and sums are fp32; the
  * softmax weights are rounded to bfloat16 (float16 over an E4M3 pool with
- * power-of-two scales) for the product with V.
+ * power-of-two scales: weights below 2^-28 of the row's largest to a step of 2^-38
+ * of it) for the product with V.
  */
 int unipin_paged_decode_attn(const void* q, const void* k_self, const void* v_self, void* out, int out_fp32,
                              const int* page_table, int max_pages, const int* lens, int R, int H, int D, int max_len,

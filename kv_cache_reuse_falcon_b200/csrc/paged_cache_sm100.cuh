@@ -120,9 +120,10 @@ __global__ void __launch_bounds__(kPgWriteThreads) paged_write_kernel(const PgWr
 // place with one barrier per step, and slices, heads and requests give the blocks that fill the memory.
 // Bound: memory (the weights once, the kept rows read and written once) where there are many requests;
 // else the chain of the four selection passes.  Measured (B200), both kernels: 32 requests of 1500 .. 8192
-// rows to 2048, H = 8, D = 128 (515 MB) 107 us, of which the selection takes a quarter (4.8 TB/s in all); one
-// of 1000 rows to 500, D = 64, 10.6 us.  With the kept rows' numbers loaded in their own step and not the one
-// before, 122 and 12.4 us.
+// rows to 2048, H = 8, D = 128 (514 MB), none of them evicted before, 118 us (4.4 TB/s in all; the selection
+// alone 30, issue slots 63% busy, the move 86, DRAM 64%); one of 1000 rows to 500, D = 64, 10.3 us.  With the
+// kept rows' numbers loaded in their own step and not the one before, 122 and 12.4 us where a graph that
+// repeats the call took 107 and 10.6.
 
 struct PgEvictParams {
     uint8_t* pool_k;       // the layer's planes [S, H, ps, D]

@@ -41,12 +41,18 @@
 // under a tenth of the tensor cores' rate at the full memory rate, and a TMEM
 // accumulator would put a chain of barriers (load, S, softmax, P, P.V) into
 // every tile.
-// Measured (B200, with the join): 32 requests of 1024 .. 2048 rows, H = 8, D = 64, bf16 21.8 us (102 MB:
-// 4.7 TB/s, 71% of the rate of a copy); 256 of 32 .. 4096 under a window of 1024, D = 128, E4M3 97.6 us
-// (477 MB: 4.9 TB/s, 75%); 8 of 777 .. 32768, H = 8 over 2, D = 128, with key_weights 38 us (150 MB); one of
-// 500 rows 8.3 us.  What is left is instruction issue (at 12 warps per SM a wait for an issue slot, a product
-// or a row stands behind most stalls) and the first and last units of a block; the smallest calls are one
-// chain: lengths, page, rows, S, P, O, join of the warps.
+// Measured (B200, with the join), call by call over rows that are not in L2: 32 requests of 1024 .. 2048 rows,
+// H = 8, D = 64, bf16 28.4 us (102 MB: 3.6 TB/s, 55% of the rate of a copy; repeated over the same rows, which
+// the L2 holds in good part, 21.6); 256 of 32 .. 4096 under a window of 1024, D = 128, E4M3 100 us (477 MB: 4.8
+// TB/s, 73%); 8 of 777 .. 32768, H = 8 over 2, D = 128, with key_weights 40.4 us (150 MB: 3.7 TB/s); one of 500
+// rows 10.2 us, 8.2 in a graph.  Repeated in a graph, 32 requests of 1024 .. 2048, H = 8: bf16 D = 32, 64, 128
+// 15.4, 21.6 and 41.3 us; E4M3 14.4, 18.0 and 25.7; E4M3 with other scales 16.4, 22.0 and 34.4 (and 136 for
+// the window's 99); bf16 D = 64 with 8 and 16 heads over one 12.2 and 14.1.
+// What is left is latency: at 12 warps per SM no warp can issue in two of three cycles over bf16 and in half of
+// them over E4M3 (issue slots busy 32% and 49%), for the rows' way into the ring (one stage of two in flight
+// while the other is used), the chain of a tile and the barriers at a row's end; DRAM is at 55 and 63%.  The
+// join is a launch of 7 to 10 us, in part beside the main kernel.  The smallest calls are one chain: lengths,
+// page, rows, S, P, O, join of the warps.
 // Scores, row maxima, row sums and O are float32.  P is rounded to the type of
 // V's fragment (bfloat16; float16 over E4M3 codes with power-of-two scales), as
 // in the prefill: one rounding of relative size <= 2^-8 (2^-11, see PgWeights) per
@@ -56,8 +62,9 @@
 // scales are powers of two that is value(c) * scale exactly, so the codes go to
 // the tensor cores as float16 (exact), the scales are applied to the scores and
 // to O, and q goes to float16 after a power-of-two scaling of its row that puts
-// the row's largest element into [2^9, 2^10): bfloat16 has 8 significant bits,
-// float16 11, so only elements below 2^-33 of the row's largest can lose bits.
+// the row's largest element into [2^9, 2^10): bfloat16 has 8 significant bits
+// and float16's smallest step is 2^-24, so only elements below 2^-26 of the row's
+// largest lose bits, and none more than 2^-34 of it.
 // Other scales take the float32 product and its rounding to bfloat16 per element.
 #pragma once
 

@@ -47,8 +47,9 @@
 // the least exact of the results (relative error 2.5e-3 in place of 1.8e-3, where the gradients' own rounding
 // to bfloat16 is 1.7e-3).  Scores, P, dS and all sums are float32.
 // Bound: the chain of a tile (0.8 us of softmax, 0.7 us of products alone on an SM; a third of the softmax is
-// the exponentials' rate) at one or two blocks per SM; the first loads and the epilogue of a block are 5 of
-// its 12 us.  Measured (B200), with the forward: 64 segments of 256 + 128 rows, H = 8, D = 64, window 128,
+// the exponentials' rate) at one or two blocks per SM: the tensor pipe is busy 18% of the time at D = 64 and 35%
+// at D = 128, the issue slots 35% and 30%.  The first loads and the epilogue of a block are 5 of its 12 us.
+// Measured (B200), with the forward: 64 segments of 256 + 128 rows, H = 8, D = 64, window 128,
 // 184 us (forward 45, this kernel 124, the prep kernel's exposed part; 304 MB); 8 segments of 700 .. 1500,
 // H = 8 over 2, D = 128, window 300, 164 us; one of 186 + 125, H = 8 over 1, D = 128, window 80, 42 us.  A
 // persistent block that took its items from a ring of its own took 145 us for this kernel in the first case;

@@ -19,13 +19,15 @@
 // so the next tile's S is computed while the softmax works; at D <= 64 one, and
 // the other blocks' products run meanwhile.
 // Warps: 0-3 softmax and epilogue, 4 TMA producer, 5 MMA issuer (owns TMEM).
-// Bound, at D = 128: the products themselves.  An M = 128, N = 64 product from shared memory takes about 50
-// cycles where its rate is 32 (its A is read again for few columns), P V's N = 128 about 65: 650 of the 700
-// cycles that an SM takes per tile.  (Wider key tiles would need TMEM that the second block has.)  Measured
-// (B200): 16 segments of 500 .. 2048 past rows and 50 .. 256 candidates, H = 8, D = 128, window 512, 99 us
-// (40.4 GFLOP of allowed pairs: 408 TFLOP/s, 25% of the rate of a large product; 191 MB); 2 segments of 300,
-// D = 64, 10.3 us.  The masked prefill's engine with a window took 162 us for the first; two threads per row
-// at D = 128 105 us; MMAs issued behind `lane == 0` and not elect.sync 110 us.
+// Bound: the chain of a tile (S, its load from TMEM, softmax, P's store, P V) with two blocks per SM to fill
+// each other's gaps.  At D = 128, 16 segments of 500 .. 2048 past rows and 50 .. 256 candidates, H = 8, window
+// 512, are 89 key tiles per SM and 2200 cycles each.  The products take about 660 of these (an M = 128, N = 64
+// product from shared memory 50 cycles, where its rate is 32, P V's N = 128 65); the tensor pipe is busy 27% of
+// the time, the issue slots 31%, the MUFU 23%, DRAM 22%.  Measured (B200): that case 99 us in a graph (40.4
+// GFLOP of allowed pairs: 408 TFLOP/s, 25% of the rate of a large product; 191 MB); 2 segments of 300, D = 64,
+// 10.3 us.  Two threads per row at D = 128 took 105 us, MMAs issued behind `lane == 0` and not elect.sync 110.
+// The masked prefill's engine with a window took 162 us, but with its MMAs issued behind `lane == 0`; behind
+// elect.sync it has not been measured.
 // What a row does not see reaches nothing of it: masked scores are replaced, and
 // rows of V that are no past key of the segment are zeroed in shared memory.  A
 // value that is NaN or infinite can still reach a row of its tile that the mask
@@ -406,8 +408,8 @@ __global__ void __launch_bounds__(WfCfg<D>::kThreads, WfCfg<D>::kBlocksPerSm)
                 m = m_new;
             }
             const float m_use = m == -INFINITY ? 0.f : m;
-            // 2^x by the MUFU alone: with the FMA-pipe polynomial for one pair in four, as in the masked
-            // prefill, the issue slots and not the MUFU were the limit here
+            // 2^x by the MUFU alone: the FMA-pipe polynomial for one pair in four, as in the masked prefill, was
+            // slower here, where the MUFU is busy 23% of the time and the polynomial lengthens a tile's chain
             const uint64_t sc2 = f2_pack(sl2, sl2), nm2 = f2_pack(-m_use, -m_use);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
