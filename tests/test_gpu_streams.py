@@ -138,3 +138,33 @@ def test_a_foreign_stream_object_is_taken_by_its_handle(ub):
             got = call(Handle(stream))
         torch.cuda.synchronize()
         assert seen == [stream.cuda_stream] * count and torch.equal(got[0], want[0])
+
+
+@pytest.mark.parametrize("calls,name", [(paged_calls, "decode"), (paged_calls, "prefill_bwd"), (slot_calls, "prefill"),
+                                        (slot_calls, "prefill_bwd")])
+def test_calls_on_a_forked_stream_are_captured(ub, calls, name):
+    """A stream forked from the capturing one: the call's memory is the graph's, and its replays give the eager bits
+    while an eager call's results live."""
+    call, _ = calls(ub)[name]
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    first = call(stream)
+    torch.cuda.synchronize()
+    want = [t.clone() for t in first]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        stream.wait_stream(torch.cuda.current_stream())
+        got = call(stream)
+        torch.cuda.current_stream().wait_stream(stream)
+    for _ in range(2):
+        for t in got:
+            t.zero_()
+        other = call(None)
+        graph.replay()
+        torch.cuda.synchronize()
+        if calls is slot_calls and name == "prefill_bwd":      # float32 sums of a few tiles in any order
+            tol = [w.abs().max() * 2.0 ** -18 for w in want]
+        else:
+            tol = [0.0] * len(want)
+        for a, b, c, t in zip(got, want, other, tol):
+            assert (a - b).abs().max() <= t and (c - b).abs().max() <= t
